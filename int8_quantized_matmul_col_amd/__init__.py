@@ -16,6 +16,13 @@ Python binding over it, with torch used only for device memory and streams.
 for it.  ``outlier_stats`` summarizes the column maxima of an activation
 (``int8_column_absmax``) and |O| at candidate thresholds
 (``int8_outlier_counts``) to help choose the threshold.
+
+Beside the matmul stand the other operators of a decode step (``serving``,
+``include/int8mm_serving.h``): ``int4_linear`` (few rows times 4-bit weights
+with group scales; ``Int4Linear`` is its module), and a paged key-value cache
+(``PagedKVCache``) with ``kv_append``, ``kv_gather``, ``kv_attention`` and the
+upkeep of its pages, ``kv_pages_reserve``, ``_copy``, ``_fork``, ``_free`` and
+``_compact``.
 """
 
 from .binding import (  # noqa: F401
@@ -42,5 +49,28 @@ from .binding import (  # noqa: F401
     load,
     workspace_for,
 )
+from .kv_cache import PagedKVCache  # noqa: F401
 from .linear import Int8Linear, replace_linear_with_int8  # noqa: F401
+from .linear4 import Int4Linear  # noqa: F401
 from .stats import outlier_stats, suggest_threshold  # noqa: F401
+from .serving import (  # noqa: F401
+    INT8MM_KV_BAD_ROW,
+    INT8MM_KV_DONE,
+    INT8MM_KV_NO_PAGES,
+    Int4Weight,
+    PagedKV,
+    int4_linear,
+    int4_linear_workspace_size,
+    int4_pack_weight,
+    int4_prepare_weight,
+    int4_unpack_weight,
+    kv_append,
+    kv_attention,
+    kv_attention_workspace_size,
+    kv_gather,
+    kv_pages_compact,
+    kv_pages_copy,
+    kv_pages_fork,
+    kv_pages_free,
+    kv_pages_reserve,
+)

@@ -30,8 +30,10 @@ LIB_PATH = os.path.join(HERE, "libint8mm.so")
 PROBE_LIB_PATH = os.path.join(HERE, "libint8mm_ceilings.so")
 PROBE_SOURCES = ["ceilings.hip"]
 
-SOURCES = ["api.hip", "prepare.hip", "activation.hip", "gemm_prefill.hip", "gemm_decode.hip"]
-HEADERS = ["device_common.h", "launch.h"]
+SOURCES = ["api.hip", "prepare.hip", "activation.hip", "gemm_prefill.hip", "gemm_decode.hip",
+           "serving_api.hip", "int4_linear.hip", "kv_attention.hip", "kv_rows.hip",
+           "kv_pages.hip"]
+HEADERS = ["device_common.h", "launch.h", "serving_launch.h"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

@@ -10,19 +10,26 @@
 
 #include "int8mm.h"
 #include "launch.h"
+#include "serving_launch.h"
 #include "tile_layout.h"
 
 static_assert(INT8MM_MAX_COUNT_THRESHOLDS == i8mm::kMaxCountThresholds,
               "threshold count limit of the header and the kernel");
 
 namespace {
-
 thread_local char g_hip_error[256] = "";
+}
 
-int hip_fail(hipError_t e) {
+namespace i8mm {
+int record_hip_error(hipError_t e) {
   snprintf(g_hip_error, sizeof(g_hip_error), "%s: %s", hipGetErrorName(e), hipGetErrorString(e));
   return INT8MM_EHIP;
 }
+}  // namespace i8mm
+
+namespace {
+
+int hip_fail(hipError_t e) { return i8mm::record_hip_error(e); }
 
 constexpr size_t kAlign = 256;
 

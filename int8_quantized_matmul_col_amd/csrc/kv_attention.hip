@@ -1,0 +1,517 @@
+// The attention of one new token per sequence over a paged key-value cache.
+//
+//   out[h] = sum_t softmax_t(scale * q[h] . k[t]) v[t],  lse[h] = log sum_t exp(...)
+//
+// What bounds it: every key and value is read once from HBM; 4 flops per
+// element and query head, which the matrix cores have in plenty for up to 16
+// query heads on one kv head.
+//
+// One wave takes a chunk of 32 tokens (64 of an int8 cache) of one kv head at
+// a time.  Scores are K x Q^T tiles: the 16 rows are tokens, the 16 columns
+// the query heads of the kv head, so a lane ends up with 4 tokens' scores of
+// one head.  Which token a tile's row stands for is free: row 4a+i of tile t
+// is token 8a+4t+i (16a+4t+i for int8), and then the probabilities that a
+// lane holds are exactly the 8 (16) consecutive tokens that it has to feed to
+// V^T x P^T, whose other operand is one 16-byte load from the [dim][token]
+// value page.  Nothing moves between lanes except the running maximum, and
+// that only when a score exceeds it by 2^8 or more: a factor common to sum
+// and output cancels, so the maximum need not be exact.
+//
+// Precision: scores, maxima, sums and outputs are fp32.  A probability goes
+// to the matrix cores as two numbers of the operand type, its rounding and
+// the rest (16 or more bits together): the cores are far from bound, and the
+// result then differs from fp32 by its final rounding only.  int8 codes are
+// exact operands; the key's scale multiplies the fp32 score, the value's the
+// fp32 probability.
+//
+// A long axis is split over workgroups, a workgroup's range over its 4
+// waves; waves join in LDS, workgroups in a second kernel, each in a fixed
+// order.
+#include "device_common.h"
+#include "serving_launch.h"
+
+namespace i8mm {
+
+namespace {
+
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+constexpr int kMinTokens = 256;  // tokens per piece at least
+constexpr int kSplitAlign = 64;  // tokens; a multiple of both chunk sizes
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kSlack = 8.0f;  // how far (log2) a score may exceed the running maximum
+
+enum { kF16 = 0, kBF16 = 1, kI8 = 2 };
+
+template <bool BF16>
+__device__ __forceinline__ v4f mfma32(const v4u& a, const v4u& b, const v4f& c) {
+  if constexpr (BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a),
+                                                   __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// Two probabilities as a pair of the operand type from below and the pair of
+// what is left.  Both parts of a positive number are positive, so that an
+// infinite value stays one (its product with a remainder of 0, or with one of
+// the other sign, would be NaN).  float16's lower part comes off 2^-12 lower,
+// for a remainder of 2^-12 or more that float16 can hold.
+template <bool BF16>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  constexpr uint32_t kBelow = BF16 ? 1u : 4096u;
+  const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), kBelow);
+  const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), kBelow);
+  if constexpr (BF16) {
+    hi = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+    const v2f l = {a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u)};
+    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(l, v2b));
+  } else {
+    const v2h h = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(ua), __uint_as_float(ub)));
+    hi = __builtin_bit_cast(uint32_t, h);
+    lo = f2h2(a - (float)h[0], b - (float)h[1]);
+  }
+}
+
+// 4 int8 codes -> two dwords of exact bfloat16 / float16 numbers.
+__device__ __forceinline__ void codes_bf16(uint32_t u, uint32_t& a, uint32_t& b) {
+  const float f0 = (float)(int8_t)u, f1 = (float)(int8_t)(u >> 8);
+  const float f2 = (float)(int8_t)(u >> 16), f3 = (float)(int8_t)(u >> 24);
+  a = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
+  b = __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
+}
+__device__ __forceinline__ void codes_f16(uint32_t u, uint32_t& a, uint32_t& b) {
+  const uint32_t x = u ^ 0x80808080u;  // code + 128; 0x6400 | that = 1152 + code
+  const v2h c = {(_Float16)1152.0f, (_Float16)1152.0f};
+  a = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, x, 0x04010400u)) - c);
+  b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, x, 0x04030402u)) - c);
+}
+template <bool BF16>
+__device__ __forceinline__ v4u codes8(uint32_t u0, uint32_t u1) {
+  uint32_t a, b, c, d;
+  if constexpr (BF16) {
+    codes_bf16(u0, a, b);
+    codes_bf16(u1, c, d);
+  } else {
+    codes_f16(u0, a, b);
+    codes_f16(u1, c, d);
+  }
+  return v4u{a, b, c, d};
+}
+
+// x of lane N of this lane's row of 16 lanes.
+template <int N>
+__device__ __forceinline__ float row_lane(float x) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x150 + N, 0xf, 0xf, true));
+}
+
+// Scores (probabilities) times their tokens' factors: lane N of a row of 16
+// lanes holds the factor of the row's token N.
+template <int N, int NT>
+__device__ __forceinline__ void scale_tokens(v4f (&s)[NT], float x) {
+  s[N / 4][N % 4] *= row_lane<N>(x);
+  if constexpr (N + 1 < 4 * NT) scale_tokens<N + 1>(s, x);
+}
+
+struct Range {
+  int row, lo, len;  // visible tokens [lo, len)
+};
+__device__ __forceinline__ Range visible(const KvAttentionArgs& a, int b, int num_pages, int ps) {
+  Range v{0, 0, 0};
+  v.row = a.rows != nullptr ? a.rows[b] : b;
+  if ((unsigned)v.row >= (unsigned)a.table_rows || num_pages == 0) return v;
+  int64_t top = (int64_t)a.table_width * ps;
+  if (top > a.max_len) top = a.max_len;
+  const int n = a.lengths[v.row];
+  v.len = n < 0 ? 0 : n > top ? (int)top : n;
+  v.lo = a.window > 0 && a.window < v.len ? v.len - (int)a.window : 0;
+  return v;
+}
+
+struct Pages {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* ks;
+  const float* vs;
+  int64_t k_page, v_page;    // bytes
+  int64_t ks_page, vs_page;  // floats
+  int num_pages, kv_heads, ps, lps, D;
+};
+
+// CT: the cache's type; QBF: bfloat16 queries and results; NK: 32-dim steps
+// (EXACT: head_dim is NK * 32, otherwise at most that).
+template <int CT, bool QBF, int NK, bool EXACT>
+__global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a, Pages pg) {
+  constexpr bool I8 = CT == kI8;
+  constexpr bool PBF = CT != kF16;      // type of the P x V operands
+  constexpr int CH = I8 ? 64 : 32;      // tokens per chunk
+  constexpr int SUB = CH / 4;           // consecutive tokens a lane feeds to P x V
+  constexpr int NT = CH / 16;           // score tiles
+  constexpr int NKL = I8 ? NK / 2 : NK;  // 16-byte key loads per token row and lane
+  constexpr int DT = NK * 2;            // output tiles of 16 dims
+  constexpr int EB = I8 ? 1 : 2;
+  // float16 probabilities are held times 2^6: at most 2^14, and numbers down
+  // to 2^-30 of the maximum keep full precision
+  constexpr float kBias = CT == kF16 ? 6.0f : 0.0f;
+  const int D = EXACT ? NK * 32 : pg.D;
+
+  __shared__ float so[kWaves * DT * 256];  // outputs, [wave][tile][4][lane]
+  __shared__ float sm[kWaves * 16], sl[kWaves * 16];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, qd = lane >> 4;
+  const int group = a.q_heads / pg.kv_heads;
+  const int tiles_h = (group + kKvHeadTile - 1) / kKvHeadTile;
+  int id = blockIdx.x;
+  const int sp = id % a.split.splits;
+  id /= a.split.splits;
+  const int ht = id % tiles_h;
+  id /= tiles_h;
+  const int kvh = id % pg.kv_heads;
+  const int b = id / pg.kv_heads;
+  const int heads = min(group - ht * kKvHeadTile, kKvHeadTile);  // query heads of this tile
+  const int head0 = kvh * group + ht * kKvHeadTile;
+
+  const Range vis = visible(a, b, pg.num_pages, pg.ps);
+  const int s0 = (vis.lo & ~(kSplitAlign - 1)) + sp * a.split.tokens;
+  const int s1 = min(vis.len, s0 + a.split.tokens);
+  if (s0 >= s1 && a.split.splits > 1) return;  // the join knows
+
+  const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+  const int per = (chunks + kWaves - 1) / kWaves;
+  const int c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
+
+  v4f o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) o[i] = v4f{0, 0, 0, 0};
+  float m = -INFINITY, l = 0.0f;
+
+  if (c0 < c1) {
+    // Q^T operand: head r, dims as the key loads order them
+    v4u q[NK];
+    {
+      const uint16_t* qp = a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + min(r, heads - 1)) * a.q_head_stride;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        const int d = I8 ? (j / 2) * 64 + qd * 16 + (j & 1) * 8 : j * 32 + qd * 8;
+        q[j] = v4u{0, 0, 0, 0};
+        if (d < D) q[j] = *reinterpret_cast<const v4u*>(qp + d);
+      }
+    }
+    const int32_t* trow = a.table + (int64_t)vis.row * a.table_width;
+    int pbase = (s0 + c0 * CH) >> pg.lps;
+    int tab = pbase + lane < a.table_width ? trow[pbase + lane] : -1;
+
+    v4u kr[NT][NKL], vr[DT];
+    float ksc = 0.0f, vsc = 0.0f;
+    bool kvalid = false, vvalid = false;  // of the chunk last addressed: this lane's page exists
+    const uint8_t* vptr = nullptr;
+
+    // pages of chunk c; loads its keys (and scales)
+    auto load_k = [&](int c) __attribute__((always_inline)) {
+      const int t0 = s0 + c * CH;
+      if (((t0 + CH - 1) >> pg.lps) >= pbase + 64) {
+        pbase = t0 >> pg.lps;
+        tab = pbase + lane < a.table_width ? trow[pbase + lane] : -1;
+      }
+      const int kt = t0 + SUB * (r >> 2) + (r & 3);
+      const int vt = t0 + SUB * qd;
+      int pk = __shfl(tab, (kt >> pg.lps) - pbase);
+      int pv = __shfl(tab, (vt >> pg.lps) - pbase);
+      vvalid = (unsigned)pv < (unsigned)pg.num_pages;
+      kvalid = (unsigned)pk < (unsigned)pg.num_pages;
+      pk = kvalid ? pk : 0;
+      pv = vvalid ? pv : 0;
+      const int kslot = kt & (pg.ps - 1), vslot = vt & (pg.ps - 1);
+      const uint8_t* kp = pg.k + pk * pg.k_page + ((int64_t)kvh * pg.ps + kslot) * (D * EB) + qd * 16;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NKL; ++j) {
+          const int at = j * 64 + qd * 16;  // byte in the row
+          if (EXACT || at < D * EB)
+            kr[t][j] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(kp + t * 4 * D * EB + j * 64));
+          else
+            kr[t][j] = v4u{0, 0, 0, 0};
+        }
+      vptr = pg.v + pv * pg.v_page + ((int64_t)kvh * D * pg.ps + vslot) * EB;
+      if constexpr (I8) {
+        ksc = pg.ks[pv * pg.ks_page + kvh * pg.ps + vslot + r];
+        vsc = pg.vs[pv * pg.vs_page + kvh * pg.ps + vslot + r];
+      }
+    };
+    auto load_v = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        int d = i * 16 + r;
+        if (!EXACT) d = min(d, D - 1);  // rows past head_dim are not stored
+        vr[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(vptr + (int64_t)d * pg.ps * EB));
+      }
+    };
+
+    const float scale2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+    load_k(c0);
+    load_v();
+    for (int c = c0; c < c1; ++c) {
+      const int t0 = s0 + c * CH;
+      const bool page_ok = vvalid;
+      const bool whole = t0 >= vis.lo && t0 + CH <= s1 && __all(page_ok);
+
+      // scores
+      v4f s[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        s[t] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NKL; ++j) {
+          if constexpr (I8) {
+            s[t] = mfma32<QBF>(codes8<QBF>(kr[t][j][0], kr[t][j][1]), q[2 * j], s[t]);
+            s[t] = mfma32<QBF>(codes8<QBF>(kr[t][j][2], kr[t][j][3]), q[2 * j + 1], s[t]);
+          } else {
+            s[t] = mfma32<QBF>(kr[t][j], q[j], s[t]);
+          }
+        }
+      }
+      float ks16 = 0.0f, vs16 = 0.0f;
+      if constexpr (I8) {
+        ks16 = ksc * (1.0f / 127.0f);
+        vs16 = vsc * (1.0f / 127.0f);
+      }
+      if (c + 1 < c1) load_k(c + 1);
+
+      if constexpr (I8) {
+        scale_tokens<0>(s, ks16);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = s[t][i] * scale2;
+          if (a.softcap > 0.0f) x = a.softcap * kLog2e * tanhf(x);
+          if (!whole) {
+            const int tok = t0 + SUB * qd + 4 * t + i;
+            x = page_ok && tok >= vis.lo && tok < s1 ? x : -INFINITY;
+          }
+          s[t][i] = x;
+        }
+
+      // running maximum, per head (lane r), equal in the four lanes qd
+      float top = s[0][0];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
+      if (__any(top > m + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float f = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[i] *= f;
+      }
+      const float base = m == -INFINITY ? 0.0f : m - kBias;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[t][i] = __builtin_amdgcn_exp2f(s[t][i] - base);
+          l += s[t][i];
+        }
+      if constexpr (I8) {
+        const float vs_ok = page_ok ? vs16 : 0.0f;
+        const int tok = t0 + SUB * qd + r;  // whose scale this lane holds
+        const float vs = whole || (tok >= vis.lo && tok < s1) ? vs_ok : 0.0f;
+        scale_tokens<0>(s, vs);
+      } else if (!whole) {
+        // values of tokens that are not visible may be anything: 0, not 0 * NaN
+        v4u keep;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = t0 + SUB * qd + 2 * e;
+          const uint32_t a0 = page_ok && tok >= vis.lo && tok < s1 ? 0x0000ffffu : 0u;
+          const uint32_t a1 = page_ok && tok + 1 >= vis.lo && tok + 1 < s1 ? 0xffff0000u : 0u;
+          keep[e] = a0 | a1;
+        }
+#pragma unroll
+        for (int i = 0; i < DT; ++i) vr[i] &= keep;
+      }
+
+      // P^T operand, in two parts
+      v4u ph[NT / 2], pl[NT / 2];
+#pragma unroll
+      for (int u = 0; u < NT / 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t hi, lo;
+          split2<PBF>(s[2 * u + e / 2][2 * (e & 1)], s[2 * u + e / 2][2 * (e & 1) + 1], hi, lo);
+          ph[u][e] = hi;
+          pl[u][e] = lo;
+        }
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        if constexpr (I8) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const v4u x = codes8<true>(vr[i][2 * u], vr[i][2 * u + 1]);
+            o[i] = mfma32<true>(x, ph[u], o[i]);
+            o[i] = mfma32<true>(x, pl[u], o[i]);
+          }
+        } else {
+          o[i] = mfma32<PBF>(vr[i], ph[0], o[i]);
+          o[i] = mfma32<PBF>(vr[i], pl[0], o[i]);
+        }
+      }
+      if (c + 1 < c1) load_v();
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+  }
+
+  // join the waves
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) so[((wave * DT + i) * 4 + e) * 64 + lane] = o[i][e];
+  if (qd == 0) {
+    sm[wave * 16 + r] = m;
+    sl[wave * 16 + r] = l;
+  }
+  __syncthreads();
+  for (int at = threadIdx.x; at < heads * D; at += blockDim.x) {
+    const int h = at / D, d = at % D;
+    float mx = sm[h];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, sm[w * 16 + h]);
+    float sum = 0.0f, den = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = sm[w * 16 + h];
+      // a wave without a visible token has l = 0 and o = 0
+      const float f = mw == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mw - mx);
+      den += f * sl[w * 16 + h];
+      sum += f * so[((w * DT + (d >> 4)) * 4 + (d & 3)) * 64 + ((d & 15) >> 2) * 16 + h];
+    }
+    const int64_t bh = (int64_t)b * a.q_heads + head0 + h;
+    if (a.split.splits == 1) {
+      const float y = den == 0.0f ? 0.0f : sum * (1.0f / den);
+      a.out[bh * D + d] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
+      if (d == 0 && a.lse != nullptr)
+        a.lse[bh] = den == 0.0f ? -INFINITY : (mx - kBias + __builtin_log2f(den)) * kLn2;
+    } else {
+      const int64_t part = bh * a.split.splits + sp;
+      a.part_o[part * D + d] = sum;
+      if (d == 0) {
+        a.part_ml[2 * part] = mx - kBias;
+        a.part_ml[2 * part + 1] = den;
+      }
+    }
+  }
+}
+
+// Joins the pieces of one (sequence, query head): one block, a thread per dim.
+template <bool QBF>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttentionArgs a, int num_pages, int ps, int D) {
+  const int64_t bh = blockIdx.x;
+  const Range vis = visible(a, (int)(bh / a.q_heads), num_pages, ps);
+  const int start = vis.lo & ~(kSplitAlign - 1);
+  const int n = vis.len > vis.lo ? (vis.len - start + a.split.tokens - 1) / a.split.tokens : 0;
+  const float* ml = a.part_ml + bh * a.split.splits * 2;
+  const float* po = a.part_o + bh * a.split.splits * D;
+  float mx = -INFINITY;
+  for (int i = 0; i < n; ++i) mx = fmaxf(mx, ml[2 * i]);
+  const int d = threadIdx.x;
+  float sum = 0.0f, den = 0.0f;
+  for (int i = 0; i < n; ++i) {
+    const float f = ml[2 * i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[2 * i] - mx);
+    den += f * ml[2 * i + 1];
+    if (d < D) sum += f * po[(int64_t)i * D + d];
+  }
+  if (d < D) {
+    const float y = den == 0.0f ? 0.0f : sum * (1.0f / den);
+    a.out[bh * D + d] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
+  }
+  if (d == 0 && a.lse != nullptr)
+    a.lse[bh] = den == 0.0f ? -INFINITY : (mx + __builtin_log2f(den)) * kLn2;
+}
+
+template <int CT, bool QBF, int NK, bool EXACT>
+hipError_t run(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
+  const int group = a.q_heads / pg.kv_heads;
+  const int64_t blocks = (int64_t)a.B * pg.kv_heads * ((group + kKvHeadTile - 1) / kKvHeadTile) * a.split.splits;
+  hipLaunchKernelGGL((k_kv_attention<CT, QBF, NK, EXACT>), dim3((unsigned)blocks), dim3(64 * kWaves),
+                     0, s, a, pg);
+  return hipGetLastError();
+}
+
+template <int CT, bool QBF>
+hipError_t pick(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
+  if (pg.D == 64) return run<CT, QBF, 2, true>(a, pg, s);
+  if (pg.D == 128) return run<CT, QBF, 4, true>(a, pg, s);
+  if (pg.D < 128) return run<CT, QBF, 4, false>(a, pg, s);
+  return run<CT, QBF, 8, false>(a, pg, s);
+}
+
+}  // namespace
+
+int kv_attention_most_splits(int64_t B, int64_t head_groups, int64_t max_len) {
+  const int64_t base = B * head_groups;
+  int64_t splits = base > 0 ? (1024 + base - 1) / base : 1;
+  const int64_t most = (max_len + kMinTokens - 1) / kMinTokens;
+  if (splits > most) splits = most;
+  return (int)(splits < 1 ? 1 : splits);
+}
+
+KvSplit kv_attention_split(int64_t B, int64_t head_groups, int64_t max_len, int64_t window) {
+  // a window begins anywhere in the 64 tokens that the first piece is aligned to
+  if (window > 0 && window + kSplitAlign - 1 < max_len) max_len = window + kSplitAlign - 1;
+  const int64_t splits = kv_attention_most_splits(B, head_groups, max_len);
+  int64_t tokens = (max_len + splits - 1) / splits;
+  tokens = (tokens + kSplitAlign - 1) / kSplitAlign * kSplitAlign;
+  if (tokens < kSplitAlign) tokens = kSplitAlign;
+  const int64_t n = (max_len + tokens - 1) / tokens;
+  return KvSplit{(int)(n < 1 ? 1 : n), (int)tokens};
+}
+
+hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm_kv& kv,
+                               hipStream_t s) {
+  Pages pg;
+  const int eb = kv.dtype == INT8MM_I8 ? 1 : 2;
+  pg.k = static_cast<const uint8_t*>(kv.k);
+  pg.v = static_cast<const uint8_t*>(kv.v);
+  pg.ks = kv.k_scale;
+  pg.vs = kv.v_scale;
+  pg.k_page = kv.k_page_stride * eb;
+  pg.v_page = kv.v_page_stride * eb;
+  pg.ks_page = kv.ks_page_stride;
+  pg.vs_page = kv.vs_page_stride;
+  pg.num_pages = kv.num_pages;
+  pg.kv_heads = kv.kv_heads;
+  pg.ps = kv.page_size;
+  pg.lps = __builtin_ctz(kv.page_size);
+  pg.D = kv.head_dim;
+  hipError_t e;
+  if (kv.dtype == INT8MM_F16)
+    e = pick<kF16, false>(a, pg, s);
+  else if (kv.dtype == INT8MM_BF16)
+    e = pick<kBF16, true>(a, pg, s);
+  else
+    e = bf16 ? pick<kI8, true>(a, pg, s) : pick<kI8, false>(a, pg, s);
+  if (e != hipSuccess || a.split.splits == 1) return e;
+  const dim3 grid((unsigned)((int64_t)a.B * a.q_heads)), block((unsigned)((pg.D + 63) / 64 * 64));
+  if (bf16)
+    hipLaunchKernelGGL(k_kv_join<true>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D);
+  else
+    hipLaunchKernelGGL(k_kv_join<false>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D);
+  return hipGetLastError();
+}
+
+}  // namespace i8mm

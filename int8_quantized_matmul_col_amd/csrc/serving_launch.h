@@ -1,0 +1,100 @@
+// Host-side launchers of the serving kernels (internal; the C ABI is
+// include/int8mm_serving.h).  Arguments are validated by serving_api.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "int8mm_serving.h"
+
+namespace i8mm {
+
+// ---- 4-bit weights: tiles of 16 channels x 128 k, 1 KiB each
+constexpr int kInt4TileK = 128;
+constexpr int kInt4TileBytes = 1024;
+constexpr int kInt4PadRows = 64;  // channels padded so that a wave may take 4 tiles at once
+constexpr int kInt4RowChunk = 64;  // rows of X per pass over the weight
+
+inline int64_t int4_padded_rows(int64_t N) { return (N + kInt4PadRows - 1) / kInt4PadRows * kInt4PadRows; }
+inline int64_t int4_tiles_k(int64_t K) { return (K + kInt4TileK - 1) / kInt4TileK; }
+// 32-k steps of a tile that share one parameter entry
+inline int int4_group_steps(int64_t group) { return group >= 128 ? 4 : (int)(group / 32); }
+
+hipError_t launch_int4_pack(const uint8_t* codes, int64_t N, int64_t K, int64_t group,
+                            const uint16_t* scales, const uint8_t* zeros, uint32_t* Wq,
+                            uint16_t* params, hipStream_t s);
+hipError_t launch_int4_prepare(const uint16_t* W, bool bf16, int64_t N, int64_t K, int64_t group,
+                               bool zeros, uint32_t* Wq, uint16_t* params, hipStream_t s);
+hipError_t launch_int4_linear(const uint16_t* X, bool bf16, int64_t M, int64_t K, int64_t ldx,
+                              const void* Wq, const void* params, int64_t N, int64_t group,
+                              bool zeros, const uint16_t* bias, uint16_t* Y, uint16_t* ws,
+                              hipStream_t s);
+// Whether the kernel reads X as it is; otherwise it goes through ws (rows of K
+// rounded up to 8).
+bool int4_x_aligned(const uint16_t* X, int64_t M, int64_t K, int64_t ldx);
+
+// ---- key-value pages
+hipError_t launch_kv_append(const uint16_t* k, const uint16_t* v, bool bf16, int T, int64_t kts,
+                            int64_t khs, int64_t vts, int64_t vhs, const int8mm_kv& kv,
+                            const int32_t* table, int table_rows, int table_width,
+                            const int32_t* rows, const int32_t* positions, hipStream_t s);
+hipError_t launch_kv_gather(uint16_t* k, uint16_t* v, bool bf16, int T, const int8mm_kv& kv,
+                            const int32_t* table, int table_rows, int table_width,
+                            const int32_t* rows, const int32_t* positions, hipStream_t s);
+
+// How kv_attention splits its work: `splits` pieces of `tokens` tokens for
+// every (sequence, group of up to 16 query heads); one piece writes the
+// result itself, more are joined.
+struct KvSplit {
+  int splits;
+  int tokens;
+};
+// max_len, window: bounds of what one sequence shows.  most_splits is an upper
+// bound of `splits` over every window.
+KvSplit kv_attention_split(int64_t B, int64_t head_groups, int64_t max_len, int64_t window);
+int kv_attention_most_splits(int64_t B, int64_t head_groups, int64_t max_len);
+// Query heads of one kv head that one wave's matrix tile holds.
+constexpr int kKvHeadTile = 16;
+
+struct KvAttentionArgs {
+  const uint16_t* q;
+  int64_t q_batch_stride, q_head_stride;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* rows;
+  uint16_t* out;
+  float* lse;
+  float* part_o;   // [B][q_heads][splits][head_dim], splits > 1
+  float* part_ml;  // [B][q_heads][splits][2]
+  int B, q_heads, table_rows, table_width, max_len;
+  float scale, softcap;
+  int64_t window;
+  KvSplit split;
+};
+hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm_kv& kv,
+                               hipStream_t s);
+
+size_t kv_pages_workspace(int64_t num_pages, int64_t n);
+hipError_t launch_kv_pages_copy(const int8mm_kv& kv, const int32_t* src, const int32_t* dst, int n,
+                                hipStream_t s);
+hipError_t launch_kv_pages_reserve(int num_pages, int page_size, int32_t* table, int table_rows,
+                                   int table_width, int32_t* lengths, int32_t* refcount,
+                                   const int32_t* rows, const int32_t* new_lengths, int n,
+                                   int32_t* status, void* ws, hipStream_t s);
+hipError_t launch_kv_pages_fork(const int8mm_kv& kv, int32_t* table, int table_rows,
+                                int table_width, int32_t* lengths, int32_t* refcount,
+                                const int32_t* parents, const int32_t* children, int n,
+                                int32_t* status, void* ws, hipStream_t s);
+hipError_t launch_kv_pages_free(int num_pages, int32_t* table, int table_rows, int table_width,
+                                int32_t* lengths, int32_t* refcount, const int32_t* rows, int n,
+                                hipStream_t s);
+hipError_t launch_kv_pages_compact(const int8mm_kv& kv, const int32_t* table, int32_t* table_out,
+                                   int table_rows, int table_width, const int32_t* refcount,
+                                   int32_t* refcount_out, int32_t* n_live, void* ws,
+                                   hipStream_t s);
+
+// Records a HIP error for int8mm_last_hip_error and returns INT8MM_EHIP
+// (api.hip, shared by both ABI files).
+int record_hip_error(hipError_t e);
+
+}  // namespace i8mm
