@@ -42,10 +42,9 @@ extern "C" {
  * The prepared weight.  Codes are stored in tiles of 16 output channels x 128
  * k (1 KiB), the order in which one wave feeds them to the matrix cores with
  * one 16-byte load a lane: tile (n/16, k/128) at ((n/16)*ceil(K/128) + k/128)
- * * 1024; inside it, byte 16*l + 4*j + b holds two codes of channel l%16 of
- * the tile: bits 0-3 element {0,2,4,6}[b] and bits 4-7 element {2,..}: with
- * dword w = bytes 4j..4j+3, the 8 codes of k = 32*j + 8*(l/16) + e sit at bits
- * 4*p(e), p = {0,4,1,5,2,6,3,7}.  Padding rows and columns hold code 8.
+ * * 1024; inside it the dword at 16*l + 4*j (l = 0..63, j = 0..3) holds, for
+ * channel l%16 of the tile, the codes of k = 32*j + 8*(l/16) + e, e = 0..7, at
+ * bits 4*p(e), p = {0,4,1,5,2,6,3,7}.  Padding rows and columns hold code 8.
  * Group parameters: per tile and per sub-group of gs = min(group, 128) k, 16
  * entries (one a channel): a float16 scale, or with zero points a pair of
  * float16 (scale, z).  A group wider than 128 repeats its entry for every
@@ -167,7 +166,7 @@ INT8MM_API int kv_gather(void* k, void* v, int dtype, int64_t T, const int8mm_kv
                          const int32_t* rows, const int32_t* positions, hipStream_t stream);
 
 /* Bytes of workspace kv_attention needs for these sizes (256-byte aligned;
- * 0 for an invalid size).  max_len: see kv_attention. */
+ * 0: none, the workspace may be NULL).  max_len: see kv_attention. */
 INT8MM_API size_t kv_attention_workspace_size(int64_t B, int64_t q_heads, int64_t kv_heads,
                                               int64_t head_dim, int64_t max_len);
 

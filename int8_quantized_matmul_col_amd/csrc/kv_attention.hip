@@ -41,6 +41,9 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
+constexpr int kJoinThreads = 256;
+constexpr int kMaxSplits = 1024;
+constexpr int kPieces = 512;     // workgroups aimed at; at most kMaxSplits
 constexpr int kMinTokens = 256;  // tokens per piece at least
 constexpr int kSplitAlign = 64;  // tokens; a multiple of both chunk sizes
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -167,48 +170,53 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, qd = lane >> 4;
-  const int group = a.q_heads / pg.kv_heads;
+  const int group = a.group;
+  const int b = blockIdx.x / a.split.splits, sp = blockIdx.x % a.split.splits;
   const int tiles_h = (group + kKvHeadTile - 1) / kKvHeadTile;
-  int id = blockIdx.x;
-  const int sp = id % a.split.splits;
-  id /= a.split.splits;
-  const int ht = id % tiles_h;
-  id /= tiles_h;
-  const int kvh = id % pg.kv_heads;
-  const int b = id / pg.kv_heads;
+  const int kvh = blockIdx.y / tiles_h, ht = blockIdx.y % tiles_h;
   const int heads = min(group - ht * kKvHeadTile, kKvHeadTile);  // query heads of this tile
   const int head0 = kvh * group + ht * kKvHeadTile;
+
+  // Queries and the first table entries are requested before the length is
+  // known, so that the three do not wait for one another.
+  // Q^T operand: head r, dims as the key loads order them
+  v4u q[NK];
+  {
+    const uint16_t* qp = a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + min(r, heads - 1)) * a.q_head_stride;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      const int d = I8 ? (j / 2) * 64 + qd * 16 + (j & 1) * 8 : j * 32 + qd * 8;
+      q[j] = v4u{0, 0, 0, 0};
+      if (d < D) q[j] = *reinterpret_cast<const v4u*>(qp + d);
+    }
+  }
+  const int row = a.rows != nullptr ? a.rows[b] : b;
+  const bool row_ok = (unsigned)row < (unsigned)a.table_rows;
+  const int32_t* trow = a.table + (int64_t)(row_ok ? row : 0) * a.table_width;
+  auto entries = [&](int at) __attribute__((always_inline)) {
+    return row_ok && at + lane < a.table_width ? trow[at + lane] : -1;
+  };
+  int pbase = (sp * a.split.tokens) >> pg.lps;
+  int tab = entries(pbase);  // lane's page id: table entry pbase + lane
 
   const Range vis = visible(a, b, pg.num_pages, pg.ps);
   const int s0 = (vis.lo & ~(kSplitAlign - 1)) + sp * a.split.tokens;
   const int s1 = min(vis.len, s0 + a.split.tokens);
   if (s0 >= s1 && a.split.splits > 1) return;  // the join knows
 
-  const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
-  const int per = (chunks + kWaves - 1) / kWaves;
-  const int c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
+  if (vis.lo >= kSplitAlign) {  // the pieces begin at the window
+    pbase = s0 >> pg.lps;
+    tab = entries(pbase);
+  }
+
+  const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;  // taken by the waves in turn
 
   v4f o[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = v4f{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;
 
-  if (c0 < c1) {
-    // Q^T operand: head r, dims as the key loads order them
-    v4u q[NK];
-    {
-      const uint16_t* qp = a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + min(r, heads - 1)) * a.q_head_stride;
-#pragma unroll
-      for (int j = 0; j < NK; ++j) {
-        const int d = I8 ? (j / 2) * 64 + qd * 16 + (j & 1) * 8 : j * 32 + qd * 8;
-        q[j] = v4u{0, 0, 0, 0};
-        if (d < D) q[j] = *reinterpret_cast<const v4u*>(qp + d);
-      }
-    }
-    const int32_t* trow = a.table + (int64_t)vis.row * a.table_width;
-    int pbase = (s0 + c0 * CH) >> pg.lps;
-    int tab = pbase + lane < a.table_width ? trow[pbase + lane] : -1;
-
+  if (wave < chunks) {
     v4u kr[NT][NKL], vr[DT];
     float ksc = 0.0f, vsc = 0.0f;
     bool kvalid = false, vvalid = false;  // of the chunk last addressed: this lane's page exists
@@ -219,7 +227,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
       const int t0 = s0 + c * CH;
       if (((t0 + CH - 1) >> pg.lps) >= pbase + 64) {
         pbase = t0 >> pg.lps;
-        tab = pbase + lane < a.table_width ? trow[pbase + lane] : -1;
+        tab = entries(pbase);
       }
       const int kt = t0 + SUB * (r >> 2) + (r & 3);
       const int vt = t0 + SUB * qd;
@@ -257,9 +265,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
     };
 
     const float scale2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
-    load_k(c0);
+    load_k(wave);
     load_v();
-    for (int c = c0; c < c1; ++c) {
+    for (int c = wave; c < chunks; c += kWaves) {
       const int t0 = s0 + c * CH;
       const bool page_ok = vvalid;
       const bool whole = t0 >= vis.lo && t0 + CH <= s1 && __all(page_ok);
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
         ks16 = ksc * (1.0f / 127.0f);
         vs16 = vsc * (1.0f / 127.0f);
       }
-      if (c + 1 < c1) load_k(c + 1);
+      if (c + kWaves < chunks) load_k(c + kWaves);
 
       if constexpr (I8) {
         scale_tokens<0>(s, ks16);
@@ -370,7 +378,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
           o[i] = mfma32<PBF>(vr[i], pl[0], o[i]);
         }
       }
-      if (c + 1 < c1) load_v();
+      if (c + kWaves < chunks) load_v();
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -417,38 +425,69 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
   }
 }
 
-// Joins the pieces of one (sequence, query head): one block, a thread per dim.
+// Joins the pieces of one (sequence, query head).  Threads hold 4 dims each;
+// the block's groups of D/4 threads take the pieces in turn.
 template <bool QBF>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttentionArgs a, int num_pages, int ps, int D) {
+__global__ __launch_bounds__(kJoinThreads) void k_kv_join(KvAttentionArgs a, int num_pages, int ps,
+                                                          int D) {
+  __shared__ float f[kMaxSplits];
+  __shared__ float red[kJoinThreads / 64];
+  __shared__ v4f part[kJoinThreads];
   const int64_t bh = blockIdx.x;
   const Range vis = visible(a, (int)(bh / a.q_heads), num_pages, ps);
   const int start = vis.lo & ~(kSplitAlign - 1);
   const int n = vis.len > vis.lo ? (vis.len - start + a.split.tokens - 1) / a.split.tokens : 0;
   const float* ml = a.part_ml + bh * a.split.splits * 2;
   const float* po = a.part_o + bh * a.split.splits * D;
-  float mx = -INFINITY;
-  for (int i = 0; i < n; ++i) mx = fmaxf(mx, ml[2 * i]);
-  const int d = threadIdx.x;
-  float sum = 0.0f, den = 0.0f;
-  for (int i = 0; i < n; ++i) {
-    const float f = ml[2 * i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[2 * i] - mx);
-    den += f * ml[2 * i + 1];
-    if (d < D) sum += f * po[(int64_t)i * D + d];
+  auto all = [&](float x, auto op) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) x = op(x, __shfl_xor(x, o, 64));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = red[0];
+    for (int w = 1; w < kJoinThreads / 64; ++w) x = op(x, red[w]);
+    return x;
+  };
+  float mx = -INFINITY, den = 0.0f;
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+    f[i] = ml[2 * i];
+    mx = fmaxf(mx, f[i]);
   }
-  if (d < D) {
-    const float y = den == 0.0f ? 0.0f : sum * (1.0f / den);
-    a.out[bh * D + d] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
+  mx = all(mx, [](float x, float y) { return fmaxf(x, y); });
+  for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+    f[i] = f[i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(f[i] - mx);
+    den += f[i] * ml[2 * i + 1];
   }
-  if (d == 0 && a.lse != nullptr)
+  den = all(den, [](float x, float y) { return x + y; });
+
+  const int quads = D / 4, groups = kJoinThreads / quads;
+  const int g = threadIdx.x / quads, d = threadIdx.x % quads * 4;
+  v4f sum = {0, 0, 0, 0};
+  if (g < groups) {
+#pragma unroll 4
+    for (int i = g; i < n; i += groups) sum += f[i] * *reinterpret_cast<const v4f*>(po + (int64_t)i * D + d);
+  }
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  if (g == 0) {
+    for (int w = 1; w < groups; ++w) sum += part[w * quads + threadIdx.x];
+    const float inv = 1.0f / den;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float y = den == 0.0f ? 0.0f : sum[e] * inv;
+      a.out[bh * D + d + e] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
+    }
+  }
+  if (threadIdx.x == 0 && a.lse != nullptr)
     a.lse[bh] = den == 0.0f ? -INFINITY : (mx + __builtin_log2f(den)) * kLn2;
 }
 
 template <int CT, bool QBF, int NK, bool EXACT>
 hipError_t run(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
-  const int group = a.q_heads / pg.kv_heads;
-  const int64_t blocks = (int64_t)a.B * pg.kv_heads * ((group + kKvHeadTile - 1) / kKvHeadTile) * a.split.splits;
-  hipLaunchKernelGGL((k_kv_attention<CT, QBF, NK, EXACT>), dim3((unsigned)blocks), dim3(64 * kWaves),
-                     0, s, a, pg);
+  const dim3 grid((unsigned)a.B * a.split.splits,
+                  (unsigned)(pg.kv_heads * ((a.group + kKvHeadTile - 1) / kKvHeadTile)));
+  hipLaunchKernelGGL((k_kv_attention<CT, QBF, NK, EXACT>), grid, dim3(64 * kWaves), 0, s, a, pg);
   return hipGetLastError();
 }
 
@@ -464,7 +503,7 @@ hipError_t pick(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
 
 int kv_attention_most_splits(int64_t B, int64_t head_groups, int64_t max_len) {
   const int64_t base = B * head_groups;
-  int64_t splits = base > 0 ? (1024 + base - 1) / base : 1;
+  int64_t splits = base > 0 ? (kPieces + base - 1) / base : 1;
   const int64_t most = (max_len + kMinTokens - 1) / kMinTokens;
   if (splits > most) splits = most;
   return (int)(splits < 1 ? 1 : splits);
@@ -506,7 +545,7 @@ hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm
   else
     e = bf16 ? pick<kI8, true>(a, pg, s) : pick<kI8, false>(a, pg, s);
   if (e != hipSuccess || a.split.splits == 1) return e;
-  const dim3 grid((unsigned)((int64_t)a.B * a.q_heads)), block((unsigned)((pg.D + 63) / 64 * 64));
+  const dim3 grid((unsigned)((int64_t)a.B * a.q_heads)), block(kJoinThreads);
   if (bf16)
     hipLaunchKernelGGL(k_kv_join<true>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D);
   else

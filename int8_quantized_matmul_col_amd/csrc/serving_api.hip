@@ -64,9 +64,9 @@ bool row_type(int dtype, const int8mm_kv* kv) {
 }
 
 bool table_shape(int64_t rows, int64_t width, int64_t page_size) {
-  // token positions fit int32
-  return rows >= 0 && rows <= kMaxCount && width >= 0 && width * page_size < ((int64_t)1 << 31) &&
-         width <= kMaxCount;
+  // token positions, and sums of two of them, fit int32
+  return rows >= 0 && rows <= kMaxCount && width >= 0 && width <= kMaxCount &&
+         width * page_size <= kMaxCount;
 }
 
 bool workspace_ok(const void* ws, size_t have, size_t need) {
@@ -200,8 +200,7 @@ INT8MM_API size_t kv_attention_workspace_size(int64_t B, int64_t q_heads, int64_
       max_len >= ((int64_t)1 << 31))
     return 0;
   const int splits = i8mm::kv_attention_most_splits(B, head_groups(q_heads, kv_heads), max_len);
-  const size_t n = attention_sizes(B, q_heads, head_dim, splits).total;
-  return n < kAlign ? kAlign : n;
+  return attention_sizes(B, q_heads, head_dim, splits).total;
 }
 
 INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads,
@@ -230,7 +229,7 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   const int64_t groups = head_groups(q_heads, kv->kv_heads);
   i8mm::KvAttentionArgs a{};
   a.split = i8mm::kv_attention_split(B, groups, most, window);
-  if ((int64_t)B * groups * a.split.splits >= ((int64_t)1 << 31)) return INT8MM_ESHAPE;
+  if (B * a.split.splits > kMaxCount || groups > 65535) return INT8MM_ESHAPE;
   const AttentionSizes z = attention_sizes(B, q_heads, kv->head_dim, a.split.splits);
   if (!workspace_ok(workspace, workspace_bytes, z.total)) return INT8MM_EWORKSPACE;
   a.q = static_cast<const uint16_t*>(q);
@@ -245,6 +244,7 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + z.part_ml);
   a.B = (int)B;
   a.q_heads = (int)q_heads;
+  a.group = (int)(q_heads / kv->kv_heads);
   a.table_rows = (int)table_rows;
   a.table_width = (int)table_width;
   a.max_len = (int)max_len;

@@ -66,7 +66,7 @@ struct KvAttentionArgs {
   float* lse;
   float* part_o;   // [B][q_heads][splits][head_dim], splits > 1
   float* part_ml;  // [B][q_heads][splits][2]
-  int B, q_heads, table_rows, table_width, max_len;
+  int B, q_heads, group, table_rows, table_width, max_len;  // group: query heads per kv head
   float scale, softcap;
   int64_t window;
   KvSplit split;

@@ -74,6 +74,7 @@ SIGNATURES = {
 }
 
 _fns: Optional[ctypes.CDLL] = None
+_by_name: dict = {}
 
 
 def _lib() -> ctypes.CDLL:
@@ -84,6 +85,7 @@ def _lib() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+            _by_name[name] = fn
         _fns = lib
     return _fns
 
@@ -91,13 +93,14 @@ def _lib() -> ctypes.CDLL:
 def _call(name: str, device, *args) -> None:
     """One C call on torch's current stream of `device`, with `device` current
     (the library launches on the current device)."""
-    fn = getattr(_lib(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream)
+    if _fns is None:
+        _lib()
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        st = _by_name[name](*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream)
+            st = _by_name[name](*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         _check(name, st)
 
@@ -120,8 +123,12 @@ def _on(t, name: str, device=None) -> None:
 
 
 def _indexes(t, name: str, device, shape=None) -> None:
-    _require(t, torch.int32, name, device)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    """A contiguous int32 tensor of `device` (and shape)."""
+    # one look at what is nearly always right; _require names what is wrong
+    if not (type(t) is torch.Tensor and t.dtype is torch.int32 and t.is_contiguous()
+            and t.get_device() == device.index):
+        _require(t, torch.int32, name, device)
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -238,7 +245,7 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
         if bias.numel() != N:
             raise ValueError(f"bias has {bias.numel()} entries, expected {N}")
     if out is None:
-        Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+        Y = X.new_empty((M, N))
     else:
         _check_out(out, (M, N), X.dtype, "out", dev)
         Y = out
@@ -339,7 +346,7 @@ def _one_layer(kv: PagedKV) -> None:
 
 
 def _check_table(table, device) -> None:
-    _require(table, torch.int32, "table", device)
+    _indexes(table, "table", device)
     if table.dim() != 2:
         raise ValueError("table must be 2-D [rows][pages]")
 
@@ -357,7 +364,7 @@ def kv_append(k, v, kv: PagedKV, table, rows, positions) -> None:
     if v.dtype != k.dtype:
         raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
     shape = (positions.numel(), kv.kv_heads, kv.head_dim)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+    if k.shape != shape or v.shape != shape:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected {shape}")
     if k.stride(2) != 1 or v.stride(2) != 1:
         raise ValueError("the last dim of k and v must be contiguous")
@@ -384,8 +391,8 @@ def kv_gather(kv: PagedKV, table, rows, positions, dtype=None, out=None) -> Tupl
     _indexes(positions, "positions", dev, (T,))
     shape = (T, kv.kv_heads, kv.head_dim)
     if out is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
-        v = torch.empty(shape, dtype=dtype, device=dev)
+        k = kv.k.new_empty(shape, dtype=dtype)
+        v = kv.k.new_empty(shape, dtype=dtype)
     else:
         k, v = out
         _check_out(k, shape, dtype, "out[0] (k)", dev)
@@ -427,9 +434,7 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
         if q.data_ptr() % 16:
             q = q.clone()
     _check_table(table, dev)
-    _require(lengths, torch.int32, "lengths", dev)
-    if lengths.dim() != 1 or lengths.numel() != table.shape[0]:
-        raise ValueError(f"lengths has shape {tuple(lengths.shape)}, expected ({table.shape[0]},)")
+    _indexes(lengths, "lengths", dev, (table.shape[0],))
     if rows is not None:
         _indexes(rows, "rows", dev, (B,))
     elif B > table.shape[0]:
@@ -437,19 +442,21 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
     room = table.shape[1] * kv.page_size
     max_len = room if max_len is None else min(int(max_len), room)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=dev)
+        out = q.new_empty((B, Hq, D))
     else:
         _check_out(out, (B, Hq, D), q.dtype, "out", dev)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    lse = q.new_empty((B, Hq), dtype=torch.float32) if return_lse else None
     if workspace is None:
         n = _lib().kv_attention_workspace_size(B, Hq, kv.kv_heads, D, max_len)
-        workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
+        if n:
+            workspace = table.new_empty((n // 4,))
     _call("kv_attention", dev, q.data_ptr(), dt, B, Hq, q.stride(0), q.stride(1), kv._ref,
           table.data_ptr(), table.shape[0], table.shape[1], lengths.data_ptr(),
           None if rows is None else rows.data_ptr(), max_len,
           D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(),
-          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          None if lse is None else lse.data_ptr(),
+          None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
     return (out, lse) if return_lse else out
 
 
@@ -489,7 +496,7 @@ def kv_pages_reserve(table, lengths, refcount, rows, new_lengths, page_size: int
     _indexes(rows, "rows", dev)
     _indexes(new_lengths, "new_lengths", dev, rows.shape)
     n, P = rows.numel(), refcount.numel()
-    status = torch.empty(rows.shape, dtype=torch.int32, device=dev)
+    status = rows.new_empty(rows.shape)
     ws = _pages_workspace(P, n, dev, workspace)
     _call("kv_pages_reserve", dev, P, page_size, table.data_ptr(), table.shape[0], table.shape[1],
           lengths.data_ptr(), refcount.data_ptr(), rows.data_ptr(), new_lengths.data_ptr(), n,
@@ -506,7 +513,7 @@ def kv_pages_fork(kv: PagedKV, table, lengths, refcount, parents, children, work
     _indexes(parents, "parents", dev)
     _indexes(children, "children", dev, parents.shape)
     n = parents.numel()
-    status = torch.empty(parents.shape, dtype=torch.int32, device=dev)
+    status = parents.new_empty(parents.shape)
     ws = _pages_workspace(kv.num_pages, n, dev, workspace)
     _call("kv_pages_fork", dev, kv._ref, table.data_ptr(), table.shape[0], table.shape[1],
           lengths.data_ptr(), refcount.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
@@ -534,7 +541,7 @@ def kv_pages_compact(kv: PagedKV, table, refcount, out: Optional[Tuple] = None, 
     if out is not None:
         _check_out(t, table.shape, torch.int32, "out[0] (table)", dev)
         _check_out(r, refcount.shape, torch.int32, "out[1] (refcount)", dev)
-    n_live = torch.empty((1,), dtype=torch.int32, device=dev)
+    n_live = table.new_empty((1,))
     ws = _pages_workspace(kv.num_pages, 0, dev, workspace)
     _call("kv_pages_compact", dev, kv._ref, table.data_ptr(), t.data_ptr(), table.shape[0],
           table.shape[1], refcount.data_ptr(), r.data_ptr(), n_live.data_ptr(), ws.data_ptr(),
