@@ -45,10 +45,10 @@ extern "C" {
  * * 1024; inside it the dword at 16*l + 4*j (l = 0..63, j = 0..3) holds, for
  * channel l%16 of the tile, the codes of k = 32*j + 8*(l/16) + e, e = 0..7, at
  * bits 4*p(e), p = {0,4,1,5,2,6,3,7}.  Padding rows and columns hold code 8.
- * Group parameters: per tile and per sub-group of gs = min(group, 128) k, 16
- * entries (one a channel): a float16 scale, or with zero points a pair of
- * float16 (scale, z).  A group wider than 128 repeats its entry for every
- * tile it covers.
+ * Group parameters: per tile and channel one entry for each sub-group of
+ * min(group, 128) k: a float16 scale, or with zero points a pair of float16
+ * (scale, 1024 + z), laid out [n/16][k/128][n%16][sub-group].  A group wider
+ * than 128 repeats its entry for every tile it covers.
  */
 #define INT4_MAX_K (1 << 20)
 
@@ -84,8 +84,9 @@ INT8MM_API int int4_pack_weight(const uint8_t* codes, int64_t N, int64_t K, int6
 INT8MM_API int int4_prepare_weight(const void* W, int dtype, int64_t N, int64_t K, int64_t group,
                                    int zeros, void* Wq, void* params, hipStream_t stream);
 
-/* Bytes of workspace int4_linear needs (256-byte aligned); may be 0, and the
- * workspace may then be NULL. */
+/* Bytes of workspace int4_linear needs (256-byte aligned) for more than 16
+ * rows, or for rows that are not 16-byte aligned or not a multiple of 8 long;
+ * other calls may pass NULL. */
 INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N);
 
 /*

@@ -41,81 +41,112 @@ __device__ __forceinline__ v4f mfma32(const v4u& a, const v4u& b, const v4f& c) 
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// The 8 codes of one dword as an MFMA operand: float16 q - 8, bfloat16 128 + q.
+// Constants of the nibble extraction, held in registers: v_and_or_b32 takes
+// no literals, and with literals each nibble pair costs an and plus an or.
+struct Nibbles {
+  uint32_t lo, hi, one;
+};
 template <bool BF16>
-__device__ __forceinline__ v4u codes8(uint32_t u) {
+__device__ __forceinline__ Nibbles nibbles() {
+  Nibbles n;
+  asm("v_mov_b32 %0, 0x000f000f" : "=v"(n.lo));
+  asm("v_mov_b32 %0, 0x00f000f0" : "=v"(n.hi));
+  if constexpr (BF16)
+    asm("v_mov_b32 %0, 0x43004300" : "=v"(n.one));
+  else
+    asm("v_mov_b32 %0, 0x64006400" : "=v"(n.one));
+  return n;
+}
+
+// The 8 codes of one dword as an MFMA operand: float16 q - z, bfloat16
+// 128 + q.  bias (float16): 1024 + z twice.
+template <bool BF16>
+__device__ __forceinline__ v4u codes8(uint32_t u, uint32_t bias, const Nibbles& n) {
   if constexpr (BF16) {
-    constexpr uint32_t m = 0x000f000fu, o = 0x43004300u;
-    return v4u{(u & m) | o, ((u >> 4) & m) | o, ((u >> 8) & m) | o, ((u >> 12) & m) | o};
+    return v4u{(u & n.lo) | n.one, ((u >> 4) & n.lo) | n.one, ((u >> 8) & n.lo) | n.one,
+               ((u >> 12) & n.lo) | n.one};
   } else {
-    constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u, o = 0x64006400u;
     const uint32_t w = u >> 8;
-    const v2h c1 = {(_Float16)1032.0f, (_Float16)1032.0f};
-    const v2h c2 = {(_Float16)0.0625f, (_Float16)0.0625f};
-    const v2h c3 = {(_Float16)-72.0f, (_Float16)-72.0f};
-    auto plain = [&](uint32_t x) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, x) - c1); };
+    const v2h z = __builtin_bit_cast(v2h, bias);
+    const v2h sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const v2h c = {(_Float16)960.0f, (_Float16)960.0f};
+    const v2h y = c - z;  // -(64 + z)
+    auto plain = [&](uint32_t x) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, x) - z); };
     auto wide = [&](uint32_t x) {
-      return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(v2h, x), c2, c3));
+      return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(v2h, x), sixteenth, y));
     };
-    return v4u{plain((u & lo) | o), wide((u & hi) | o), plain((w & lo) | o), wide((w & hi) | o)};
+    return v4u{plain((u & n.lo) | n.one), wide((u & n.hi) | n.one), plain((w & n.lo) | n.one),
+               wide((w & n.hi) | n.one)};
   }
 }
 
-// Waves that share one group of tiles: as many as its registers allow.
-constexpr int max_waves(int P, int MT) { return P * MT == 1 ? 16 : MT <= 2 ? 8 : 4; }
+constexpr int kCus = 256;  // compute units of the MI355X
+
+// Waves that share one group of tiles: as many as the registers and 64 KiB
+// for their sums allow.
+constexpr int max_waves(int P, int MT) { return P * MT == 1 ? 16 : P * MT <= 8 ? 8 : 4; }
 
 // One workgroup: P tiles of 16 channels, up to 16*MT rows, its waves splitting
 // K tile by tile.  GS: 32-k steps per parameter entry.
-// X: rows 16-byte aligned, K a multiple of 8 (see k_int4_pad_x).
-template <bool BF16, bool ZEROS, int GS, int P, int MT>
+// ARR: X is in operand order (see k_int4_arrange); otherwise rows of X, 16-byte
+// aligned and K a multiple of 8 (one tile of rows only).
+//
+// X is the A operand and W the B operand, so that a lane's codes and its sums
+// belong to the same channel (lane % 16) and one parameter entry serves both.
+template <bool BF16, bool ZEROS, int GS, int P, int MT, bool ARR>
 __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
     const uint16_t* __restrict__ X, int M, int K, int64_t ldx, const uint8_t* __restrict__ Wq,
     const uint16_t* __restrict__ params, int N, const uint16_t* __restrict__ bias,
     uint16_t* __restrict__ Y) {
-  constexpr int NG = 4 / GS;             // parameter entries per tile and channel
-  constexpr int EB = ZEROS ? 2 : 1;      // 16-bit words per entry
-  constexpr bool CORR = BF16 || ZEROS;   // a constant comes off the sums
-  constexpr float kOff = BF16 ? (ZEROS ? 128.0f : 136.0f) : -8.0f;
+  constexpr int NG = 4 / GS;  // parameter entries per tile and channel
+  constexpr int PB = NG * (ZEROS ? 4 : 2);  // their bytes
+  using Par = typename std::conditional<PB == 16, v4u, typename std::conditional<PB == 8, v2u,
+              typename std::conditional<PB == 4, uint32_t, uint16_t>::type>::type>::type;
   extern __shared__ float red[];  // [waves][P][MT][4][64]
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, qd = lane >> 4;
   const int nt = (K + kInt4TileK - 1) / kInt4TileK;
   const int panel0 = blockIdx.x * P;
   const int m0 = blockIdx.y * (16 * MT);
   const int rows = min(M - m0, 16 * MT);
 
-  const uint16_t* xrow[MT];
+  const uint16_t* xp = ARR ? X + (int64_t)blockIdx.y * nt * (MT * 4 * 512)
+                           : X;
+  const int64_t xl = ARR ? lane * 8 : (int64_t)min(r, rows - 1) * ldx + qd * 8;
+  // the last workgroup may have fewer than P tiles of channels: it takes the
+  // last one again, and does not store it
+  const int panels = (N + 15) / 16;
+  int64_t first[P];
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-    xrow[t] = X + (int64_t)(m0 + min(t * 16 + r, rows - 1)) * ldx;
+  for (int p = 0; p < P; ++p) first[p] = (int64_t)min(panel0 + p, panels - 1) * nt;
+  const uint8_t* pp = reinterpret_cast<const uint8_t*>(params);
 
-  // this lane's 4 channels' entries: scales, or (scale, z) pairs
-  using Par = typename std::conditional<ZEROS, v4u, v2u>::type;
-  struct Tile {
-    v4u w[P];
-    v4u x[MT][4];
-    Par par[P][NG];
-  };
-  auto load = [&](Tile& d, int t) __attribute__((always_inline)) {
+  const Nibbles nib = nibbles<BF16>();
+
+  v4u w[2][P], x[MT][4];
+  Par par[2][P];
+  auto load_w = [&](int st, int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int64_t tile = (int64_t)(panel0 + p) * nt + t;
-      d.w[p] = __builtin_nontemporal_load(
-          reinterpret_cast<const v4u*>(Wq + tile * kInt4TileBytes + lane * 16));
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        d.par[p][g] = *reinterpret_cast<const Par*>(params + ((tile * NG + g) * 16 + 4 * qd) * EB);
-      }
+      const int64_t tile = first[p] + t;
+      w[st][p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(Wq + tile * kInt4TileBytes) + lane);
+      par[st][p] = reinterpret_cast<const Par*>(pp + tile * (16 * PB))[r];
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int k = t * kInt4TileK + s * 32 + qd * 8;
-        d.x[m][s] = v4u{0, 0, 0, 0};
-        if (k < K) d.x[m][s] = *reinterpret_cast<const v4u*>(xrow[m] + k);
-      }
+  };
+  auto load_x = [&](int t, int m, int s) __attribute__((always_inline)) {
+    x[m][s] = *reinterpret_cast<const v4u*>(
+        xp + (ARR ? (((int64_t)t * MT + m) * 4 + s) * 512 : (int64_t)t * kInt4TileK + s * 32) + xl);
+  };
+  // 16-bit word i of the entries (a scale, and with zero points 1024 + z), twice
+  auto word2 = [](const Par& e, int i) __attribute__((always_inline)) {
+    uint32_t u;
+    if constexpr (PB <= 4)
+      u = e;
+    else
+      u = e[i >> 1];
+    return __builtin_amdgcn_perm(u, u, (i & 1) ? 0x03020302u : 0x01000100u);
   };
 
   v4f tot[P][MT];
@@ -124,8 +155,10 @@ __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
 #pragma unroll
     for (int m = 0; m < MT; ++m) tot[p][m] = v4f{0, 0, 0, 0};
 
-  auto compute = [&](const Tile& d) __attribute__((always_inline)) {
-    constexpr uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;
+  // tile of stage st; a step's X registers take tile tn's as soon as the step
+  // is done (tn < 0: none)
+  auto compute = [&](int st, int tn) __attribute__((always_inline)) {
+    constexpr uint32_t one = 0x3f803f80u;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       __builtin_amdgcn_sched_barrier(0);
@@ -138,48 +171,66 @@ __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
       }
 #pragma unroll
       for (int s = g * GS; s < (g + 1) * GS; ++s) {
-        if constexpr (CORR)
+        if constexpr (BF16)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) sx[m] = mfma32<BF16>(v4u{one, one, one, one}, d.x[m][s], sx[m]);
+          for (int m = 0; m < MT; ++m) sx[m] = mfma32<true>(x[m][s], v4u{one, one, one, one}, sx[m]);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const v4u a = codes8<BF16>(d.w[p][s]);
+          const uint32_t z = ZEROS && !BF16 ? word2(par[st][p], 2 * g + 1) : 0x64086408u;
+          const v4u b = codes8<BF16>(w[st][p][s], z, nib);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[p][m] = mfma32<BF16>(a, d.x[m][s], acc[p][m]);
+          for (int m = 0; m < MT; ++m) acc[p][m] = mfma32<BF16>(x[m][s], b, acc[p][m]);
         }
+        if (tn >= 0)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) load_x(tn, m, s);
       }
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+      for (int p = 0; p < P; ++p) {
+        const float sc = h2f((uint16_t)word2(par[st][p], ZEROS ? 2 * g : g));
+        const float off = ZEROS ? h2f((uint16_t)word2(par[st][p], 2 * g + 1)) - 896.0f : 136.0f;  // 128 + z
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const Par& e = d.par[p][g];
-          const uint32_t u = ZEROS ? e[i] : e[i / 2] >> (16 * (i & 1));
-          const float sc = h2f((uint16_t)u);
-          float off = kOff;
-          if constexpr (ZEROS) off += h2f((uint16_t)(u >> 16));
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float a = acc[p][m][i];
-            if constexpr (CORR) a = __builtin_fmaf(-off, sx[m][i], a);
-            tot[p][m][i] = __builtin_fmaf(sc, a, tot[p][m][i]);
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[p][m][i];
+            if constexpr (BF16) v = __builtin_fmaf(-off, sx[m][i], v);
+            tot[p][m][i] = __builtin_fmaf(sc, v, tot[p][m][i]);
           }
-        }
+      }
     }
   };
 
-  // the next tile's loads are in flight while one is multiplied
-  if (wave < nt) {
-    Tile d[2];
-    load(d[0], wave);
-    int t = wave;
-    for (; t + waves < nt; t += 2 * waves) {
-      load(d[1], t + waves);
-      compute(d[0]);
-      if (t + 2 * waves < nt) load(d[0], t + 2 * waves);
-      compute(d[1]);
+  // whole tiles: while one is multiplied, the next one's loads are in flight
+  const int whole = ARR ? nt : K / kInt4TileK;
+  const int last = whole - 1;
+  if (wave < whole) {
+    load_w(0, wave);
+    load_w(1, min(wave + waves, last));
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) load_x(wave, m, s);
+    for (int t = wave; t < whole; t += 2 * waves) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        if (st > 0 && t + waves >= whole) break;
+        // a wave at its end reads the last tile again: with a branch around
+        // the loads their registers spill
+        compute(st, min(t + (st + 1) * waves, last));
+        load_w(st, min(t + (st + 2) * waves, last));
+      }
     }
-    if (t < nt) compute(d[0]);
+  }
+  // the last tile of a K that is not a multiple of 128
+  if (!ARR && whole < nt && wave == whole % waves) {
+    load_w(0, whole);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      x[0][s] = v4u{0, 0, 0, 0};
+      if (whole * kInt4TileK + s * 32 + qd * 8 < K) load_x(whole, 0, s);
+    }
+    compute(0, -1);
   }
 
   // the waves' partial sums, added in wave order
@@ -195,7 +246,7 @@ __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
     const int nl = o % (16 * P), m = o / (16 * P);
     const int n = panel0 * 16 + nl;
     if (n >= N) continue;
-    const int at = (((nl >> 4) * MT + (m >> 4)) * 4 + (nl & 3)) * 64 + ((nl & 15) >> 2) * 16 + (m & 15);
+    const int at = (((nl >> 4) * MT + (m >> 4)) * 4 + (m & 3)) * 64 + ((m & 15) >> 2) * 16 + (nl & 15);
     float y = 0.0f;
     for (int w = 0; w < waves; ++w) y += red[w * P * MT * 256 + at];
     if (bias != nullptr) y += BF16 ? bf2f(bias[n]) : h2f(bias[n]);
@@ -203,25 +254,37 @@ __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
   }
 }
 
-// Rows of X that are not 16-byte aligned or not a multiple of 8 long, copied
-// to rows of K rounded up to 8 with zeros behind.
-__global__ __launch_bounds__(256) void k_int4_pad_x(const uint16_t* __restrict__ X, int M, int K,
-                                                    int64_t ldx, int Kp, uint16_t* __restrict__ P) {
-  const int oct = Kp / 8;
-  const int64_t total = (int64_t)M * oct;
+// X in operand order: per 64 rows (16 * MT), k tile, 16 rows and 32 k the 64
+// lanes' 8 elements (lane l: row l % 16, k 8 * (l / 16) ..), zeros past M and K.
+// One KiB a load then comes from one place.  Rows of a usual X lie a power of
+// two apart, 16 of them in one channel of the L2, and every workgroup reads
+// them: 64 x 8192 x 13824 took 50.7 us from the rows, 26.4 us in this order.
+__global__ __launch_bounds__(256) void k_int4_arrange(const uint16_t* __restrict__ X, int M, int K,
+                                                      int64_t ldx, int MT, int64_t nt, int vec,
+                                                      int64_t total, uint16_t* __restrict__ A) {
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t m = i / oct;
-    const int k = (int)(i % oct) * 8;
-    const uint16_t* row = X + m * ldx;
-    v4u x;
+    const int l = (int)(i & 63), s = (int)(i >> 6) & 3;
+    const int64_t f = i >> 8;  // (chunk, tile, 16 rows)
+    const int m = (int)(f % MT);
+    const int64_t t = f / MT % nt, chunk = f / MT / nt;
+    const int64_t row = chunk * 16 * MT + m * 16 + (l & 15);
+    const int64_t k = t * kInt4TileK + s * 32 + (l >> 4) * 8;
+    v4u x = {0, 0, 0, 0};
+    if (row < M) {
+      const uint16_t* p = X + row * ldx + k;
+      if (vec && k + 8 <= K) {
+        x = *reinterpret_cast<const v4u*>(p);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t a = k + 2 * e < K ? row[k + 2 * e] : 0u;
-      const uint32_t b = k + 2 * e + 1 < K ? row[k + 2 * e + 1] : 0u;
-      x[e] = a | (b << 16);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a = k + 2 * e < K ? p[2 * e] : 0u;
+          const uint32_t b = k + 2 * e + 1 < K ? p[2 * e + 1] : 0u;
+          x[e] = a | (b << 16);
+        }
+      }
     }
-    *reinterpret_cast<v4u*>(P + i * 8) = x;
+    *reinterpret_cast<v4u*>(A + i * 8) = x;
   }
 }
 
@@ -262,7 +325,7 @@ __global__ void k_int4_pack(const uint8_t* __restrict__ codes, int64_t N, int64_
   }
 }
 
-// Parameter entries; i counts them in stored order [panel][tile][sub-group][channel].
+// Parameter entries; i counts them in stored order [panel][tile][channel][sub-group].
 __global__ void k_int4_params(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
                               int64_t N, int64_t K, int64_t group, int gs, int64_t nt,
                               int64_t total, uint16_t* __restrict__ params) {
@@ -270,15 +333,15 @@ __global__ void k_int4_params(const uint16_t* __restrict__ scales, const uint8_t
   const int64_t groups = (K + group - 1) / group;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t e = i >> 4, tile = e / ng;
-    const int64_t n = (tile / nt) * 16 + (i & 15);
-    const int64_t k = (tile % nt) * kInt4TileK + (e % ng) * gs;
+    const int64_t e = i / ng, tile = e >> 4;
+    const int64_t n = (tile / nt) * 16 + (e & 15);
+    const int64_t k = (tile % nt) * kInt4TileK + (i % ng) * gs;
     const bool in = n < N && k < K;
     const int64_t at = in ? n * groups + k / group : 0;
     const uint16_t sc = in ? scales[at] : (uint16_t)0;
     if (zeros != nullptr) {
       params[2 * i] = sc;
-      params[2 * i + 1] = f2h(in ? (float)(zeros[at] & 15) : 8.0f);
+      params[2 * i + 1] = f2h(1024.0f + (in ? (float)(zeros[at] & 15) : 8.0f));
     } else {
       params[i] = sc;
     }
@@ -329,11 +392,11 @@ __global__ __launch_bounds__(256) void k_int4_prepare(const uint16_t* __restrict
   const int ng = kInt4TileK / gs;
   for (int64_t k = k0 + lane * gs; k < kend; k += 64 * gs) {
     const int64_t tile = (n >> 4) * nt + (k >> 7);
-    const int64_t e = (tile * ng + (k & 127) / gs) * 16 + (n & 15);
+    const int64_t e = (tile * 16 + (n & 15)) * ng + (k & 127) / gs;
     const bool in = n < N && k < K;
     if (zeros) {
       params[2 * e] = in ? sc : (uint16_t)0;
-      params[2 * e + 1] = f2h(in ? z : 8.0f);
+      params[2 * e + 1] = f2h(1024.0f + (in ? z : 8.0f));
     } else {
       params[e] = in ? sc : (uint16_t)0;
     }
@@ -379,7 +442,7 @@ hipError_t launch_int4_prepare(const uint16_t* W, bool bf16, int64_t N, int64_t 
 
 namespace {
 
-template <bool BF16, bool ZEROS, int GS, int P, int MT>
+template <bool BF16, bool ZEROS, int GS, int P, int MT, bool ARR>
 hipError_t run(const uint16_t* X, int M, int K, int64_t ldx, const void* Wq, const void* params,
                int N, const uint16_t* bias, uint16_t* Y, hipStream_t s) {
   const int nt = (int)int4_tiles_k(K);
@@ -387,38 +450,72 @@ hipError_t run(const uint16_t* X, int M, int K, int64_t ldx, const void* Wq, con
   while (waves > nt) waves /= 2;
   const dim3 grid((unsigned)((N + 16 * P - 1) / (16 * P)), (unsigned)((M + 16 * MT - 1) / (16 * MT)));
   const size_t lds = (size_t)waves * P * MT * 1024;
-  hipLaunchKernelGGL((k_int4_linear<BF16, ZEROS, GS, P, MT>), grid, dim3(64 * waves), lds, s, X, M,
+  hipLaunchKernelGGL((k_int4_linear<BF16, ZEROS, GS, P, MT, ARR>), grid, dim3(64 * waves), lds, s, X, M,
                      K, ldx, static_cast<const uint8_t*>(Wq), static_cast<const uint16_t*>(params),
                      N, bias, Y);
   return hipGetLastError();
 }
 
+// P tiles of channels per wave, so that one round of workgroups covers N with
+// one on every CU: X is read once per workgroup, from the L2, and that is what
+// small P costs; large P leaves CUs idle (1 x 8192 x 28672: 23.5 us with 7 and
+// 256 workgroups, 27.3 with 4, 32 with 1; 1 x 11008 x 4096: 9.7 us with 1, 17.1
+// with 4).
 template <bool BF16, bool ZEROS, int GS>
-hipError_t pick_tile(const uint16_t* X, int M, int K, int64_t ldx, const void* Wq,
+hipError_t pick_tile(const uint16_t* X, bool arranged, int M, int K, int64_t ldx, const void* Wq,
                      const void* params, int N, const uint16_t* bias, uint16_t* Y, hipStream_t s) {
-  constexpr int kWide = GS == 1 ? 2 : 4;  // tiles of channels a wave takes at once
-  constexpr int kRows = GS == 1 ? 1 : 2;
-  if (M <= 16 && N < 16384) return run<BF16, ZEROS, GS, 1, 1>(X, M, K, ldx, Wq, params, N, bias, Y, s);
-  if (M <= 16) return run<BF16, ZEROS, GS, kWide, 1>(X, M, K, ldx, Wq, params, N, bias, Y, s);
-  if (M <= 32) return run<BF16, ZEROS, GS, kRows, 2>(X, M, K, ldx, Wq, params, N, bias, Y, s);
-  return run<BF16, ZEROS, GS, kRows, 4>(X, M, K, ldx, Wq, params, N, bias, Y, s);
+#define INT4_RUN(p, m, a) return run<BF16, ZEROS, GS, p, m, a>(X, M, K, ldx, Wq, params, N, bias, Y, s)
+  const int panels = (N + 15) / 16;
+  const int P = (panels + kCus - 1) / kCus;
+  if (!arranged) {
+    if (P <= 1) INT4_RUN(1, 1, false);
+    if (P == 2) INT4_RUN(2, 1, false);
+    if (P == 3) INT4_RUN(3, 1, false);
+    if constexpr (GS > 1) {  // 32-wide groups: no registers for more than 4
+      if (P == 5) INT4_RUN(5, 1, false);
+      if (P > 5) INT4_RUN(7, 1, false);
+    }
+    INT4_RUN(4, 1, false);
+  }
+  const int mt = int4_row_tiles(M);
+  if (mt == 1 && P <= 2) INT4_RUN(1, 1, true);
+  if (mt == 1) INT4_RUN(4, 1, true);
+  if (P <= 1 && mt == 2) INT4_RUN(1, 2, true);
+  if (P <= 1 && mt == 3) INT4_RUN(1, 3, true);
+  if (P <= 1) INT4_RUN(1, 4, true);
+  if (P == 2 || GS == 1) {
+    if (mt == 2) INT4_RUN(2, 2, true);
+    if (mt == 3) INT4_RUN(2, 3, true);
+    INT4_RUN(2, 4, true);
+  }
+  if constexpr (GS > 1) {
+    if (mt == 2) INT4_RUN(4, 2, true);
+    if (mt == 3) INT4_RUN(4, 3, true);
+  }
+  INT4_RUN(GS > 1 ? 4 : 2, 4, true);
+#undef INT4_RUN
 }
 
 template <bool BF16, bool ZEROS>
-hipError_t pick_group(const uint16_t* X, int M, int K, int64_t ldx, const void* Wq,
+hipError_t pick_group(const uint16_t* X, bool arranged, int M, int K, int64_t ldx, const void* Wq,
                       const void* params, int N, int steps, const uint16_t* bias, uint16_t* Y,
                       hipStream_t s) {
   switch (steps) {
-    case 1: return pick_tile<BF16, ZEROS, 1>(X, M, K, ldx, Wq, params, N, bias, Y, s);
-    case 2: return pick_tile<BF16, ZEROS, 2>(X, M, K, ldx, Wq, params, N, bias, Y, s);
-    default: return pick_tile<BF16, ZEROS, 4>(X, M, K, ldx, Wq, params, N, bias, Y, s);
+    case 1: return pick_tile<BF16, ZEROS, 1>(X, arranged, M, K, ldx, Wq, params, N, bias, Y, s);
+    case 2: return pick_tile<BF16, ZEROS, 2>(X, arranged, M, K, ldx, Wq, params, N, bias, Y, s);
+    default: return pick_tile<BF16, ZEROS, 4>(X, arranged, M, K, ldx, Wq, params, N, bias, Y, s);
   }
 }
 
 }  // namespace
 
-bool int4_x_aligned(const uint16_t* X, int64_t M, int64_t K, int64_t ldx) {
-  return K % 8 == 0 && (ldx % 8 == 0 || M == 1) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
+bool int4_x_direct(const uint16_t* X, int64_t M, int64_t K, int64_t ldx) {
+  return M <= 16 && K % 8 == 0 && (ldx % 8 == 0 || M == 1) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
+}
+
+size_t int4_arranged_bytes(int64_t M, int64_t K) {
+  const int64_t per = 16 * int4_row_tiles(M);
+  return (size_t)((M + per - 1) / per * per) * int4_tiles_k(K) * kInt4TileK * 2;
 }
 
 hipError_t launch_int4_linear(const uint16_t* X, bool bf16, int64_t M, int64_t K, int64_t ldx,
@@ -430,21 +527,22 @@ hipError_t launch_int4_linear(const uint16_t* X, bool bf16, int64_t M, int64_t K
                        (int)N, Y);
     return hipGetLastError();
   }
-  if (!int4_x_aligned(X, M, K, ldx)) {
-    const int Kp = (int)((K + 7) / 8 * 8);
-    hipLaunchKernelGGL(k_int4_pad_x, dim3(grid_for(M * (Kp / 8), 256)), dim3(256), 0, s, X, (int)M,
-                       (int)K, ldx, Kp, ws);
+  const bool arr = !int4_x_direct(X, M, K, ldx);
+  if (arr) {
+    const int64_t total = (int64_t)int4_arranged_bytes(M, K) / 16;
+    const int vec = (ldx % 8 == 0 || M == 1) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
+    hipLaunchKernelGGL(k_int4_arrange, dim3(grid_for(total, 256)), dim3(256), 0, s, X, (int)M,
+                       (int)K, ldx, int4_row_tiles(M), int4_tiles_k(K), vec, total, ws);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     X = ws;
-    K = ldx = Kp;
   }
   const int steps = int4_group_steps(group), m = (int)M, k = (int)K, n = (int)N;
   if (bf16)
-    return zeros ? pick_group<true, true>(X, m, k, ldx, Wq, params, n, steps, bias, Y, s)
-                 : pick_group<true, false>(X, m, k, ldx, Wq, params, n, steps, bias, Y, s);
-  return zeros ? pick_group<false, true>(X, m, k, ldx, Wq, params, n, steps, bias, Y, s)
-               : pick_group<false, false>(X, m, k, ldx, Wq, params, n, steps, bias, Y, s);
+    return zeros ? pick_group<true, true>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s)
+                 : pick_group<true, false>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s);
+  return zeros ? pick_group<false, true>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s)
+               : pick_group<false, false>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s);
 }
 
 }  // namespace i8mm

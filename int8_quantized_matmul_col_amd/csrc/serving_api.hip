@@ -130,8 +130,8 @@ INT8MM_API int int4_prepare_weight(const void* W, int dtype, int64_t N, int64_t 
 
 INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N) {
   if (!int4_shape(N, K) || M < 0 || M > kMaxCount) return 0;
-  // rows that the kernel cannot read as they are (see int4_x_aligned)
-  return align_up((size_t)M * (size_t)((K + 7) / 8 * 8) * 2);
+  if (M == 0 || K == 0) return 0;
+  return align_up(i8mm::int4_arranged_bytes(M, K));
 }
 
 INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx,
@@ -146,7 +146,7 @@ INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64
   if (!aligned(X, 2) || !aligned(Y, 2) || !aligned(bias, 2) || !aligned(Wq, 16) || !aligned(params, 16))
     return INT8MM_EINVAL;
   const uint16_t* x = static_cast<const uint16_t*>(X);
-  if (K > 0 && !i8mm::int4_x_aligned(x, M, K, ldx) &&
+  if (K > 0 && !i8mm::int4_x_direct(x, M, K, ldx) &&
       !workspace_ok(workspace, workspace_bytes, int4_linear_workspace_size(M, K, N)))
     return INT8MM_EWORKSPACE;
   return status_of(i8mm::launch_int4_linear(x, dtype == INT8MM_BF16, M, K, ldx, Wq, params, N,

@@ -12,10 +12,10 @@ namespace i8mm {
 // ---- 4-bit weights: tiles of 16 channels x 128 k, 1 KiB each
 constexpr int kInt4TileK = 128;
 constexpr int kInt4TileBytes = 1024;
-constexpr int kInt4PadRows = 64;  // channels padded so that a wave may take 4 tiles at once
-constexpr int kInt4RowChunk = 64;  // rows of X per pass over the weight
+// 16-row tiles of X per pass over the weight
+inline int int4_row_tiles(int64_t M) { return M > 48 ? 4 : (int)((M + 15) / 16); }
 
-inline int64_t int4_padded_rows(int64_t N) { return (N + kInt4PadRows - 1) / kInt4PadRows * kInt4PadRows; }
+inline int64_t int4_padded_rows(int64_t N) { return (N + 15) / 16 * 16; }
 inline int64_t int4_tiles_k(int64_t K) { return (K + kInt4TileK - 1) / kInt4TileK; }
 // 32-k steps of a tile that share one parameter entry
 inline int int4_group_steps(int64_t group) { return group >= 128 ? 4 : (int)(group / 32); }
@@ -29,9 +29,10 @@ hipError_t launch_int4_linear(const uint16_t* X, bool bf16, int64_t M, int64_t K
                               const void* Wq, const void* params, int64_t N, int64_t group,
                               bool zeros, const uint16_t* bias, uint16_t* Y, uint16_t* ws,
                               hipStream_t s);
-// Whether the kernel reads X as it is; otherwise it goes through ws (rows of K
-// rounded up to 8).
-bool int4_x_aligned(const uint16_t* X, int64_t M, int64_t K, int64_t ldx);
+// Whether the kernel reads X as it is; otherwise X goes through ws in operand
+// order (int4_arranged_bytes).
+bool int4_x_direct(const uint16_t* X, int64_t M, int64_t K, int64_t ldx);
+size_t int4_arranged_bytes(int64_t M, int64_t K);
 
 // ---- key-value pages
 hipError_t launch_kv_append(const uint16_t* k, const uint16_t* v, bool bf16, int T, int64_t kts,

@@ -198,7 +198,7 @@ def int4_unpack_weight(w: Int4Weight) -> Tuple:
     a prepared weight: the reverse of int4_pack_weight (an index permutation)."""
     N, K, g = w.out_features, w.in_features, w.group_size
     nt, gs = (K + 127) // 128, min(g, 128)
-    Np = (N + 63) // 64 * 64
+    Np = (N + 15) // 16 * 16
     dev = w.Wq.device
     if N == 0 or K == 0:
         shape = (N, (K + g - 1) // g)
@@ -210,11 +210,11 @@ def int4_unpack_weight(w: Int4Weight) -> Tuple:
     nib = torch.stack((b & 15, b >> 4), -1).flatten(-2)           # [.., 8] by bit position
     nib = nib[..., [0, 4, 1, 5, 2, 6, 3, 7]]                        # element e at p(e)
     codes = nib.permute(0, 3, 1, 4, 2, 5).reshape(Np, nt * 128)    # k = 32 j + 8 q + e
-    par = w.params.view(torch.float16).view(Np // 16, nt, 128 // gs, 16, 2 if w.zeros else 1)
-    par = par.permute(0, 3, 1, 2, 4).reshape(Np, nt * (128 // gs), -1)[:N, ::g // gs]
+    par = w.params.view(torch.float16).view(Np // 16, nt, 16, 128 // gs, 2 if w.zeros else 1)
+    par = par.permute(0, 2, 1, 3, 4).reshape(Np, nt * (128 // gs), -1)[:N, ::g // gs]
     par = par[:, : (K + g - 1) // g]
     return (codes[:N, :K].contiguous(), par[..., 0].contiguous(),
-            par[..., 1].to(torch.uint8).contiguous() if w.zeros else None)
+            (par[..., 1] - 1024).to(torch.uint8).contiguous() if w.zeros else None)
 
 
 def int4_linear_workspace_size(M: int, K: int, N: int) -> int:
@@ -249,8 +249,8 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
     else:
         _check_out(out, (M, N), X.dtype, "out", dev)
         Y = out
-    # only rows that are not on 16 bytes pass through a workspace
-    if workspace is None and (K % 8 or ldx % 8 or X.data_ptr() % 16):
+    # up to 16 rows on 16 bytes are read as they are, others through a workspace
+    if workspace is None and (M > 16 or K % 8 or ldx % 8 or X.data_ptr() % 16):
         workspace = torch.empty((int4_linear_workspace_size(M, K, N),), dtype=torch.uint8, device=dev)
     _call("int4_linear", dev, X.data_ptr(), dt, M, K, ldx, w.Wq.data_ptr(), w.params.data_ptr(), N,
           w.group_size, w.zeros, None if bias is None else bias.data_ptr(), Y.data_ptr(),

@@ -76,8 +76,8 @@ def test_header_is_c_and_the_struct_matches(tmp_path):
 
 def test_int4_sizes(lib):
     assert lib.int4_weight_bytes(64, 128) == 64 * 64
-    assert lib.int4_weight_bytes(1, 1) == 64 * 64
-    assert lib.int4_weight_bytes(65, 129) == 128 * 128
+    assert lib.int4_weight_bytes(1, 1) == 16 * 64
+    assert lib.int4_weight_bytes(65, 129) == 80 * 128
     assert lib.int4_param_bytes(64, 128, 128, 0) == 128
     assert lib.int4_param_bytes(64, 128, 32, 1) == 64 * 4 * 4
     assert lib.int4_param_bytes(64, 1024, 512, 0) == 64 * 8 * 2
