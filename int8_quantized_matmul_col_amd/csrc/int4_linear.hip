@@ -491,8 +491,9 @@ hipError_t pick_tile(const uint16_t* X, bool arranged, int M, int K, int64_t ldx
   if constexpr (GS > 1) {
     if (mt == 2) INT4_RUN(4, 2, true);
     if (mt == 3) INT4_RUN(4, 3, true);
+    INT4_RUN(4, 4, true);
   }
-  INT4_RUN(GS > 1 ? 4 : 2, 4, true);
+  return hipErrorInvalidValue;  // not reached
 #undef INT4_RUN
 }
 
