@@ -24,9 +24,14 @@
 // exact operands; the key's scale multiplies the fp32 score, the value's the
 // fp32 probability.
 //
-// A long axis is split over workgroups, a workgroup's range over its 4
-// waves; waves join in LDS, workgroups in a second kernel, each in a fixed
-// order.
+// The batch's tokens, one sequence after the other, are dealt out evenly to 512
+// workgroups (two on every CU), which find their sequences from the lengths;
+// a workgroup's 4 waves take its chunks in turn.  So very different lengths
+// cost nothing (64 sequences of 1..8192 tokens, int8: 150 us with pieces of
+// one length, 103 us so), and one long sequence is split as well.  Waves join
+// in LDS, cut sequences in a second kernel, each in a fixed order.  Where no
+// sequence can be longer than 256 tokens each is one workgroup's, and there is
+// no second kernel (12.3 instead of 17.5 us for one of 200).
 #include "device_common.h"
 #include "serving_launch.h"
 
@@ -42,10 +47,9 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr int kJoinThreads = 256;
-constexpr int kMaxSplits = 1024;
-constexpr int kPieces = 512;     // workgroups aimed at; at most kMaxSplits
-constexpr int kMinTokens = 256;  // tokens per piece at least
-constexpr int kSplitAlign = 64;  // tokens; a multiple of both chunk sizes
+constexpr int kAlign = 64;  // of a sequence's first token, a multiple of both chunk sizes
+constexpr int kMaxParts = 512;  // workgroups that share a batch: two on every CU
+constexpr int kWhole = 256;     // tokens up to which a sequence is one workgroup's
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.0f;  // how far (log2) a score may exceed the running maximum
@@ -138,6 +142,34 @@ __device__ __forceinline__ Range visible(const KvAttentionArgs& a, int b, int nu
   return v;
 }
 
+// Work is counted in units of kWaves chunks.  units(): of a sequence.
+__device__ __forceinline__ int units(const Range& v, int unit) {
+  return v.len > v.lo ? (v.len - (v.lo & ~(kAlign - 1)) + unit - 1) / unit : 0;
+}
+// `total` units dealt out to `parts` workgroups: the first `more` get one more
+// than the others.
+struct Deal {
+  uint32_t each, more;
+  __device__ __forceinline__ Deal(uint32_t total, uint32_t parts)
+      : each(total / parts), more(total - total / parts * parts) {}
+  // where part x begins
+  __device__ __forceinline__ uint32_t begin(uint32_t x) const { return x * each + min(x, more); }
+  // the part that has unit u
+  __device__ __forceinline__ uint32_t of(uint32_t u) const {
+    const uint32_t big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
+  }
+};
+__device__ __forceinline__ int wave_scan(int n) {  // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(n, o, 64);
+    if (lane >= o) n += y;
+  }
+  return n;
+}
+
 struct Pages {
   const uint8_t* k;
   const uint8_t* v;
@@ -151,7 +183,7 @@ struct Pages {
 // CT: the cache's type; QBF: bfloat16 queries and results; NK: 32-dim steps
 // (EXACT: head_dim is NK * 32, otherwise at most that).
 template <int CT, bool QBF, int NK, bool EXACT>
-__global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a, Pages pg) {
+__global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(KvAttentionArgs a, Pages pg) {
   constexpr bool I8 = CT == kI8;
   constexpr bool PBF = CT != kF16;      // type of the P x V operands
   constexpr int CH = I8 ? 64 : 32;      // tokens per chunk
@@ -171,14 +203,70 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, qd = lane >> 4;
   const int group = a.group;
-  const int b = blockIdx.x / a.split.splits, sp = blockIdx.x % a.split.splits;
   const int tiles_h = (group + kKvHeadTile - 1) / kKvHeadTile;
   const int kvh = blockIdx.y / tiles_h, ht = blockIdx.y % tiles_h;
   const int heads = min(group - ht * kKvHeadTile, kKvHeadTile);  // query heads of this tile
   const int head0 = kvh * group + ht * kKvHeadTile;
+  constexpr int kUnit = kWaves * CH;
 
-  // Queries and the first table entries are requested before the length is
-  // known, so that the three do not wait for one another.
+  // This workgroup's units.  One workgroup per sequence: all of them.
+  // Otherwise the batch's units, one sequence after the other, are dealt out
+  // evenly, and the workgroup finds its sequences from the lengths.
+  int b = blockIdx.x, first = 0;      // lane i holds sequence first + i below
+  uint32_t u0 = 0, u1 = 0, before = 0;  // units of sequences before `first`
+  Range mine{0, 0, 0};
+  int own = 0, upto = 0;               // this lane's sequence: units, and with the lanes before
+  auto lanes = [&](int at) __attribute__((always_inline)) {
+    first = at;
+    mine = Range{0, 0, 0};
+    if (at + lane < a.B) mine = visible(a, at + lane, pg.num_pages, pg.ps);
+    own = units(mine, kUnit);
+    upto = wave_scan(own);
+  };
+  int idx = 0;  // of the current sequence among the lanes
+  int next_tab = -1;
+  bool looked = false;  // next_tab holds the next sequence's entries
+  if (a.parts > 0) {
+    uint32_t total = 0;
+    for (int at = 0; at < a.B; at += 64) {
+      lanes(at);
+      total += __builtin_amdgcn_readlane(upto, 63);
+    }
+    const Deal deal(total, a.parts);
+    u0 = deal.begin(blockIdx.x);
+    u1 = deal.begin(blockIdx.x + 1);
+    if (u0 >= u1) return;
+    if (first > 0) lanes(0);
+    while (before + __builtin_amdgcn_readlane(upto, 63) <= u0) {
+      before += __builtin_amdgcn_readlane(upto, 63);
+      lanes(first + 64);
+    }
+    idx = __builtin_ctzll(__ballot(before + upto > u0));
+  }
+
+  for (bool again = true, fresh = true; again; fresh = false) {
+  int row, lo, len, ua, ub, n;
+  if (a.parts > 0) {
+    b = first + idx;
+    row = __builtin_amdgcn_readlane(mine.row, idx);
+    lo = __builtin_amdgcn_readlane(mine.lo, idx);
+    len = __builtin_amdgcn_readlane(mine.len, idx);
+    n = __builtin_amdgcn_readlane(own, idx);
+    const uint32_t begin = before + __builtin_amdgcn_readlane(upto, idx) - n;
+    ua = u0 > begin ? (int)(u0 - begin) : 0;
+    ub = u1 - begin < (uint32_t)n ? (int)(u1 - begin) : n;
+    again = u1 > begin + n;
+  } else {
+    const Range v = visible(a, b, pg.num_pages, pg.ps);
+    row = v.row, lo = v.lo, len = v.len;
+    n = units(v, kUnit);
+    ua = 0, ub = n;
+    again = false;
+  }
+  const int s0 = (lo & ~(kAlign - 1)) + ua * kUnit;
+  const int s1 = min(len, (lo & ~(kAlign - 1)) + ub * kUnit);
+  const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;  // taken by the waves in turn
+
   // Q^T operand: head r, dims as the key loads order them
   v4u q[NK];
   {
@@ -190,26 +278,27 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
       if (d < D) q[j] = *reinterpret_cast<const v4u*>(qp + d);
     }
   }
-  const int row = a.rows != nullptr ? a.rows[b] : b;
-  const bool row_ok = (unsigned)row < (unsigned)a.table_rows;
-  const int32_t* trow = a.table + (int64_t)(row_ok ? row : 0) * a.table_width;
+  const int32_t* trow = a.table + (int64_t)row * a.table_width;
   auto entries = [&](int at) __attribute__((always_inline)) {
-    return row_ok && at + lane < a.table_width ? trow[at + lane] : -1;
+    return at + lane < a.table_width ? trow[at + lane] : -1;
   };
-  int pbase = (sp * a.split.tokens) >> pg.lps;
-  int tab = entries(pbase);  // lane's page id: table entry pbase + lane
-
-  const Range vis = visible(a, b, pg.num_pages, pg.ps);
-  const int s0 = (vis.lo & ~(kSplitAlign - 1)) + sp * a.split.tokens;
-  const int s1 = min(vis.len, s0 + a.split.tokens);
-  if (s0 >= s1 && a.split.splits > 1) return;  // the join knows
-
-  if (vis.lo >= kSplitAlign) {  // the pieces begin at the window
-    pbase = s0 >> pg.lps;
-    tab = entries(pbase);
+  int pbase = s0 >> pg.lps;
+  int tab;  // lane's page id: table entry pbase + lane
+  if (!looked)
+    tab = chunks > 0 ? entries(pbase) : -1;
+  else
+    tab = next_tab;
+  if (again) {
+    // the next sequence's first table entries, long before they are needed
+    int i = idx;
+    do ++i; while (i < 64 && __builtin_amdgcn_readlane(own, i) == 0);
+    looked = i < 64;
+    if (looked) {
+      const int at = (__builtin_amdgcn_readlane(mine.lo, i) & ~(kAlign - 1)) >> pg.lps;
+      const int32_t* t = a.table + (int64_t)__builtin_amdgcn_readlane(mine.row, i) * a.table_width;
+      next_tab = at + lane < a.table_width ? t[at + lane] : -1;
+    }
   }
-
-  const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;  // taken by the waves in turn
 
   v4f o[DT];
 #pragma unroll
@@ -270,7 +359,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
     for (int c = wave; c < chunks; c += kWaves) {
       const int t0 = s0 + c * CH;
       const bool page_ok = vvalid;
-      const bool whole = t0 >= vis.lo && t0 + CH <= s1 && __all(page_ok);
+      const bool whole = t0 >= lo && t0 + CH <= s1 && __all(page_ok);
 
       // scores
       v4f s[NT];
@@ -305,7 +394,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
           if (a.softcap > 0.0f) x = a.softcap * kLog2e * tanhf(x);
           if (!whole) {
             const int tok = t0 + SUB * qd + 4 * t + i;
-            x = page_ok && tok >= vis.lo && tok < s1 ? x : -INFINITY;
+            x = page_ok && tok >= lo && tok < s1 ? x : -INFINITY;
           }
           s[t][i] = x;
         }
@@ -337,7 +426,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
       if constexpr (I8) {
         const float vs_ok = page_ok ? vs16 : 0.0f;
         const int tok = t0 + SUB * qd + r;  // whose scale this lane holds
-        const float vs = whole || (tok >= vis.lo && tok < s1) ? vs_ok : 0.0f;
+        const float vs = whole || (tok >= lo && tok < s1) ? vs_ok : 0.0f;
         scale_tokens<0>(s, vs);
       } else if (!whole) {
         // values of tokens that are not visible may be anything: 0, not 0 * NaN
@@ -345,8 +434,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = t0 + SUB * qd + 2 * e;
-          const uint32_t a0 = page_ok && tok >= vis.lo && tok < s1 ? 0x0000ffffu : 0u;
-          const uint32_t a1 = page_ok && tok + 1 >= vis.lo && tok + 1 < s1 ? 0xffff0000u : 0u;
+          const uint32_t a0 = page_ok && tok >= lo && tok < s1 ? 0x0000ffffu : 0u;
+          const uint32_t a1 = page_ok && tok + 1 >= lo && tok + 1 < s1 ? 0xffff0000u : 0u;
           keep[e] = a0 | a1;
         }
 #pragma unroll
@@ -408,84 +497,123 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attention(KvAttentionArgs a,
       den += f * sl[w * 16 + h];
       sum += f * so[((w * DT + (d >> 4)) * 4 + (d & 3)) * 64 + ((d & 15) >> 2) * 16 + h];
     }
-    const int64_t bh = (int64_t)b * a.q_heads + head0 + h;
-    if (a.split.splits == 1) {
+    if (ua == 0 && ub == n) {  // the whole sequence
+      const int64_t bh = (int64_t)b * a.q_heads + head0 + h;
       const float y = den == 0.0f ? 0.0f : sum * (1.0f / den);
       a.out[bh * D + d] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
       if (d == 0 && a.lse != nullptr)
         a.lse[bh] = den == 0.0f ? -INFINITY : (mx - kBias + __builtin_log2f(den)) * kLn2;
     } else {
-      const int64_t part = bh * a.split.splits + sp;
-      a.part_o[part * D + d] = sum;
+      // only a workgroup's first and last sequence can be cut: two places
+      const int64_t piece = ((int64_t)blockIdx.y * a.parts + blockIdx.x) * 2 + (fresh ? 0 : 1);
+      const int64_t at_h = piece * a.tile_heads + h;
+      a.part_o[at_h * D + d] = sum;
       if (d == 0) {
-        a.part_ml[2 * part] = mx - kBias;
-        a.part_ml[2 * part + 1] = den;
+        a.part_ml[2 * at_h] = mx - kBias;
+        a.part_ml[2 * at_h + 1] = den;
       }
     }
   }
+  if (again) {
+    __syncthreads();  // the next sequence's sums take the same place
+    do {
+      if (++idx == 64) {
+        before += __builtin_amdgcn_readlane(upto, 63);
+        lanes(first + 64);
+        idx = 0;
+        looked = false;
+      }
+    } while (__builtin_amdgcn_readlane(own, idx) == 0);
+  }
+  }
 }
 
-// Joins the pieces of one (sequence, query head).  Threads hold 4 dims each;
-// the block's groups of D/4 threads take the pieces in turn.
+// Joins the pieces of one (sequence, query head); a lane holds 4 dims.
 template <bool QBF>
 __global__ __launch_bounds__(kJoinThreads) void k_kv_join(KvAttentionArgs a, int num_pages, int ps,
-                                                          int D) {
-  __shared__ float f[kMaxSplits];
-  __shared__ float red[kJoinThreads / 64];
+                                                          int D, int unit) {
+  __shared__ float f[kMaxParts];
+  __shared__ float dens[kJoinThreads / 64];
   __shared__ v4f part[kJoinThreads];
   const int64_t bh = blockIdx.x;
-  const Range vis = visible(a, (int)(bh / a.q_heads), num_pages, ps);
-  const int start = vis.lo & ~(kSplitAlign - 1);
-  const int n = vis.len > vis.lo ? (vis.len - start + a.split.tokens - 1) / a.split.tokens : 0;
-  const float* ml = a.part_ml + bh * a.split.splits * 2;
-  const float* po = a.part_o + bh * a.split.splits * D;
-  auto all = [&](float x, auto op) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x = op(x, __shfl_xor(x, o, 64));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = red[0];
-    for (int w = 1; w < kJoinThreads / 64; ++w) x = op(x, red[w]);
-    return x;
+  const int b = (int)(bh / a.q_heads), hq = (int)(bh % a.q_heads);
+  const int lane = threadIdx.x & 63;
+  // where this sequence's units lie among the batch's
+  uint32_t total = 0, begin = 0;
+  int own = 0;
+  for (int at = 0; at < a.B; at += 64) {
+    const int n = at + lane < a.B ? units(visible(a, at + lane, num_pages, ps), unit) : 0;
+    const int upto = wave_scan(n);
+    if (b >= at && b < at + 64) {
+      own = __builtin_amdgcn_readlane(n, b - at);
+      begin = total + __builtin_amdgcn_readlane(upto, b - at) - own;
+    }
+    total += __builtin_amdgcn_readlane(upto, 63);
+  }
+  const Deal deal(total, a.parts);
+  const int x0 = own > 0 ? deal.of(begin) : 0, x1 = own > 0 ? deal.of(begin + own - 1) : 0;
+  if (own > 0 && x0 == x1) return;  // one workgroup had it all
+  const int n = own > 0 ? x1 - x0 + 1 : 0;
+  const int tiles_h = (a.group + kKvHeadTile - 1) / kKvHeadTile;
+  const int gy = hq / a.group * tiles_h + hq % a.group / kKvHeadTile;
+  const int h = hq % a.group % kKvHeadTile;
+  // Piece i: of workgroup x0 + i, its first place unless it began with another
+  // sequence.  (Parts between two that have units have units too.)
+  auto piece = [&](int i) {
+    const int64_t at = ((int64_t)gy * a.parts + x0 + i) * 2 + (deal.begin(x0 + i) < begin ? 1 : 0);
+    return at * a.tile_heads + h;
   };
+  // every wave forms the maximum over all pieces; the factors are shared
   float mx = -INFINITY, den = 0.0f;
+  for (int i = lane; i < n; i += 64) mx = fmaxf(mx, a.part_ml[2 * piece(i)]);
+  mx = wave_max(mx);
   for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-    f[i] = ml[2 * i];
-    mx = fmaxf(mx, f[i]);
+    const float* ml = a.part_ml + 2 * piece(i);
+    // no visible score: the sums are 0 (or NaN, which stays)
+    f[i] = ml[0] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - mx);
+    den += f[i] * ml[1];
   }
-  mx = all(mx, [](float x, float y) { return fmaxf(x, y); });
-  for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-    f[i] = f[i] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(f[i] - mx);
-    den += f[i] * ml[2 * i + 1];
-  }
-  den = all(den, [](float x, float y) { return x + y; });
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) den += __shfl_xor(den, o, 64);
+  if (lane == 0) dens[threadIdx.x >> 6] = den;
+  __syncthreads();
 
   const int quads = D / 4, groups = kJoinThreads / quads;
   const int g = threadIdx.x / quads, d = threadIdx.x % quads * 4;
   v4f sum = {0, 0, 0, 0};
   if (g < groups) {
-#pragma unroll 4
-    for (int i = g; i < n; i += groups) sum += f[i] * *reinterpret_cast<const v4f*>(po + (int64_t)i * D + d);
+    constexpr int kU = 4;  // loads in flight
+    for (int i = g; i < n; i += groups * kU) {
+      v4f v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i + u * groups < n)
+          v[u] = *reinterpret_cast<const v4f*>(a.part_o + piece(i + u * groups) * D + d);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i + u * groups < n) sum += f[i + u * groups] * v[u];
+    }
   }
   part[threadIdx.x] = sum;
   __syncthreads();
   if (g == 0) {
-    for (int w = 1; w < groups; ++w) sum += part[w * quads + threadIdx.x];
+    den = 0.0f;
+    for (int w = 0; w < kJoinThreads / 64; ++w) den += dens[w];
+    for (int w = 1; w < groups && w < n; ++w) sum += part[w * quads + threadIdx.x];
     const float inv = 1.0f / den;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float y = den == 0.0f ? 0.0f : sum[e] * inv;
       a.out[bh * D + d + e] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
     }
+    if (threadIdx.x == 0 && a.lse != nullptr)
+      a.lse[bh] = den == 0.0f ? -INFINITY : (mx + __builtin_log2f(den)) * kLn2;
   }
-  if (threadIdx.x == 0 && a.lse != nullptr)
-    a.lse[bh] = den == 0.0f ? -INFINITY : (mx + __builtin_log2f(den)) * kLn2;
 }
 
 template <int CT, bool QBF, int NK, bool EXACT>
 hipError_t run(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
-  const dim3 grid((unsigned)a.B * a.split.splits,
+  const dim3 grid((unsigned)(a.parts > 0 ? a.parts : a.B),
                   (unsigned)(pg.kv_heads * ((a.group + kKvHeadTile - 1) / kKvHeadTile)));
   hipLaunchKernelGGL((k_kv_attention<CT, QBF, NK, EXACT>), grid, dim3(64 * kWaves), 0, s, a, pg);
   return hipGetLastError();
@@ -501,23 +629,14 @@ hipError_t pick(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
 
 }  // namespace
 
-int kv_attention_most_splits(int64_t B, int64_t head_groups, int64_t max_len) {
-  const int64_t base = B * head_groups;
-  int64_t splits = base > 0 ? (kPieces + base - 1) / base : 1;
-  const int64_t most = (max_len + kMinTokens - 1) / kMinTokens;
-  if (splits > most) splits = most;
-  return (int)(splits < 1 ? 1 : splits);
-}
-
-KvSplit kv_attention_split(int64_t B, int64_t head_groups, int64_t max_len, int64_t window) {
-  // a window begins anywhere in the 64 tokens that the first piece is aligned to
-  if (window > 0 && window + kSplitAlign - 1 < max_len) max_len = window + kSplitAlign - 1;
-  const int64_t splits = kv_attention_most_splits(B, head_groups, max_len);
-  int64_t tokens = (max_len + splits - 1) / splits;
-  tokens = (tokens + kSplitAlign - 1) / kSplitAlign * kSplitAlign;
-  if (tokens < kSplitAlign) tokens = kSplitAlign;
-  const int64_t n = (max_len + tokens - 1) / tokens;
-  return KvSplit{(int)(n < 1 ? 1 : n), (int)tokens};
+int kv_attention_parts(int64_t B, int64_t head_groups, int64_t max_len, int64_t window) {
+  // a window begins anywhere in the 64 tokens that a sequence's first unit is aligned to
+  if (window > 0 && window + kAlign - 1 < max_len) max_len = window + kAlign - 1;
+  if (max_len <= kWhole) return 0;
+  const int64_t most = B * ((max_len + 127) / 128);
+  int64_t parts = (kMaxParts + head_groups - 1) / head_groups;
+  if (parts > most) parts = most;
+  return (int)parts;
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm_kv& kv,
@@ -544,12 +663,15 @@ hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm
     e = pick<kBF16, true>(a, pg, s);
   else
     e = bf16 ? pick<kI8, true>(a, pg, s) : pick<kI8, false>(a, pg, s);
-  if (e != hipSuccess || a.split.splits == 1) return e;
+  if (e != hipSuccess || a.parts == 0) return e;
+  const int unit = kWaves * (kv.dtype == INT8MM_I8 ? 64 : 32);
   const dim3 grid((unsigned)((int64_t)a.B * a.q_heads)), block(kJoinThreads);
   if (bf16)
-    hipLaunchKernelGGL(k_kv_join<true>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D);
+    hipLaunchKernelGGL(k_kv_join<true>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D,
+                       unit);
   else
-    hipLaunchKernelGGL(k_kv_join<false>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D);
+    hipLaunchKernelGGL(k_kv_join<false>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D,
+                       unit);
   return hipGetLastError();
 }
 

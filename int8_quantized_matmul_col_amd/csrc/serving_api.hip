@@ -76,13 +76,18 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 struct AttentionSizes {
   size_t part_ml = 0, total = 0;
 };
-AttentionSizes attention_sizes(int64_t B, int64_t q_heads, int64_t D, int splits) {
+AttentionSizes attention_sizes(int64_t groups, int64_t tile_heads, int64_t D, int parts) {
   AttentionSizes z;
-  if (splits > 1) {
-    z.part_ml = align_up((size_t)B * q_heads * splits * D * 4);
-    z.total = z.part_ml + align_up((size_t)B * q_heads * splits * 2 * 4);
+  if (parts > 0) {
+    const size_t n = (size_t)groups * parts * 2 * tile_heads;
+    z.part_ml = align_up(n * D * 4);
+    z.total = z.part_ml + align_up(n * 2 * 4);
   }
   return z;
+}
+int64_t tile_heads(int64_t q_heads, int64_t kv_heads) {
+  const int64_t group = q_heads / kv_heads;
+  return group < i8mm::kKvHeadTile ? group : i8mm::kKvHeadTile;
 }
 int64_t head_groups(int64_t q_heads, int64_t kv_heads) {
   const int64_t group = q_heads / kv_heads;
@@ -199,8 +204,9 @@ INT8MM_API size_t kv_attention_workspace_size(int64_t B, int64_t q_heads, int64_
       q_heads > 65536 || head_dim < 16 || head_dim > INT8MM_KV_MAX_HEAD_DIM || max_len < 0 ||
       max_len >= ((int64_t)1 << 31))
     return 0;
-  const int splits = i8mm::kv_attention_most_splits(B, head_groups(q_heads, kv_heads), max_len);
-  return attention_sizes(B, q_heads, head_dim, splits).total;
+  const int64_t groups = head_groups(q_heads, kv_heads);
+  return attention_sizes(groups, tile_heads(q_heads, kv_heads), head_dim,
+                         i8mm::kv_attention_parts(B, groups, max_len, 0)).total;
 }
 
 INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads,
@@ -226,11 +232,14 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   // what a sequence can show at most, which the split goes by
   int64_t most = table_width * kv->page_size;
   if (most > max_len) most = max_len;
+  // units of 128 tokens are counted in 32 bits
+  if (B * (most / 128 + 2) > kMaxCount) return INT8MM_ESHAPE;
   const int64_t groups = head_groups(q_heads, kv->kv_heads);
   i8mm::KvAttentionArgs a{};
-  a.split = i8mm::kv_attention_split(B, groups, most, window);
-  if (B * a.split.splits > kMaxCount || groups > 65535) return INT8MM_ESHAPE;
-  const AttentionSizes z = attention_sizes(B, q_heads, kv->head_dim, a.split.splits);
+  if (groups > 65535) return INT8MM_ESHAPE;
+  a.parts = i8mm::kv_attention_parts(B, groups, most, window);
+  a.tile_heads = (int)tile_heads(q_heads, kv->kv_heads);
+  const AttentionSizes z = attention_sizes(groups, a.tile_heads, kv->head_dim, a.parts);
   if (!workspace_ok(workspace, workspace_bytes, z.total)) return INT8MM_EWORKSPACE;
   a.q = static_cast<const uint16_t*>(q);
   a.q_batch_stride = q_batch_stride;

@@ -43,17 +43,10 @@ hipError_t launch_kv_gather(uint16_t* k, uint16_t* v, bool bf16, int T, const in
                             const int32_t* table, int table_rows, int table_width,
                             const int32_t* rows, const int32_t* positions, hipStream_t s);
 
-// How kv_attention splits its work: `splits` pieces of `tokens` tokens for
-// every (sequence, group of up to 16 query heads); one piece writes the
-// result itself, more are joined.
-struct KvSplit {
-  int splits;
-  int tokens;
-};
-// max_len, window: bounds of what one sequence shows.  most_splits is an upper
-// bound of `splits` over every window.
-KvSplit kv_attention_split(int64_t B, int64_t head_groups, int64_t max_len, int64_t window);
-int kv_attention_most_splits(int64_t B, int64_t head_groups, int64_t max_len);
+// Workgroups that share the batch's tokens evenly for every group of up to 16
+// query heads (a second kernel joins sequences that were cut); 0: one
+// workgroup for each sequence.  max_len, window: bounds of what one shows.
+int kv_attention_parts(int64_t B, int64_t head_groups, int64_t max_len, int64_t window);
 // Query heads of one kv head that one wave's matrix tile holds.
 constexpr int kKvHeadTile = 16;
 
@@ -65,12 +58,13 @@ struct KvAttentionArgs {
   const int32_t* rows;
   uint16_t* out;
   float* lse;
-  float* part_o;   // [B][q_heads][splits][head_dim], splits > 1
-  float* part_ml;  // [B][q_heads][splits][2]
+  float* part_o;   // [head groups][parts][2][tile_heads][head_dim]
+  float* part_ml;  // [head groups][parts][2][tile_heads][2]
   int B, q_heads, group, table_rows, table_width, max_len;  // group: query heads per kv head
   float scale, softcap;
   int64_t window;
-  KvSplit split;
+  int parts;       // kv_attention_parts
+  int tile_heads;  // min(group, kKvHeadTile)
 };
 hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm_kv& kv,
                                hipStream_t s);
