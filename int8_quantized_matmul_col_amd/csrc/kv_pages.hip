@@ -286,7 +286,8 @@ Copier copier_of(const int8mm_kv& kv) {
   return c;
 }
 
-// Slice `at` (0 .. layers * slices[3] - 1) of page src to page dst, by one workgroup.
+// Slice `at` (0 .. layers * slices[3] - 1) of page src to page dst, by one
+// workgroup; at, src and dst are the same for all its threads.
 __device__ __forceinline__ void copy_slice(const Copier& c, int at, int src, int dst) {
   const int layer = at / c.slices[3];
   const int sl = at % c.slices[3];
@@ -303,20 +304,23 @@ __device__ __forceinline__ void copy_slice(const Copier& c, int at, int src, int
       size = min(kSlice, c.bytes[i] - from);
     }
   }
-  const v4u* a = reinterpret_cast<const v4u*>(base + src * page_stride);
-  v4u* b = reinterpret_cast<v4u*>(base + dst * page_stride);
-  const int units = size / 16;
-  constexpr int kU = kSlice / 16 / kThreads;  // 8 loads in flight
-  v4u x[kU];
+  const uint8_t* a = base + src * page_stride;
+  uint8_t* b = base + dst * page_stride;
+  constexpr uint32_t kStep = kThreads * 16;
+  constexpr int kU = kSlice / kStep;  // 8 loads in flight
+  const uint32_t e = threadIdx.x * 16u;
+  if (size == kSlice) {  // (with a condition on each load they would wait for one another)
+    v4u x[kU];
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int e = threadIdx.x + u * kThreads;
-    if (e < units) x[u] = a[e];
-  }
+    for (int u = 0; u < kU; ++u)
+      x[u] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(a + (e + u * kStep)));
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int e = threadIdx.x + u * kThreads;
-    if (e < units) b[e] = x[u];
+    for (int u = 0; u < kU; ++u)
+      __builtin_nontemporal_store(x[u], reinterpret_cast<v4u*>(b + (e + u * kStep)));
+  } else {
+    for (uint32_t i = e; i < (uint32_t)size; i += kStep)
+      __builtin_nontemporal_store(__builtin_nontemporal_load(reinterpret_cast<const v4u*>(a + i)),
+                                  reinterpret_cast<v4u*>(b + i));
   }
 }
 
@@ -327,9 +331,10 @@ __global__ __launch_bounds__(kThreads) void k_pages_copy(Copier c, const int32_t
   const int64_t total = (int64_t)n * per;
 #pragma unroll 1
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-    const int a = src[w / per], b = dst[w / per];
+    const int64_t k = w / per;
+    const int a = __builtin_amdgcn_readfirstlane(src[k]), b = __builtin_amdgcn_readfirstlane(dst[k]);
     if ((unsigned)a < (unsigned)num_pages && (unsigned)b < (unsigned)num_pages && a != b)
-      copy_slice(c, (int)(w % per), a, b);
+      copy_slice(c, (int)(w - k * per), a, b);
   }
 }
 
@@ -369,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_fork(Rows r, Snapshot s, int
     if (first >= pre[blocks])
       st = INT8MM_KV_NO_PAGES;
     else
-      fresh = select_page<true>(s, pre, blocks, first);
+      fresh = __builtin_amdgcn_readfirstlane(select_page<true>(s, pre, blocks, first));
   }
   if (sl == 0 && threadIdx.x == 0) r.status[i] = st;
   if (st != INT8MM_KV_DONE) return;
@@ -393,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_fork(Rows r, Snapshot s, int
       r.lengths[child] = len;
     }
   }
-  if (fresh >= 0) copy_slice(c, sl, from[whole], fresh);
+  if (fresh >= 0) copy_slice(c, sl, __builtin_amdgcn_readfirstlane(from[whole]), fresh);
 }
 
 __global__ __launch_bounds__(kThreads) void k_pages_free(Rows r) {
@@ -426,11 +431,20 @@ __global__ __launch_bounds__(kThreads) void k_pages_compact(
   // pages
   const int per = c.layers * c.slices[3];
   const int64_t total = (int64_t)holes * per;
+  // each workgroup takes slices that follow one another: few pairs to find
+  const int64_t each = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t w1 = min(total, (blockIdx.x + 1) * each);
+  int64_t pair = -1;
+  int src = 0, dst = 0;
 #pragma unroll 1
-  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-    const uint32_t k = (uint32_t)(w / per);
-    copy_slice(c, (int)(w % per), select_page<false>(s, pre, blocks, stay + k),
-               select_page<true>(s, pre, blocks, k));
+  for (int64_t w = blockIdx.x * each; w < w1; ++w) {
+    const int64_t k = w / per;
+    if (k != pair) {
+      pair = k;
+      src = __builtin_amdgcn_readfirstlane(select_page<false>(s, pre, blocks, stay + (uint32_t)k));
+      dst = __builtin_amdgcn_readfirstlane(select_page<true>(s, pre, blocks, (uint32_t)k));
+    }
+    copy_slice(c, (int)(w - k * per), src, dst);
   }
 
   const int64_t step = (int64_t)gridDim.x * kThreads;
