@@ -138,6 +138,12 @@ __device__ void plan_rows(const Rows& r, const Snapshot& s, uint32_t* part, int3
     }
     bool ok = (unsigned)own < (unsigned)r.table_rows;
     if (FORK) ok = ok && (unsigned)parent < (unsigned)r.table_rows;
+    // what decides, requested before the names are compared
+    const int own_len = ok ? r.lengths[own] : 0;
+    const int len = FORK ? (ok ? r.lengths[parent] : 0) : own_len;
+    const int want = !FORK && ok ? r.b[i] : 0;
+    int page = -1;
+    if (FORK && ok && len >= 0 && len < room) page = r.table[(int64_t)parent * r.table_width + (len >> r.lps)];
     for (int j0 = 0; j0 < r.n; j0 += kScanThreads) {
       __syncthreads();
       if (j0 + (int)threadIdx.x < r.n) names[threadIdx.x] = named[j0 + threadIdx.x];
@@ -150,15 +156,12 @@ __device__ void plan_rows(const Rows& r, const Snapshot& s, uint32_t* part, int3
     }
     uint32_t need = 0;
     if (ok && FORK) {
-      const int len = r.lengths[parent];
-      ok = r.lengths[own] == 0 && len >= 0 && len <= room;
+      ok = own_len == 0 && len >= 0 && len <= room;
       if (ok && (len & (ps - 1)) != 0) {
         need = 1;
-        const int page = r.table[(int64_t)parent * r.table_width + (len >> r.lps)];
         ok = (unsigned)page < (unsigned)r.num_pages;
       }
     } else if (ok) {
-      const int len = r.lengths[own], want = r.b[i];
       ok = len >= 0 && want >= len && want <= room;
       // (len + ps - 1) may pass 2^31 near the largest length
       if (ok) need = (uint32_t)((((int64_t)want + ps - 1) >> r.lps) - (((int64_t)len + ps - 1) >> r.lps));
