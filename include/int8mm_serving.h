@@ -84,9 +84,9 @@ INT8MM_API int int4_pack_weight(const uint8_t* codes, int64_t N, int64_t K, int6
 INT8MM_API int int4_prepare_weight(const void* W, int dtype, int64_t N, int64_t K, int64_t group,
                                    int zeros, void* Wq, void* params, hipStream_t stream);
 
-/* Bytes of workspace int4_linear needs (256-byte aligned) for more than 16
- * rows, or for rows that are not 16-byte aligned or not a multiple of 8 long;
- * other calls may pass NULL. */
+/* Bytes of workspace int4_linear needs (256-byte aligned; 0: none) for more
+ * than 16 rows, or for rows that are not 16-byte aligned or not a multiple of
+ * 8 long; other calls may pass NULL. */
 INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N);
 
 /*

@@ -82,135 +82,124 @@ __device__ __forceinline__ v4u codes8(uint32_t u, uint32_t bias, const Nibbles& 
 
 constexpr int kCus = 256;  // compute units of the MI355X
 
-// Waves that share one group of tiles: as many as the registers and 64 KiB
-// for their sums allow.
-constexpr int max_waves(int P, int MT) { return P * MT == 1 ? 16 : P * MT <= 8 ? 8 : 4; }
-
-// One workgroup: P tiles of 16 channels, up to 16*MT rows, its waves splitting
-// K tile by tile.  GS: 32-k steps per parameter entry.
-// ARR: X is in operand order (see k_int4_arrange); otherwise rows of X, 16-byte
-// aligned and K a multiple of 8 (one tile of rows only).
-//
-// X is the A operand and W the B operand, so that a lane's codes and its sums
-// belong to the same channel (lane % 16) and one parameter entry serves both.
-template <bool BF16, bool ZEROS, int GS, int P, int MT, bool ARR>
-__global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
-    const uint16_t* __restrict__ X, int M, int K, int64_t ldx, const uint8_t* __restrict__ Wq,
-    const uint16_t* __restrict__ params, int N, const uint16_t* __restrict__ bias,
-    uint16_t* __restrict__ Y) {
-  constexpr int NG = 4 / GS;  // parameter entries per tile and channel
-  constexpr int PB = NG * (ZEROS ? 4 : 2);  // their bytes
+// What both kernels do with one parameter entry and one dword of codes.
+template <bool BF16, bool ZEROS, int GS>
+struct Group {
+  static constexpr int NG = 4 / GS;                    // entries per tile and channel
+  static constexpr int PB = NG * (ZEROS ? 4 : 2);      // their bytes
   using Par = typename std::conditional<PB == 16, v4u, typename std::conditional<PB == 8, v2u,
               typename std::conditional<PB == 4, uint32_t, uint16_t>::type>::type>::type;
-  extern __shared__ float red[];  // [waves][P][MT][4][64]
-
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, qd = lane >> 4;
-  const int nt = (K + kInt4TileK - 1) / kInt4TileK;
-  const int panel0 = blockIdx.x * P;
-  const int m0 = blockIdx.y * (16 * MT);
-  const int rows = min(M - m0, 16 * MT);
-
-  const uint16_t* xp = ARR ? X + (int64_t)blockIdx.y * nt * (MT * 4 * 512)
-                           : X;
-  const int64_t xl = ARR ? lane * 8 : (int64_t)min(r, rows - 1) * ldx + qd * 8;
-  // the last workgroup may have fewer than P tiles of channels: it takes the
-  // last one again, and does not store it
-  const int panels = (N + 15) / 16;
-  int64_t first[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) first[p] = (int64_t)min(panel0 + p, panels - 1) * nt;
-  const uint8_t* pp = reinterpret_cast<const uint8_t*>(params);
-
-  const Nibbles nib = nibbles<BF16>();
-
-  v4u w[2][P], x[MT][4];
-  Par par[2][P];
-  auto load_w = [&](int st, int t) __attribute__((always_inline)) {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int64_t tile = first[p] + t;
-      w[st][p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(Wq + tile * kInt4TileBytes) + lane);
-      par[st][p] = reinterpret_cast<const Par*>(pp + tile * (16 * PB))[r];
-    }
-  };
-  auto load_x = [&](int t, int m, int s) __attribute__((always_inline)) {
-    x[m][s] = *reinterpret_cast<const v4u*>(
-        xp + (ARR ? (((int64_t)t * MT + m) * 4 + s) * 512 : (int64_t)t * kInt4TileK + s * 32) + xl);
-  };
-  // 16-bit word i of the entries (a scale, and with zero points 1024 + z), twice
-  auto word2 = [](const Par& e, int i) __attribute__((always_inline)) {
+  // 16-bit word i of the entries, twice
+  static __device__ __forceinline__ uint32_t word2(const Par& e, int i) {
     uint32_t u;
     if constexpr (PB <= 4)
       u = e;
     else
       u = e[i >> 1];
     return __builtin_amdgcn_perm(u, u, (i & 1) ? 0x03020302u : 0x01000100u);
+  }
+  // entry g's scale; 1024 + z twice (float16 operands); 128 + z (bfloat16 sums)
+  static __device__ __forceinline__ float scale(const Par& e, int g) {
+    return h2f((uint16_t)word2(e, ZEROS ? 2 * g : g));
+  }
+  static __device__ __forceinline__ uint32_t bias(const Par& e, int g) {
+    return ZEROS && !BF16 ? word2(e, 2 * g + 1) : 0x64086408u;
+  }
+  static __device__ __forceinline__ float offset(const Par& e, int g) {
+    return ZEROS ? h2f((uint16_t)word2(e, 2 * g + 1)) - 896.0f : 136.0f;
+  }
+};
+constexpr uint32_t kOnesBf16 = 0x3f803f80u;
+
+// ------------------------------------------------------ up to 16 rows
+//
+// One workgroup: P tiles of 16 channels, its waves splitting K tile by tile.
+// GS: 32-k steps per parameter entry.  Rows 16-byte aligned, K a multiple of 8.
+//
+// X is the A operand and W the B operand, so that a lane's codes and its sums
+// belong to the same channel (lane % 16) and one parameter entry serves both.
+constexpr int max_waves(int P) { return P == 1 ? 16 : 8; }
+
+template <bool BF16, bool ZEROS, int GS, int P>
+__global__ __launch_bounds__(64 * max_waves(P)) void k_int4_few(
+    const uint16_t* __restrict__ X, int M, int K, int64_t ldx, const uint8_t* __restrict__ Wq,
+    const uint8_t* __restrict__ params, int N, const uint16_t* __restrict__ bias,
+    uint16_t* __restrict__ Y) {
+  using G = Group<BF16, ZEROS, GS>;
+  extern __shared__ float red[];  // [waves][P][4][64]
+
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, qd = lane >> 4;
+  const int nt = (K + kInt4TileK - 1) / kInt4TileK;
+  const int panel0 = blockIdx.x * P;
+  const int64_t xl = (int64_t)min(r, M - 1) * ldx + qd * 8;
+
+  // the last workgroup may have fewer than P tiles of channels: it takes the
+  // last one again, and does not store it
+  const int panels = (N + 15) / 16;
+  int64_t first[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) first[p] = (int64_t)min(panel0 + p, panels - 1) * nt;
+  const Nibbles nib = nibbles<BF16>();
+
+  v4u w[2][P], x[4];
+  typename G::Par par[2][P];
+  auto load_w = [&](int st, int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int64_t tile = first[p] + t;
+      w[st][p] = __builtin_nontemporal_load(
+          reinterpret_cast<const v4u*>(Wq + tile * kInt4TileBytes) + lane);
+      par[st][p] = reinterpret_cast<const typename G::Par*>(params + tile * (16 * G::PB))[r];
+    }
+  };
+  auto load_x = [&](int t, int s) __attribute__((always_inline)) {
+    x[s] = *reinterpret_cast<const v4u*>(X + t * kInt4TileK + s * 32 + xl);
   };
 
-  v4f tot[P][MT];
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) tot[p][m] = v4f{0, 0, 0, 0};
+  const int whole = K / kInt4TileK, last = whole - 1;
 
-  // tile of stage st; a step's X registers take tile tn's as soon as the step
+  v4f tot[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) tot[p] = v4f{0, 0, 0, 0};
+
+  // tile t of stage st; a step's X registers take tile tn's as soon as the step
   // is done (tn < 0: none)
   auto compute = [&](int st, int tn) __attribute__((always_inline)) {
-    constexpr uint32_t one = 0x3f803f80u;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
+    for (int g = 0; g < G::NG; ++g) {
       __builtin_amdgcn_sched_barrier(0);
-      v4f acc[P][MT], sx[MT];
+      v4f acc[P], sx = {0, 0, 0, 0};
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        sx[m] = v4f{0, 0, 0, 0};
-#pragma unroll
-        for (int p = 0; p < P; ++p) acc[p][m] = v4f{0, 0, 0, 0};
-      }
+      for (int p = 0; p < P; ++p) acc[p] = v4f{0, 0, 0, 0};
 #pragma unroll
       for (int s = g * GS; s < (g + 1) * GS; ++s) {
-        if constexpr (BF16)
+        if constexpr (BF16) sx = mfma32<true>(x[s], v4u{kOnesBf16, kOnesBf16, kOnesBf16, kOnesBf16}, sx);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) sx[m] = mfma32<true>(x[m][s], v4u{one, one, one, one}, sx[m]);
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const uint32_t z = ZEROS && !BF16 ? word2(par[st][p], 2 * g + 1) : 0x64086408u;
-          const v4u b = codes8<BF16>(w[st][p][s], z, nib);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[p][m] = mfma32<BF16>(x[m][s], b, acc[p][m]);
-        }
-        if (tn >= 0)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) load_x(tn, m, s);
+        for (int p = 0; p < P; ++p)
+          acc[p] = mfma32<BF16>(x[s], codes8<BF16>(w[st][p][s], G::bias(par[st][p], g), nib), acc[p]);
+        if (tn >= 0) load_x(tn, s);
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        const float sc = h2f((uint16_t)word2(par[st][p], ZEROS ? 2 * g : g));
-        const float off = ZEROS ? h2f((uint16_t)word2(par[st][p], 2 * g + 1)) - 896.0f : 136.0f;  // 128 + z
+        const float sc = G::scale(par[st][p], g), off = G::offset(par[st][p], g);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = acc[p][m][i];
-            if constexpr (BF16) v = __builtin_fmaf(-off, sx[m][i], v);
-            tot[p][m][i] = __builtin_fmaf(sc, v, tot[p][m][i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          float v = acc[p][i];
+          if constexpr (BF16) v = __builtin_fmaf(-off, sx[i], v);
+          tot[p][i] = __builtin_fmaf(sc, v, tot[p][i]);
+        }
       }
     }
   };
 
   // whole tiles: while one is multiplied, the next one's loads are in flight
-  const int whole = ARR ? nt : K / kInt4TileK;
-  const int last = whole - 1;
   if (wave < whole) {
     load_w(0, wave);
     load_w(1, min(wave + waves, last));
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) load_x(wave, m, s);
+    for (int s = 0; s < 4; ++s) load_x(wave, s);
     for (int t = wave; t < whole; t += 2 * waves) {
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
@@ -223,12 +212,12 @@ __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
     }
   }
   // the last tile of a K that is not a multiple of 128
-  if (!ARR && whole < nt && wave == whole % waves) {
+  if (whole < nt && wave == whole % waves) {
     load_w(0, whole);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      x[0][s] = v4u{0, 0, 0, 0};
-      if (whole * kInt4TileK + s * 32 + qd * 8 < K) load_x(whole, 0, s);
+      x[s] = v4u{0, 0, 0, 0};
+      if (whole * kInt4TileK + s * 32 + qd * 8 < K) load_x(whole, s);
     }
     compute(0, -1);
   }
@@ -237,54 +226,227 @@ __global__ __launch_bounds__(64 * max_waves(P, MT)) void k_int4_linear(
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[(((wave * P + p) * MT + m) * 4 + i) * 64 + lane] = tot[p][m][i];
+    for (int i = 0; i < 4; ++i) red[((wave * P + p) * 4 + i) * 64 + lane] = tot[p][i];
   __syncthreads();
-  for (int o = threadIdx.x; o < rows * 16 * P; o += blockDim.x) {
+  for (int o = threadIdx.x; o < M * 16 * P; o += blockDim.x) {
     const int nl = o % (16 * P), m = o / (16 * P);
     const int n = panel0 * 16 + nl;
     if (n >= N) continue;
-    const int at = (((nl >> 4) * MT + (m >> 4)) * 4 + (m & 3)) * 64 + ((m & 15) >> 2) * 16 + (nl & 15);
+    const int at = ((nl >> 4) * 4 + (m & 3)) * 64 + (m >> 2) * 16 + (nl & 15);
     float y = 0.0f;
-    for (int w = 0; w < waves; ++w) y += red[w * P * MT * 256 + at];
+    for (int w = 0; w < waves; ++w) y += red[w * P * 256 + at];
     if (bias != nullptr) y += BF16 ? bf2f(bias[n]) : h2f(bias[n]);
-    Y[(int64_t)(m0 + m) * N + n] = BF16 ? f2bf(y) : f2h(y);
+    Y[(int64_t)m * N + n] = BF16 ? f2bf(y) : f2h(y);
   }
 }
 
-// X in operand order: per 64 rows (16 * MT), k tile, 16 rows and 32 k the 64
-// lanes' 8 elements (lane l: row l % 16, k 8 * (l / 16) ..), zeros past M and K.
-// One KiB a load then comes from one place.  Rows of a usual X lie a power of
-// two apart, 16 of them in one channel of the L2, and every workgroup reads
-// them: 64 x 8192 x 13824 took 50.7 us from the rows, 26.4 us in this order.
-__global__ __launch_bounds__(256) void k_int4_arrange(const uint16_t* __restrict__ X, int M, int K,
-                                                      int64_t ldx, int MT, int64_t nt, int vec,
-                                                      int64_t total, uint16_t* __restrict__ A) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int l = (int)(i & 63), s = (int)(i >> 6) & 3;
-    const int64_t f = i >> 8;  // (chunk, tile, 16 rows)
-    const int m = (int)(f % MT);
-    const int64_t t = f / MT % nt, chunk = f / MT / nt;
-    const int64_t row = chunk * 16 * MT + m * 16 + (l & 15);
-    const int64_t k = t * kInt4TileK + s * 32 + (l >> 4) * 8;
-    v4u x = {0, 0, 0, 0};
-    if (row < M) {
-      const uint16_t* p = X + row * ldx + k;
-      if (vec && k + 8 <= K) {
-        x = *reinterpret_cast<const v4u*>(p);
+// ------------------------------------------- more rows, or any alignment
+//
+// 8 waves share X: 4 groups of P channel tiles times the 2 tiles of K of a
+// step.  A step's X, up to 64 rows of 512 contiguous bytes, goes through
+// registers into LDS in operand order, the next step's while this one is
+// multiplied; a chunk's place is exclusive-ored with its k so that neither side
+// has bank conflicts.  Rows past M and k past K are zeros there, so every shape
+// and alignment takes this one path.  Where few channels leave CUs idle K is
+// split over workgroups too (blockIdx.z), and a second kernel adds their sums.
+//
+// 64 x 8192 x 28672 takes 53 us, of which 28 are the matrix instructions and
+// the groups' scales alone (1.1 of the 1.2 PFLOP/s that a large library product
+// reaches here), 10 the codes and LDS, the rest the loads; 48 x 5120 x 13811 25
+// us, 64 x 4096 x 11008 20.
+constexpr int kManyWaves = 8;
+constexpr int kStages = 3;  // weights in flight: two steps ahead
+
+template <bool BF16, bool ZEROS, int GS, int MT, int P>
+__global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
+    const uint16_t* __restrict__ X, int M, int K, int64_t ldx, int vec,
+    const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ params, int N,
+    const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y, float* __restrict__ part) {
+  using G = Group<BF16, ZEROS, GS>;
+  constexpr int kChunk = MT * 2 * 4 * 64;  // 16-byte units of one step's X
+  constexpr int kSums = kManyWaves * P * MT * 256 * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kChunk * 16 > kSums ? 2 * kChunk * 16 : kSums];
+  v4u* xs = reinterpret_cast<v4u*>(lds);        // [2][tile][MT][step][64]
+  float* red = reinterpret_cast<float*>(lds);   // [wave][P][MT][4][64]
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, qd = lane >> 4;
+  const int pg = wave & 3, ks = wave >> 2;
+  const int nt = (K + kInt4TileK - 1) / kInt4TileK, pairs = (nt + 1) / 2;
+  // this workgroup's steps
+  const int step0 = (int)((int64_t)blockIdx.z * pairs / gridDim.z);
+  const int step1 = (int)((int64_t)(blockIdx.z + 1) * pairs / gridDim.z);
+  const int m0 = blockIdx.y * (16 * MT);
+  const int panels = (N + 15) / 16, panel0 = blockIdx.x * (4 * P) + pg * P;
+  int64_t first[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) first[p] = (int64_t)min(panel0 + p, panels - 1) * nt;
+  const Nibbles nib = nibbles<BF16>();
+
+  // staging: this thread's chunk of 8 k in rows row0 + 16 i
+  const int c = threadIdx.x & 31, row0 = threadIdx.x >> 5;
+  v4u hold[MT];
+  auto fetch = [&](int step) __attribute__((always_inline)) {
+    const int k = step * 256 + c * 8;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = m0 + row0 + 16 * i;
+      hold[i] = v4u{0, 0, 0, 0};
+      if (m >= M || k >= K) continue;
+      const uint16_t* p = X + (int64_t)m * ldx + k;
+      if (vec) {
+        hold[i] = *reinterpret_cast<const v4u*>(p);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t a = k + 2 * e < K ? p[2 * e] : 0u;
           const uint32_t b = k + 2 * e + 1 < K ? p[2 * e + 1] : 0u;
-          x[e] = a | (b << 16);
+          hold[i][e] = a | (b << 16);
         }
       }
     }
-    *reinterpret_cast<v4u*>(A + i * 8) = x;
+  };
+  auto stage = [&](int buf) __attribute__((always_inline)) {
+    const int t = c >> 4, sq = c & 15;  // tile of the step, (32-k step, quarter)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      xs[buf * kChunk + ((t * MT + i) * 4 + (sq >> 2)) * 64 + (sq & 3) * 16 + (row0 ^ sq)] = hold[i];
+  };
+
+  v4u w[kStages][P];
+  typename G::Par par[kStages][P];
+  auto load_w = [&](int st, int step) __attribute__((always_inline)) {
+    const int t = min(step * 2 + ks, nt - 1);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int64_t tile = first[p] + t;
+      w[st][p] = __builtin_nontemporal_load(
+          reinterpret_cast<const v4u*>(Wq + tile * kInt4TileBytes) + lane);
+      par[st][p] = reinterpret_cast<const typename G::Par*>(params + tile * (16 * G::PB))[r];
+    }
+  };
+
+  v4f tot[P][MT];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) tot[p][m] = v4f{0, 0, 0, 0};
+
+  auto compute = [&](int st, int buf) __attribute__((always_inline)) {
+    const v4u* xb = xs + buf * kChunk + ks * MT * 256;
+#pragma unroll
+    for (int g = 0; g < G::NG; ++g) {
+      __builtin_amdgcn_sched_barrier(0);
+      v4f acc[P][MT], sx[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        sx[m] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < P; ++p) acc[p][m] = v4f{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int s = g * GS; s < (g + 1) * GS; ++s) {
+        v4u x[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) x[m] = xb[(m * 4 + s) * 64 + qd * 16 + (r ^ (s * 4 + qd))];
+        if constexpr (BF16)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            sx[m] = mfma32<true>(x[m], v4u{kOnesBf16, kOnesBf16, kOnesBf16, kOnesBf16}, sx[m]);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const v4u b = codes8<BF16>(w[st][p][s], G::bias(par[st][p], g), nib);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[p][m] = mfma32<BF16>(x[m], b, acc[p][m]);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float sc = G::scale(par[st][p], g), off = G::offset(par[st][p], g);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[p][m][i];
+            if constexpr (BF16) v = __builtin_fmaf(-off, sx[m][i], v);
+            tot[p][m][i] = __builtin_fmaf(sc, v, tot[p][m][i]);
+          }
+      }
+    }
+  };
+  // LDS of this workgroup is written and read; loads into registers stay in flight
+  auto sync = [&]() __attribute__((always_inline)) {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+
+  // The second tile of the last step may lie past K: its X is zero, and the
+  // weight read in its place is finite.
+  const int last = step1 - 1;
+  if (step0 < step1) {
+    fetch(step0);
+#pragma unroll
+    for (int st = 0; st < kStages - 1; ++st) load_w(st, min(step0 + st, last));
+    stage(0);
+    sync();
+    for (int t = step0; t < step1; t += kStages) {
+#pragma unroll
+      for (int st = 0; st < kStages; ++st) {
+        if (st > 0 && t + st > last) break;
+        const int now = t + st, buf = (now - step0) & 1;
+        // X first: loads return in order, and waiting for X must not wait for
+        // the weight of two steps on
+        fetch(min(now + 1, last));
+        load_w((st + kStages - 1) % kStages, min(now + kStages - 1, last));
+        compute(st, buf);
+        stage(buf ^ 1);  // (read last a step ago, before the barrier there)
+        sync();
+      }
+    }
+  }
+
+  // the waves' partial sums: the two halves of K, in order
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[(((wave * P + p) * MT + m) * 4 + i) * 64 + lane] = tot[p][m][i];
+  __syncthreads();
+  const int rows = min(M - m0, 16 * MT);
+  constexpr int kCols = 4 * P * 16;
+  for (int o = threadIdx.x; o < rows * kCols; o += 64 * kManyWaves) {
+    const int nl = o % kCols, m = o / kCols;
+    const int n = blockIdx.x * kCols + nl;
+    if (n >= N) continue;
+    const int wv = nl / (16 * P), p = nl / 16 % P;
+    const int at = (((wv * P + p) * MT + (m >> 4)) * 4 + (m & 3)) * 64 + ((m & 15) >> 2) * 16 + (nl & 15);
+    float y = red[at] + red[at + 4 * P * MT * 256];
+    if (part != nullptr) {
+      part[((int64_t)blockIdx.z * M + m0 + m) * N + n] = y;
+    } else {
+      if (bias != nullptr) y += BF16 ? bf2f(bias[n]) : h2f(bias[n]);
+      Y[(int64_t)(m0 + m) * N + n] = BF16 ? f2bf(y) : f2h(y);
+    }
+  }
+}
+
+// Adds the parts of K, in order.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_int4_sum(const float* __restrict__ part, int parts,
+                                                  int64_t total, int N,
+                                                  const uint16_t* __restrict__ bias,
+                                                  uint16_t* __restrict__ Y) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    float y = 0.0f;
+    for (int z = 0; z < parts; ++z) y += part[z * total + i];
+    if (bias != nullptr) {
+      const uint16_t b = bias[i % N];
+      y += BF16 ? bf2f(b) : h2f(b);
+    }
+    Y[i] = BF16 ? f2bf(y) : f2h(y);
   }
 }
 
@@ -442,17 +604,14 @@ hipError_t launch_int4_prepare(const uint16_t* W, bool bf16, int64_t N, int64_t 
 
 namespace {
 
-template <bool BF16, bool ZEROS, int GS, int P, int MT, bool ARR>
-hipError_t run(const uint16_t* X, int M, int K, int64_t ldx, const void* Wq, const void* params,
-               int N, const uint16_t* bias, uint16_t* Y, hipStream_t s) {
-  const int nt = (int)int4_tiles_k(K);
-  int waves = max_waves(P, MT);
+template <bool BF16, bool ZEROS, int GS, int P>
+hipError_t run_few(const Int4Args& a, hipStream_t s) {
+  const int nt = (int)int4_tiles_k(a.K);
+  int waves = max_waves(P);
   while (waves > nt) waves /= 2;
-  const dim3 grid((unsigned)((N + 16 * P - 1) / (16 * P)), (unsigned)((M + 16 * MT - 1) / (16 * MT)));
-  const size_t lds = (size_t)waves * P * MT * 1024;
-  hipLaunchKernelGGL((k_int4_linear<BF16, ZEROS, GS, P, MT, ARR>), grid, dim3(64 * waves), lds, s, X, M,
-                     K, ldx, static_cast<const uint8_t*>(Wq), static_cast<const uint16_t*>(params),
-                     N, bias, Y);
+  hipLaunchKernelGGL((k_int4_few<BF16, ZEROS, GS, P>), dim3((a.N + 16 * P - 1) / (16 * P)),
+                     dim3(64 * waves), (size_t)waves * P * 1024, s, a.X, a.M, a.K, a.ldx, a.Wq,
+                     a.params, a.N, a.bias, a.Y);
   return hipGetLastError();
 }
 
@@ -462,88 +621,92 @@ hipError_t run(const uint16_t* X, int M, int K, int64_t ldx, const void* Wq, con
 // 256 workgroups, 27.3 with 4, 32 with 1; 1 x 11008 x 4096: 9.7 us with 1, 17.1
 // with 4).
 template <bool BF16, bool ZEROS, int GS>
-hipError_t pick_tile(const uint16_t* X, bool arranged, int M, int K, int64_t ldx, const void* Wq,
-                     const void* params, int N, const uint16_t* bias, uint16_t* Y, hipStream_t s) {
-#define INT4_RUN(p, m, a) return run<BF16, ZEROS, GS, p, m, a>(X, M, K, ldx, Wq, params, N, bias, Y, s)
-  const int panels = (N + 15) / 16;
-  const int P = (panels + kCus - 1) / kCus;
-  if (!arranged) {
-    if (P <= 1) INT4_RUN(1, 1, false);
-    if (P == 2) INT4_RUN(2, 1, false);
-    if (P == 3) INT4_RUN(3, 1, false);
-    if constexpr (GS > 1) {  // 32-wide groups: no registers for more than 4
-      if (P == 5) INT4_RUN(5, 1, false);
-      if (P > 5) INT4_RUN(7, 1, false);
-    }
-    INT4_RUN(4, 1, false);
+hipError_t pick_few(const Int4Args& a, hipStream_t s) {
+  const int P = ((a.N + 15) / 16 + kCus - 1) / kCus;
+  if (P <= 1) return run_few<BF16, ZEROS, GS, 1>(a, s);
+  if (P == 2) return run_few<BF16, ZEROS, GS, 2>(a, s);
+  if (P == 3) return run_few<BF16, ZEROS, GS, 3>(a, s);
+  if constexpr (GS > 1) {  // 32-wide groups: no registers for more than 4
+    if (P == 5) return run_few<BF16, ZEROS, GS, 5>(a, s);
+    if (P > 5) return run_few<BF16, ZEROS, GS, 7>(a, s);
   }
-  const int mt = int4_row_tiles(M);
-  if (mt == 1 && P <= 2) INT4_RUN(1, 1, true);
-  if (mt == 1) INT4_RUN(4, 1, true);
-  if (P <= 1 && mt == 2) INT4_RUN(1, 2, true);
-  if (P <= 1 && mt == 3) INT4_RUN(1, 3, true);
-  if (P <= 1) INT4_RUN(1, 4, true);
-  if (P == 2 || GS == 1) {
-    if (mt == 2) INT4_RUN(2, 2, true);
-    if (mt == 3) INT4_RUN(2, 3, true);
-    INT4_RUN(2, 4, true);
-  }
-  if constexpr (GS > 1) {
-    if (mt == 2) INT4_RUN(4, 2, true);
-    if (mt == 3) INT4_RUN(4, 3, true);
-    INT4_RUN(4, 4, true);
-  }
-  return hipErrorInvalidValue;  // not reached
-#undef INT4_RUN
+  return run_few<BF16, ZEROS, GS, 4>(a, s);
+}
+
+template <bool BF16, bool ZEROS, int GS, int MT, int P>
+hipError_t run_many(const Int4Args& a, hipStream_t s) {
+  const int z = int4_k_parts(a.M, a.K, a.N);
+  const dim3 grid((a.N + 64 * P - 1) / (64 * P), (a.M + 16 * MT - 1) / (16 * MT), z);
+  const int vec = a.K % 8 == 0 && (a.ldx % 8 == 0 || a.M == 1) && (reinterpret_cast<uintptr_t>(a.X) & 15) == 0;
+  hipLaunchKernelGGL((k_int4_many<BF16, ZEROS, GS, MT, P>), grid, dim3(64 * kManyWaves), 0, s, a.X,
+                     a.M, a.K, a.ldx, vec, a.Wq, a.params, a.N, a.bias, a.Y,
+                     z > 1 ? a.part : nullptr);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || z == 1) return e;
+  const int64_t total = (int64_t)a.M * a.N;
+  hipLaunchKernelGGL((k_int4_sum<BF16>), dim3(grid_for(total, 256)), dim3(256), 0, s, a.part, z,
+                     total, a.N, a.bias, a.Y);
+  return hipGetLastError();
+}
+
+// Two channel tiles a wave halve the reads of X, but need twice the channels
+// to fill the GPU (64 x 8192 x 28672: 53 us against 60 with one; 64 x 4096 x
+// 11008: 26.5 against 20.3).
+template <bool BF16, bool ZEROS, int GS, int MT>
+hipError_t pick_many(const Int4Args& a, hipStream_t s) {
+  if constexpr (MT > 1)
+    if (a.N >= 128 * 200) return run_many<BF16, ZEROS, GS, MT, 2>(a, s);
+  return run_many<BF16, ZEROS, GS, MT, 1>(a, s);
+}
+
+template <bool BF16, bool ZEROS, int GS>
+hipError_t pick(const Int4Args& a, bool few, hipStream_t s) {
+  if (few) return pick_few<BF16, ZEROS, GS>(a, s);
+  if (a.M <= 16) return pick_many<BF16, ZEROS, GS, 1>(a, s);
+  if (a.M <= 32) return pick_many<BF16, ZEROS, GS, 2>(a, s);
+  if (a.M <= 48) return pick_many<BF16, ZEROS, GS, 3>(a, s);
+  return pick_many<BF16, ZEROS, GS, 4>(a, s);
 }
 
 template <bool BF16, bool ZEROS>
-hipError_t pick_group(const uint16_t* X, bool arranged, int M, int K, int64_t ldx, const void* Wq,
-                      const void* params, int N, int steps, const uint16_t* bias, uint16_t* Y,
-                      hipStream_t s) {
+hipError_t pick_group(const Int4Args& a, int steps, bool few, hipStream_t s) {
   switch (steps) {
-    case 1: return pick_tile<BF16, ZEROS, 1>(X, arranged, M, K, ldx, Wq, params, N, bias, Y, s);
-    case 2: return pick_tile<BF16, ZEROS, 2>(X, arranged, M, K, ldx, Wq, params, N, bias, Y, s);
-    default: return pick_tile<BF16, ZEROS, 4>(X, arranged, M, K, ldx, Wq, params, N, bias, Y, s);
+    case 1: return pick<BF16, ZEROS, 1>(a, few, s);
+    case 2: return pick<BF16, ZEROS, 2>(a, few, s);
+    default: return pick<BF16, ZEROS, 4>(a, few, s);
   }
 }
 
 }  // namespace
 
-bool int4_x_direct(const uint16_t* X, int64_t M, int64_t K, int64_t ldx) {
+bool int4_few_rows(const uint16_t* X, int64_t M, int64_t K, int64_t ldx) {
   return M <= 16 && K % 8 == 0 && (ldx % 8 == 0 || M == 1) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
 }
 
-size_t int4_arranged_bytes(int64_t M, int64_t K) {
-  const int64_t per = 16 * int4_row_tiles(M);
-  return (size_t)((M + per - 1) / per * per) * int4_tiles_k(K) * kInt4TileK * 2;
+// Parts of K of the kernel for many rows: up to one round of workgroups, at
+// least 10 steps each (24 x 11008 x 4096: 15.1 us in 4 parts, 30 in one; 20 x
+// 4096 x 4096: 12.2 in one, 13.6 in 2).
+int int4_k_parts(int64_t M, int64_t K, int64_t N) {
+  const int64_t groups = ((N + 63) / 64) * ((M + 63) / 64);
+  const int64_t most = int4_tiles_k(K) / 20;
+  int64_t z = groups > 0 ? kCus / groups : 1;
+  if (z > most) z = most;
+  return (int)(z < 1 ? 1 : z);
 }
 
-hipError_t launch_int4_linear(const uint16_t* X, bool bf16, int64_t M, int64_t K, int64_t ldx,
-                              const void* Wq, const void* params, int64_t N, int64_t group,
-                              bool zeros, const uint16_t* bias, uint16_t* Y, uint16_t* ws,
+hipError_t launch_int4_linear(const Int4Args& a, bool bf16, int64_t group, bool zeros,
                               hipStream_t s) {
-  if (K == 0) {
-    hipLaunchKernelGGL(k_int4_bias, dim3(grid_for(M * N, 256)), dim3(256), 0, s, bias, M * N,
-                       (int)N, Y);
+  if (a.K == 0) {
+    const int64_t total = (int64_t)a.M * a.N;
+    hipLaunchKernelGGL(k_int4_bias, dim3(grid_for(total, 256)), dim3(256), 0, s, a.bias, total, a.N,
+                       a.Y);
     return hipGetLastError();
   }
-  const bool arr = !int4_x_direct(X, M, K, ldx);
-  if (arr) {
-    const int64_t total = (int64_t)int4_arranged_bytes(M, K) / 16;
-    const int vec = (ldx % 8 == 0 || M == 1) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
-    hipLaunchKernelGGL(k_int4_arrange, dim3(grid_for(total, 256)), dim3(256), 0, s, X, (int)M,
-                       (int)K, ldx, int4_row_tiles(M), int4_tiles_k(K), vec, total, ws);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    X = ws;
-  }
-  const int steps = int4_group_steps(group), m = (int)M, k = (int)K, n = (int)N;
+  const int steps = int4_group_steps(group);
+  const bool few = int4_few_rows(a.X, a.M, a.K, a.ldx);
   if (bf16)
-    return zeros ? pick_group<true, true>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s)
-                 : pick_group<true, false>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s);
-  return zeros ? pick_group<false, true>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s)
-               : pick_group<false, false>(X, arr, m, k, ldx, Wq, params, n, steps, bias, Y, s);
+    return zeros ? pick_group<true, true>(a, steps, few, s) : pick_group<true, false>(a, steps, few, s);
+  return zeros ? pick_group<false, true>(a, steps, few, s) : pick_group<false, false>(a, steps, few, s);
 }
 
 }  // namespace i8mm

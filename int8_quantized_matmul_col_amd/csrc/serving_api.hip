@@ -135,8 +135,9 @@ INT8MM_API int int4_prepare_weight(const void* W, int dtype, int64_t N, int64_t 
 
 INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N) {
   if (!int4_shape(N, K) || M < 0 || M > kMaxCount) return 0;
-  if (M == 0 || K == 0) return 0;
-  return align_up(i8mm::int4_arranged_bytes(M, K));
+  if (M == 0 || K == 0 || N == 0) return 0;
+  const int parts = i8mm::int4_k_parts(M, K, N);
+  return parts > 1 ? align_up((size_t)parts * M * N * 4) : 0;
 }
 
 INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx,
@@ -150,14 +151,21 @@ INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64
   if (Y == nullptr || (K > 0 && (X == nullptr || Wq == nullptr || params == nullptr))) return INT8MM_EINVAL;
   if (!aligned(X, 2) || !aligned(Y, 2) || !aligned(bias, 2) || !aligned(Wq, 16) || !aligned(params, 16))
     return INT8MM_EINVAL;
-  const uint16_t* x = static_cast<const uint16_t*>(X);
-  if (K > 0 && !i8mm::int4_x_direct(x, M, K, ldx) &&
+  i8mm::Int4Args a{};
+  a.X = static_cast<const uint16_t*>(X);
+  if (K > 0 && !i8mm::int4_few_rows(a.X, M, K, ldx) &&
       !workspace_ok(workspace, workspace_bytes, int4_linear_workspace_size(M, K, N)))
     return INT8MM_EWORKSPACE;
-  return status_of(i8mm::launch_int4_linear(x, dtype == INT8MM_BF16, M, K, ldx, Wq, params, N,
-                                            group, zeros != 0, static_cast<const uint16_t*>(bias),
-                                            static_cast<uint16_t*>(Y),
-                                            static_cast<uint16_t*>(workspace), stream));
+  a.Wq = static_cast<const uint8_t*>(Wq);
+  a.params = static_cast<const uint8_t*>(params);
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.Y = static_cast<uint16_t*>(Y);
+  a.part = static_cast<float*>(workspace);
+  a.ldx = ldx;
+  a.M = (int)M;
+  a.K = (int)K;
+  a.N = (int)N;
+  return status_of(i8mm::launch_int4_linear(a, dtype == INT8MM_BF16, group, zeros != 0, stream));
 }
 
 INT8MM_API int kv_append(const void* k, const void* v, int dtype, int64_t T,

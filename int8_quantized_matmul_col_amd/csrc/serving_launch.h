@@ -12,9 +12,6 @@ namespace i8mm {
 // ---- 4-bit weights: tiles of 16 channels x 128 k, 1 KiB each
 constexpr int kInt4TileK = 128;
 constexpr int kInt4TileBytes = 1024;
-// 16-row tiles of X per pass over the weight
-inline int int4_row_tiles(int64_t M) { return M > 48 ? 4 : (int)((M + 15) / 16); }
-
 inline int64_t int4_padded_rows(int64_t N) { return (N + 15) / 16 * 16; }
 inline int64_t int4_tiles_k(int64_t K) { return (K + kInt4TileK - 1) / kInt4TileK; }
 // 32-k steps of a tile that share one parameter entry
@@ -25,14 +22,22 @@ hipError_t launch_int4_pack(const uint8_t* codes, int64_t N, int64_t K, int64_t 
                             uint16_t* params, hipStream_t s);
 hipError_t launch_int4_prepare(const uint16_t* W, bool bf16, int64_t N, int64_t K, int64_t group,
                                bool zeros, uint32_t* Wq, uint16_t* params, hipStream_t s);
-hipError_t launch_int4_linear(const uint16_t* X, bool bf16, int64_t M, int64_t K, int64_t ldx,
-                              const void* Wq, const void* params, int64_t N, int64_t group,
-                              bool zeros, const uint16_t* bias, uint16_t* Y, uint16_t* ws,
+struct Int4Args {
+  const uint16_t* X;
+  const uint8_t* Wq;
+  const uint8_t* params;
+  const uint16_t* bias;
+  uint16_t* Y;
+  float* part;  // [int4_k_parts][M][N] if that is more than one
+  int64_t ldx;
+  int M, K, N;
+};
+hipError_t launch_int4_linear(const Int4Args& a, bool bf16, int64_t group, bool zeros,
                               hipStream_t s);
-// Whether the kernel reads X as it is; otherwise X goes through ws in operand
-// order (int4_arranged_bytes).
-bool int4_x_direct(const uint16_t* X, int64_t M, int64_t K, int64_t ldx);
-size_t int4_arranged_bytes(int64_t M, int64_t K);
+// Whether the kernel for up to 16 aligned rows takes them; it needs no
+// workspace.  The other splits K into int4_k_parts.
+bool int4_few_rows(const uint16_t* X, int64_t M, int64_t K, int64_t ldx);
+int int4_k_parts(int64_t M, int64_t K, int64_t N);
 
 // ---- key-value pages
 hipError_t launch_kv_append(const uint16_t* k, const uint16_t* v, bool bf16, int T, int64_t kts,

@@ -249,9 +249,11 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
     else:
         _check_out(out, (M, N), X.dtype, "out", dev)
         Y = out
-    # up to 16 rows on 16 bytes are read as they are, others through a workspace
+    # up to 16 rows on 16 bytes need no workspace
     if workspace is None and (M > 16 or K % 8 or ldx % 8 or X.data_ptr() % 16):
-        workspace = torch.empty((int4_linear_workspace_size(M, K, N),), dtype=torch.uint8, device=dev)
+        n = _lib().int4_linear_workspace_size(M, K, N)
+        if n:
+            workspace = X.new_empty((n // 4,), dtype=torch.float32)
     _call("int4_linear", dev, X.data_ptr(), dt, M, K, ldx, w.Wq.data_ptr(), w.params.data_ptr(), N,
           w.group_size, w.zeros, None if bias is None else bias.data_ptr(), Y.data_ptr(),
           None if workspace is None else workspace.data_ptr(),

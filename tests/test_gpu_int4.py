@@ -51,6 +51,9 @@ SHAPES = [
     (31, 260, 33, 32), (32, 1000, 90, 64), (33, 136, 257, 128), (48, 320, 65, 32),
     (64, 264, 40, 384), (65, 192, 50, 64), (130, 256, 31, 128), (1, 2200, 24, 128),
     (2, 4100, 16400, 128), (16, 520, 16390, 32), (9, 2048, 100, 1024),
+    # K in parts, many channels, tiles of K that end inside a step
+    (20, 5300, 70, 64), (64, 5200, 33, 128), (3, 5251, 40, 32), (40, 140, 25700, 128),
+    (18, 250, 16, 32), (64, 383, 130, 64),
 ]
 
 
@@ -139,6 +142,30 @@ def test_infinite_input_stays_in_its_row(lib):
     w = lib.int4_pack_weight(codes, torch.ones((3, 1), dtype=torch.float16, device="cuda"), None, 64)
     Y = lib.int4_linear(X, w)
     assert torch.all(Y[0] == 64) and torch.all(Y[1] == float("inf"))
+
+
+def test_graph_and_another_stream(lib):
+    g = rng(77)
+    for M, K, N in ((1, 512, 300), (20, 5300, 70), (3, 77, 50)):
+        X, codes, scales, z = _case(g, M, K, N, 64, True, "f16")
+        w = lib.int4_pack_weight(dev(codes), dev(scales), dev(z), 64)
+        want = lib.int4_linear(X, w)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = lib.int4_linear(X, w)
+        side.synchronize()
+        assert torch.equal(got, want)
+        Y = torch.empty_like(want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lib.int4_linear(X, w, out=Y)
+        for k in range(3):
+            X.copy_(X.roll(1, 0) * 0.5)
+            Y.fill_(9)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(Y, lib.int4_linear(X, w))
 
 
 def test_empty(lib):

@@ -99,10 +99,16 @@ def test_int4_refusals(lib):
         assert _lin(lib, **{n: None}) == EINVAL
     assert _lin(lib, X=FAKE + 1) == EINVAL and _lin(lib, W=FAKE + 8) == EINVAL
     assert _lin(lib, p=FAKE + 8) == EINVAL and _lin(lib, b=FAKE + 1) == EINVAL
-    # rows that are not on 16 bytes need the workspace
-    assert _lin(lib, X=FAKE + 2) == EWORKSPACE and _lin(lib, ldx=65) == EWORKSPACE
-    assert _lin(lib, K=63, ws=FAKE + 16, nb=1 << 20) == EWORKSPACE
-    assert _lin(lib, K=63, ws=FAKE, nb=lib.int4_linear_workspace_size(2, 63, 4) - 1) == EWORKSPACE
+    # more than 16 rows on few channels and a long K need the workspace, also
+    # fewer that are not on 16 bytes
+    big = dict(K=8192, ldx=8192, N=64)
+    need = lib.int4_linear_workspace_size(20, 8192, 64)
+    assert need >= 2 * 20 * 64 * 4
+    assert _lin(lib, M=20, **big) == EWORKSPACE
+    assert _lin(lib, M=20, ws=FAKE + 16, nb=1 << 30, **big) == EWORKSPACE
+    assert _lin(lib, M=20, ws=FAKE, nb=need - 1, **big) == EWORKSPACE
+    assert _lin(lib, X=FAKE + 2, **big) == EWORKSPACE
+    assert lib.int4_linear_workspace_size(20, 1024, 64) == 0
     assert _lin(lib, M=0) == OK and _lin(lib, N=0) == OK
     assert lib.int4_pack_weight(FAKE, 4, 64, 64, FAKE, None, None, FAKE, None) == EINVAL
     assert lib.int4_pack_weight(FAKE, 4, 64, 65, FAKE, None, FAKE, FAKE, None) == ESHAPE
