@@ -90,17 +90,20 @@ def _lib() -> ctypes.CDLL:
     return _fns
 
 
-def _call(name: str, device, *args) -> None:
-    """One C call on torch's current stream of `device`, with `device` current
-    (the library launches on the current device)."""
+_device = torch._C._cuda_getDevice
+_stream_of = torch._C._cuda_getCurrentRawStream
+
+
+def _call(name: str, index: int, *args) -> None:
+    """One C call on torch's current stream of GPU `index`, with that GPU
+    current (the library launches on the current one)."""
     if _fns is None:
         _lib()
-    index = device.index
-    if torch._C._cuda_getDevice() == index:
-        st = _by_name[name](*args, torch._C._cuda_getCurrentRawStream(index))
+    if _device() == index:
+        st = _by_name[name](*args, _stream_of(index))
     else:
-        with torch.cuda.device(device):
-            st = _by_name[name](*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            st = _by_name[name](*args, _stream_of(index))
     if st:
         _check(name, st)
 
@@ -114,6 +117,9 @@ def _row_dtype(t, name: str) -> int:
 
 def _on(t, name: str, device=None) -> None:
     """A GPU tensor (of `device`); contiguity and type are the caller's checks."""
+    if t.__class__ is torch.Tensor and t.is_cuda and (device is None
+                                                      or t.get_device() == device.index):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -125,7 +131,7 @@ def _on(t, name: str, device=None) -> None:
 def _indexes(t, name: str, device, shape=None) -> None:
     """A contiguous int32 tensor of `device` (and shape)."""
     # one look at what is nearly always right; _require names what is wrong
-    if not (type(t) is torch.Tensor and t.dtype is torch.int32 and t.is_contiguous()
+    if not (t.__class__ is torch.Tensor and t.dtype is torch.int32 and t.is_contiguous()
             and t.get_device() == device.index):
         _require(t, torch.int32, name, device)
     if shape is not None and t.shape != shape:
@@ -172,7 +178,7 @@ def int4_pack_weight(codes, scales, zeros=None, group_size: int = 128) -> Int4We
         _require(t, dt, name, codes.device)
         if tuple(t.shape) != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    _call("int4_pack_weight", codes.device, codes.data_ptr(), N, K, g, scales.data_ptr(),
+    _call("int4_pack_weight", codes.device.index, codes.data_ptr(), N, K, g, scales.data_ptr(),
           None if zeros is None else zeros.data_ptr(), Wq.data_ptr(), params.data_ptr())
     return Int4Weight(Wq, params, N, K, g, zeros is not None)
 
@@ -188,7 +194,7 @@ def int4_prepare_weight(W, group_size: int = 128, symmetric: bool = True) -> Int
     N, K = W.shape
     g = int(group_size)
     Wq, params = _int4_buffers(N, K, g, not symmetric, W.device)
-    _call("int4_prepare_weight", W.device, W.data_ptr(), dt, N, K, g, int(not symmetric),
+    _call("int4_prepare_weight", W.device.index, W.data_ptr(), dt, N, K, g, int(not symmetric),
           Wq.data_ptr(), params.data_ptr())
     return Int4Weight(Wq, params, N, K, g, not symmetric)
 
@@ -254,10 +260,10 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
         n = _lib().int4_linear_workspace_size(M, K, N)
         if n:
             workspace = X.new_empty((n // 4,), dtype=torch.float32)
-    _call("int4_linear", dev, X.data_ptr(), dt, M, K, ldx, w.Wq.data_ptr(), w.params.data_ptr(), N,
+    _call("int4_linear", dev.index, X.data_ptr(), dt, M, K, ldx, w.Wq.data_ptr(), w.params.data_ptr(), N,
           w.group_size, w.zeros, None if bias is None else bias.data_ptr(), Y.data_ptr(),
           None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+          0 if workspace is None else workspace.nbytes)
     return Y
 
 
@@ -312,6 +318,9 @@ class PagedKV:
         self.layered = layered
         self.layers, self.num_pages, self.kv_heads = s.layers, pages, heads
         self.page_size, self.head_dim, self.dtype, self.device = ps, D, k.dtype, dev
+        self.index = dev.index
+        # the types of rows beside this cache
+        self._rows = dict(_DTYPES) if dt == INT8MM_I8 else {k.dtype: dt}
         self._struct = s
         self._ref = ctypes.byref(s)
 
@@ -333,14 +342,16 @@ class PagedKV:
 
     def row_dtype(self, dtype, name: str) -> int:
         """Code of the rows' type beside this cache."""
-        code = _DTYPES.get(dtype)
-        if code is None or (self.dtype != torch.int8 and dtype != self.dtype):
+        code = self._rows.get(dtype)
+        if code is None:
             want = "torch.float16 or torch.bfloat16" if self.dtype == torch.int8 else self.dtype
             raise TypeError(f"{name} must be {want}, got {dtype}")
         return code
 
 
 def _one_layer(kv: PagedKV) -> None:
+    if kv.__class__ is PagedKV and not kv.layered:
+        return
     if not isinstance(kv, PagedKV):
         raise TypeError("kv must be a PagedKV")
     if kv.layered:
@@ -368,13 +379,13 @@ def kv_append(k, v, kv: PagedKV, table, rows, positions) -> None:
     shape = (positions.numel(), kv.kv_heads, kv.head_dim)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected {shape}")
-    if k.stride(2) != 1 or v.stride(2) != 1:
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    if kd != 1 or vd != 1:
         raise ValueError("the last dim of k and v must be contiguous")
     _check_table(table, dev)
     _indexes(rows, "rows", dev, shape[:1])
     _indexes(positions, "positions", dev, shape[:1])
-    _call("kv_append", dev, k.data_ptr(), v.data_ptr(), dt, shape[0], k.stride(0), k.stride(1),
-          v.stride(0), v.stride(1), kv._ref, table.data_ptr(), table.shape[0], table.shape[1],
+    _call("kv_append", kv.index, k.data_ptr(), v.data_ptr(), dt, shape[0], kt, kh, vt, vh, kv._ref, table.data_ptr(), table.shape[0], table.shape[1],
           rows.data_ptr(), positions.data_ptr())
 
 
@@ -399,7 +410,7 @@ def kv_gather(kv: PagedKV, table, rows, positions, dtype=None, out=None) -> Tupl
         k, v = out
         _check_out(k, shape, dtype, "out[0] (k)", dev)
         _check_out(v, shape, dtype, "out[1] (v)", dev)
-    _call("kv_gather", dev, k.data_ptr(), v.data_ptr(), dt, T, kv._ref, table.data_ptr(),
+    _call("kv_gather", kv.index, k.data_ptr(), v.data_ptr(), dt, T, kv._ref, table.data_ptr(),
           table.shape[0], table.shape[1], rows.data_ptr(), positions.data_ptr())
     return k, v
 
@@ -426,25 +437,29 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
     dev = kv.device
     dt = kv.row_dtype(q.dtype, "q")
     _on(q, "q", dev)
-    if q.dim() != 3 or q.shape[2] != kv.head_dim:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [B][q_heads][{kv.head_dim}]")
-    B, Hq, D = q.shape
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != kv.head_dim:
+        raise ValueError(f"q has shape {tuple(shape)}, expected [B][q_heads][{kv.head_dim}]")
+    B, Hq, D = shape
     if Hq == 0 or Hq % kv.kv_heads:
         raise ValueError(f"{Hq} query heads do not divide over {kv.kv_heads} kv heads")
-    if q.stride(2) != 1 or q.stride(0) % 8 or q.stride(1) % 8 or q.data_ptr() % 16:
+    sb, sh, sd = q.stride()
+    if sd != 1 or sb % 8 or sh % 8 or q.data_ptr() % 16:
         q = q.contiguous()
         if q.data_ptr() % 16:
             q = q.clone()
+        sb, sh, _ = q.stride()
     _check_table(table, dev)
-    _indexes(lengths, "lengths", dev, (table.shape[0],))
+    S, width = table.shape
+    _indexes(lengths, "lengths", dev, (S,))
     if rows is not None:
         _indexes(rows, "rows", dev, (B,))
-    elif B > table.shape[0]:
-        raise ValueError(f"{B} queries, and the table has {table.shape[0]} rows")
-    room = table.shape[1] * kv.page_size
+    elif B > S:
+        raise ValueError(f"{B} queries, and the table has {S} rows")
+    room = width * kv.page_size
     max_len = room if max_len is None else min(int(max_len), room)
     if out is None:
-        out = q.new_empty((B, Hq, D))
+        out = q.new_empty(shape)
     else:
         _check_out(out, (B, Hq, D), q.dtype, "out", dev)
     lse = q.new_empty((B, Hq), dtype=torch.float32) if return_lse else None
@@ -452,13 +467,13 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
         n = _lib().kv_attention_workspace_size(B, Hq, kv.kv_heads, D, max_len)
         if n:
             workspace = table.new_empty((n // 4,))
-    _call("kv_attention", dev, q.data_ptr(), dt, B, Hq, q.stride(0), q.stride(1), kv._ref,
-          table.data_ptr(), table.shape[0], table.shape[1], lengths.data_ptr(),
+    _call("kv_attention", kv.index, q.data_ptr(), dt, B, Hq, sb, sh, kv._ref,
+          table.data_ptr(), S, width, lengths.data_ptr(),
           None if rows is None else rows.data_ptr(), max_len,
           D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(),
           None if lse is None else lse.data_ptr(),
           None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+          0 if workspace is None else workspace.nbytes)
     return (out, lse) if return_lse else out
 
 
@@ -484,7 +499,7 @@ def kv_pages_copy(kv: PagedKV, src, dst) -> None:
     twice, nor as a source."""
     _indexes(src, "src", kv.device)
     _indexes(dst, "dst", kv.device, src.shape)
-    _call("kv_pages_copy", kv.device, kv._ref, src.data_ptr(), dst.data_ptr(), src.numel())
+    _call("kv_pages_copy", kv.index, kv._ref, src.data_ptr(), dst.data_ptr(), src.numel())
 
 
 def kv_pages_reserve(table, lengths, refcount, rows, new_lengths, page_size: int, workspace=None):
@@ -500,9 +515,9 @@ def kv_pages_reserve(table, lengths, refcount, rows, new_lengths, page_size: int
     n, P = rows.numel(), refcount.numel()
     status = rows.new_empty(rows.shape)
     ws = _pages_workspace(P, n, dev, workspace)
-    _call("kv_pages_reserve", dev, P, page_size, table.data_ptr(), table.shape[0], table.shape[1],
+    _call("kv_pages_reserve", dev.index, P, page_size, table.data_ptr(), table.shape[0], table.shape[1],
           lengths.data_ptr(), refcount.data_ptr(), rows.data_ptr(), new_lengths.data_ptr(), n,
-          status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+          status.data_ptr(), ws.data_ptr(), ws.nbytes)
     return status
 
 
@@ -517,9 +532,9 @@ def kv_pages_fork(kv: PagedKV, table, lengths, refcount, parents, children, work
     n = parents.numel()
     status = parents.new_empty(parents.shape)
     ws = _pages_workspace(kv.num_pages, n, dev, workspace)
-    _call("kv_pages_fork", dev, kv._ref, table.data_ptr(), table.shape[0], table.shape[1],
+    _call("kv_pages_fork", kv.index, kv._ref, table.data_ptr(), table.shape[0], table.shape[1],
           lengths.data_ptr(), refcount.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
-          status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+          status.data_ptr(), ws.data_ptr(), ws.nbytes)
     return status
 
 
@@ -529,7 +544,7 @@ def kv_pages_free(table, lengths, refcount, rows) -> None:
     dev = table.device
     _pages_args(table, lengths, refcount, None, dev)
     _indexes(rows, "rows", dev)
-    _call("kv_pages_free", dev, refcount.numel(), table.data_ptr(), table.shape[0], table.shape[1],
+    _call("kv_pages_free", dev.index, refcount.numel(), table.data_ptr(), table.shape[0], table.shape[1],
           lengths.data_ptr(), refcount.data_ptr(), rows.data_ptr(), rows.numel())
 
 
@@ -545,7 +560,7 @@ def kv_pages_compact(kv: PagedKV, table, refcount, out: Optional[Tuple] = None, 
         _check_out(r, refcount.shape, torch.int32, "out[1] (refcount)", dev)
     n_live = table.new_empty((1,))
     ws = _pages_workspace(kv.num_pages, 0, dev, workspace)
-    _call("kv_pages_compact", dev, kv._ref, table.data_ptr(), t.data_ptr(), table.shape[0],
+    _call("kv_pages_compact", kv.index, kv._ref, table.data_ptr(), t.data_ptr(), table.shape[0],
           table.shape[1], refcount.data_ptr(), r.data_ptr(), n_live.data_ptr(), ws.data_ptr(),
-          ws.numel() * ws.element_size())
+          ws.nbytes)
     return t, r, n_live
