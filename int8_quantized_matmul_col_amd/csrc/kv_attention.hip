@@ -235,8 +235,27 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
     const Deal deal(total, a.parts);
     u0 = deal.begin(blockIdx.x);
     u1 = deal.begin(blockIdx.x + 1);
-    if (u0 >= u1) return;
     if (first > 0) lanes(0);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) {
+      // for the join: the first part that has units of a sequence, whether
+      // another sequence comes before in it, and how many parts have some
+      uint32_t base = 0;
+      for (int at = 0;;) {
+        const uint32_t begin = base + upto - own;
+        int2 c = {0, 0};
+        if (own > 0) {
+          const uint32_t x = deal.of(begin);
+          c.x = (int)(x * 2 + (deal.begin(x) < begin ? 1 : 0));
+          c.y = (int)(deal.of(begin + own - 1) - x + 1);
+        }
+        if (at + lane < a.B) a.cuts[at + lane] = c;
+        base += __builtin_amdgcn_readlane(upto, 63);
+        if ((at += 64) >= a.B) break;
+        lanes(at);
+      }
+      if (first > 0) lanes(0);
+    }
+    if (u0 >= u1) return;
     while (before + __builtin_amdgcn_readlane(upto, 63) <= u0) {
       before += __builtin_amdgcn_readlane(upto, 63);
       lanes(first + 64);
@@ -530,39 +549,35 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
 
 // Joins the pieces of one (sequence, query head); a lane holds 4 dims.
 template <bool QBF>
-__global__ __launch_bounds__(kJoinThreads) void k_kv_join(KvAttentionArgs a, int num_pages, int ps,
-                                                          int D, int unit) {
+__global__ __launch_bounds__(kJoinThreads) void k_kv_join(KvAttentionArgs a, int D) {
   __shared__ float f[kMaxParts];
   __shared__ float dens[kJoinThreads / 64];
   __shared__ v4f part[kJoinThreads];
   const int64_t bh = blockIdx.x;
   const int b = (int)(bh / a.q_heads), hq = (int)(bh % a.q_heads);
   const int lane = threadIdx.x & 63;
-  // where this sequence's units lie among the batch's
-  uint32_t total = 0, begin = 0;
-  int own = 0;
-  for (int at = 0; at < a.B; at += 64) {
-    const int n = at + lane < a.B ? units(visible(a, at + lane, num_pages, ps), unit) : 0;
-    const int upto = wave_scan(n);
-    if (b >= at && b < at + 64) {
-      own = __builtin_amdgcn_readlane(n, b - at);
-      begin = total + __builtin_amdgcn_readlane(upto, b - at) - own;
-    }
-    total += __builtin_amdgcn_readlane(upto, 63);
-  }
-  const Deal deal(total, a.parts);
-  const int x0 = own > 0 ? deal.of(begin) : 0, x1 = own > 0 ? deal.of(begin + own - 1) : 0;
-  if (own > 0 && x0 == x1) return;  // one workgroup had it all
-  const int n = own > 0 ? x1 - x0 + 1 : 0;
+  const int2 cut = a.cuts[b];
+  const int n = cut.y;
+  if (n == 1) return;  // one workgroup had it all
   const int tiles_h = (a.group + kKvHeadTile - 1) / kKvHeadTile;
   const int gy = hq / a.group * tiles_h + hq % a.group / kKvHeadTile;
   const int h = hq % a.group % kKvHeadTile;
-  // Piece i: of workgroup x0 + i, its first place unless it began with another
-  // sequence.  (Parts between two that have units have units too.)
+  // piece i: of part cut.x / 2 + i; the first may be that part's second place
   auto piece = [&](int i) {
-    const int64_t at = ((int64_t)gy * a.parts + x0 + i) * 2 + (deal.begin(x0 + i) < begin ? 1 : 0);
+    const int64_t at = ((int64_t)gy * a.parts + (cut.x >> 1) + i) * 2 + (i == 0 ? cut.x & 1 : 0);
     return at * a.tile_heads + h;
   };
+  // the outputs' first loads, before the factors are known
+  const int quads = D / 4, groups = kJoinThreads / quads;
+  const int g = threadIdx.x / quads, d = threadIdx.x % quads * 4;
+  constexpr int kU = 4;  // loads in flight
+  v4f v[kU];
+  auto load = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      v[u] = *reinterpret_cast<const v4f*>(a.part_o + piece(min(i + u * groups, n - 1)) * D + d);
+  };
+  if (n > 0) load(g);
   // every wave forms the maximum over all pieces; the factors are shared
   float mx = -INFINITY, den = 0.0f;
   for (int i = lane; i < n; i += 64) mx = fmaxf(mx, a.part_ml[2 * piece(i)]);
@@ -578,17 +593,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(KvAttentionArgs a, int
   if (lane == 0) dens[threadIdx.x >> 6] = den;
   __syncthreads();
 
-  const int quads = D / 4, groups = kJoinThreads / quads;
-  const int g = threadIdx.x / quads, d = threadIdx.x % quads * 4;
   v4f sum = {0, 0, 0, 0};
   if (g < groups) {
-    constexpr int kU = 4;  // loads in flight
     for (int i = g; i < n; i += groups * kU) {
-      v4f v[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (i + u * groups < n)
-          v[u] = *reinterpret_cast<const v4f*>(a.part_o + piece(i + u * groups) * D + d);
+      if (i != g) load(i);
 #pragma unroll
       for (int u = 0; u < kU; ++u)
         if (i + u * groups < n) sum += f[i + u * groups] * v[u];
@@ -664,14 +672,11 @@ hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm
   else
     e = bf16 ? pick<kI8, true>(a, pg, s) : pick<kI8, false>(a, pg, s);
   if (e != hipSuccess || a.parts == 0) return e;
-  const int unit = kWaves * (kv.dtype == INT8MM_I8 ? 64 : 32);
   const dim3 grid((unsigned)((int64_t)a.B * a.q_heads)), block(kJoinThreads);
   if (bf16)
-    hipLaunchKernelGGL(k_kv_join<true>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D,
-                       unit);
+    hipLaunchKernelGGL(k_kv_join<true>, grid, block, 0, s, a, pg.D);
   else
-    hipLaunchKernelGGL(k_kv_join<false>, grid, block, 0, s, a, pg.num_pages, pg.ps, pg.D,
-                       unit);
+    hipLaunchKernelGGL(k_kv_join<false>, grid, block, 0, s, a, pg.D);
   return hipGetLastError();
 }
 

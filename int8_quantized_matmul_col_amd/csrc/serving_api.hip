@@ -74,14 +74,15 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 }
 
 struct AttentionSizes {
-  size_t part_ml = 0, total = 0;
+  size_t part_ml = 0, cuts = 0, total = 0;
 };
-AttentionSizes attention_sizes(int64_t groups, int64_t tile_heads, int64_t D, int parts) {
+AttentionSizes attention_sizes(int64_t B, int64_t groups, int64_t tile_heads, int64_t D, int parts) {
   AttentionSizes z;
   if (parts > 0) {
     const size_t n = (size_t)groups * parts * 2 * tile_heads;
     z.part_ml = align_up(n * D * 4);
-    z.total = z.part_ml + align_up(n * 2 * 4);
+    z.cuts = z.part_ml + align_up(n * 2 * 4);
+    z.total = z.cuts + align_up((size_t)B * 8);
   }
   return z;
 }
@@ -213,7 +214,7 @@ INT8MM_API size_t kv_attention_workspace_size(int64_t B, int64_t q_heads, int64_
       max_len >= ((int64_t)1 << 31))
     return 0;
   const int64_t groups = head_groups(q_heads, kv_heads);
-  return attention_sizes(groups, tile_heads(q_heads, kv_heads), head_dim,
+  return attention_sizes(B, groups, tile_heads(q_heads, kv_heads), head_dim,
                          i8mm::kv_attention_parts(B, groups, max_len, 0)).total;
 }
 
@@ -247,7 +248,7 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   if (groups > 65535) return INT8MM_ESHAPE;
   a.parts = i8mm::kv_attention_parts(B, groups, most, window);
   a.tile_heads = (int)tile_heads(q_heads, kv->kv_heads);
-  const AttentionSizes z = attention_sizes(groups, a.tile_heads, kv->head_dim, a.parts);
+  const AttentionSizes z = attention_sizes(B, groups, a.tile_heads, kv->head_dim, a.parts);
   if (!workspace_ok(workspace, workspace_bytes, z.total)) return INT8MM_EWORKSPACE;
   a.q = static_cast<const uint16_t*>(q);
   a.q_batch_stride = q_batch_stride;
@@ -259,6 +260,7 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + z.part_ml);
+  a.cuts = reinterpret_cast<int2*>(static_cast<char*>(workspace) + z.cuts);
   a.B = (int)B;
   a.q_heads = (int)q_heads;
   a.group = (int)(q_heads / kv->kv_heads);

@@ -65,6 +65,7 @@ struct KvAttentionArgs {
   float* lse;
   float* part_o;   // [head groups][parts][2][tile_heads][head_dim]
   float* part_ml;  // [head groups][parts][2][tile_heads][2]
+  int2* cuts;      // [B], where each sequence was cut
   int B, q_heads, group, table_rows, table_width, max_len;  // group: query heads per kv head
   float scale, softcap;
   int64_t window;
