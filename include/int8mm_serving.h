@@ -15,6 +15,12 @@
  * calls).  Indexes that live on the device (page ids, row ids, positions,
  * lengths) are bounds-checked by the kernels: an entry out of range is
  * skipped, as described for each call, and never dereferenced.
+ *
+ * Limits (ESHAPE beyond): table_rows <= 2^30, table_width * page_size <= 2^30,
+ * 1024 kv heads, 65536 query heads, 4096 layers, 2^30 bytes for a page's keys
+ * in 16 bits; 2^28 tokens for a kv_append or kv_gather, B * q_heads < 2^24 for
+ * a kv_attention, 16384 rows or pairs for a kv_pages_reserve or _fork, 2^23
+ * rows for a kv_pages_free, 2^30 pairs for a kv_pages_copy.
  */
 #ifndef INT8MM_SERVING_H
 #define INT8MM_SERVING_H
@@ -51,6 +57,8 @@ extern "C" {
  * than 128 repeats its entry for every tile it covers.
  */
 #define INT4_MAX_K (1 << 20)
+#define INT4_MAX_N (1 << 24)
+#define INT4_MAX_M (1 << 21)
 
 /* Bytes of the prepared codes, and of the prepared group parameters; -1 for
  * an invalid shape or group.  group: 32, 64, or a multiple of 128. */
@@ -95,8 +103,9 @@ INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N);
  *        (ldx >= K); Y [M][N] and bias [N] (or NULL) of the same dtype.
  *   Wq, params, group, zeros: a prepared weight.
  * Meant for the few rows of a decode step: rows are taken 64 at a time, and
- * each 64 read the weight once.  M == 0 or N == 0: nothing to do.  K == 0:
- * Y = bias, or 0.  Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.
+ * each 64 read the weight once.  An infinity or NaN in X (or in a scale) makes
+ * what depends on it infinite or NaN, which of the two is unspecified, and
+ * nothing else.  M == 0 or N == 0: nothing to do.  K == 0: Y = bias, or 0.  Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.
  */
 INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx,
                            const void* Wq, const void* params, int64_t N, int64_t group, int zeros,
@@ -146,7 +155,7 @@ typedef struct int8mm_kv {
  *             sequence in table row rows[i].
  * A token whose row (0 .. table_rows-1), position (0 .. table_width *
  * page_size - 1) or page id is out of range is skipped.  Two tokens of one
- * call for the same place: one of them stays, which is unspecified.  An int8
+ * call for the same place: what it then holds is unspecified.  An int8
  * cache takes finite values; a token with an infinity or NaN reads back as
  * NaN in some or all places.  Errors: EINVAL, ESHAPE, EHIP.
  */

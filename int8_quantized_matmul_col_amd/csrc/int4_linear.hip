@@ -519,8 +519,8 @@ __global__ __launch_bounds__(256) void k_int4_prepare(const uint16_t* __restrict
                                                       uint16_t* __restrict__ params) {
   const int lane = threadIdx.x & 63;
   const int64_t groups = (K + group - 1) / group;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= Np * groups) return;
+  for (int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); id < Np * groups;
+       id += (int64_t)gridDim.x * 4) {
   const int64_t n = id / groups, g = id % groups;
   const int64_t k0 = g * group, k1 = min(K, k0 + group);
   // the last group also fills the padding of its tile
@@ -563,6 +563,7 @@ __global__ __launch_bounds__(256) void k_int4_prepare(const uint16_t* __restrict
       params[e] = in ? sc : (uint16_t)0;
     }
   }
+  }
 }
 
 unsigned grid_for(int64_t total, int block) {
@@ -592,7 +593,8 @@ hipError_t launch_int4_prepare(const uint16_t* W, bool bf16, int64_t N, int64_t 
   const int64_t Np = int4_padded_rows(N), nt = int4_tiles_k(K);
   const int gs = 32 * int4_group_steps(group);
   const int64_t waves = Np * ((K + group - 1) / group);
-  const dim3 grid((unsigned)((waves + 3) / 4));
+  // at most 2^20 workgroups: a launch holds fewer than 2^32 threads
+  const dim3 grid((unsigned)(waves < (1 << 22) ? (waves + 3) / 4 : 1 << 20));
   if (bf16)
     hipLaunchKernelGGL(k_int4_prepare<true>, grid, dim3(256), 0, s, W, N, K, Np, group, gs, nt,
                        zeros, Wq, params);

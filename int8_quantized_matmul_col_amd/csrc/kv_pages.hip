@@ -362,13 +362,13 @@ __global__ __launch_bounds__(kThreads) void k_pages_reserve(Rows r, Snapshot s, 
   if (threadIdx.x == 0) r.lengths[row] = want;
 }
 
-// Workgroups of pair i: `per` of them copy the partly filled page, the first
-// also writes the child's row.
+// Workgroups of pair i: they share the `per` slices of the partly filled page,
+// the first also writes the child's row.
 __global__ __launch_bounds__(kThreads) void k_pages_fork(Rows r, Snapshot s, int blocks, Copier c,
                                                          int per) {
   __shared__ uint32_t pre[kMaxBlocks + 1];
   __shared__ uint32_t part[kThreads / 64];
-  const int i = blockIdx.x / per, sl = blockIdx.x % per;
+  const int i = blockIdx.y, sl = blockIdx.x;
   int st = s.plan[i];
   const uint32_t first = s.first[i], need = s.need[i];
   int fresh = -1;
@@ -401,7 +401,11 @@ __global__ __launch_bounds__(kThreads) void k_pages_fork(Rows r, Snapshot s, int
       r.lengths[child] = len;
     }
   }
-  if (fresh >= 0) copy_slice(c, sl, __builtin_amdgcn_readfirstlane(from[whole]), fresh);
+  if (fresh >= 0) {
+    const int src = __builtin_amdgcn_readfirstlane(from[whole]);
+#pragma unroll 1
+    for (int w = sl; w < per; w += gridDim.x) copy_slice(c, w, src, fresh);
+  }
 }
 
 __global__ __launch_bounds__(kThreads) void k_pages_free(Rows r) {
@@ -527,8 +531,8 @@ hipError_t launch_kv_pages_fork(const int8mm_kv& kv, int32_t* table, int table_r
   if (e != hipSuccess) return e;
   const Copier c = copier_of(kv);
   const int per = c.layers * c.slices[3];
-  hipLaunchKernelGGL(k_pages_fork, dim3((unsigned)n * per), dim3(kThreads), 0, s, r, sn, blocks, c,
-                     per);
+  hipLaunchKernelGGL(k_pages_fork, dim3((unsigned)(per < 65536 ? per : 65536), (unsigned)n),
+                     dim3(kThreads), 0, s, r, sn, blocks, c, per);
   return hipGetLastError();
 }
 
@@ -547,10 +551,12 @@ hipError_t launch_kv_pages_compact(const int8mm_kv& kv, const int32_t* table, in
                                    hipStream_t s) {
   const Snapshot sn = carve(ws, kv.num_pages, 0, nullptr);
   const int blocks = blocks_of(kv.num_pages);
-  hipLaunchKernelGGL(k_pages_scan, dim3(blocks), dim3(kScanThreads), 0, s, refcount, kv.num_pages,
-                     sn);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (blocks > 0) {
+    hipLaunchKernelGGL(k_pages_scan, dim3(blocks), dim3(kScanThreads), 0, s, refcount, kv.num_pages,
+                       sn);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(k_pages_compact, dim3(2048), dim3(kThreads), 0, s, table, table_out,
                      (int64_t)table_rows * table_width, refcount, refcount_out, kv.num_pages, sn,
                      blocks, copier_of(kv), n_live);

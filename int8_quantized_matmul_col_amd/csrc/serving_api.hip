@@ -11,6 +11,9 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxCount = (int64_t)1 << 30;  // int32 indexing in the kernels
 constexpr int64_t kMaxNamed = 16384;             // rows or pairs of one reserve or fork
+// a launch holds fewer than 2^32 threads
+constexpr int64_t kMaxTokens = (int64_t)1 << 28;
+constexpr int64_t kMaxFreed = (int64_t)1 << 23;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
@@ -19,7 +22,7 @@ int status_of(hipError_t e) { return e == hipSuccess ? INT8MM_OK : i8mm::record_
 // ------------------------------------------------------------ 4-bit weights
 
 bool int4_shape(int64_t N, int64_t K) {
-  return N >= 0 && K >= 0 && K <= INT4_MAX_K && N <= kMaxCount;
+  return N >= 0 && K >= 0 && K <= INT4_MAX_K && N <= INT4_MAX_N;
 }
 bool int4_group(int64_t group) {
   return group == 32 || group == 64 || (group >= 128 && group % 128 == 0 && group <= INT4_MAX_K);
@@ -135,7 +138,7 @@ INT8MM_API int int4_prepare_weight(const void* W, int dtype, int64_t N, int64_t 
 }
 
 INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N) {
-  if (!int4_shape(N, K) || M < 0 || M > kMaxCount) return 0;
+  if (!int4_shape(N, K) || M < 0 || M > INT4_MAX_M) return 0;
   if (M == 0 || K == 0 || N == 0) return 0;
   const int parts = i8mm::int4_k_parts(M, K, N);
   return parts > 1 ? align_up((size_t)parts * M * N * 4) : 0;
@@ -146,7 +149,7 @@ INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64
                            const void* bias, void* Y, void* workspace, size_t workspace_bytes,
                            hipStream_t stream) {
   if (dtype != INT8MM_F16 && dtype != INT8MM_BF16) return INT8MM_EINVAL;
-  if (!int4_shape(N, K) || !int4_group(group) || M < 0 || M > kMaxCount) return INT8MM_ESHAPE;
+  if (!int4_shape(N, K) || !int4_group(group) || M < 0 || M > INT4_MAX_M) return INT8MM_ESHAPE;
   if (M == 0 || N == 0) return INT8MM_OK;
   if (ldx < K) return INT8MM_ESHAPE;
   if (Y == nullptr || (K > 0 && (X == nullptr || Wq == nullptr || params == nullptr))) return INT8MM_EINVAL;
@@ -177,7 +180,7 @@ INT8MM_API int kv_append(const void* k, const void* v, int dtype, int64_t T,
   const int st = check_kv(kv, false);
   if (st != INT8MM_OK) return st;
   if (!row_type(dtype, kv)) return INT8MM_EINVAL;
-  if (T < 0 || T > kMaxCount || !table_shape(table_rows, table_width, kv->page_size)) return INT8MM_ESHAPE;
+  if (T < 0 || T > kMaxTokens || !table_shape(table_rows, table_width, kv->page_size)) return INT8MM_ESHAPE;
   if (T == 0 || kv->num_pages == 0) return INT8MM_OK;
   if (k == nullptr || v == nullptr || rows == nullptr || positions == nullptr) return INT8MM_EINVAL;
   if (table == nullptr && table_rows > 0 && table_width > 0) return INT8MM_EINVAL;
@@ -195,7 +198,7 @@ INT8MM_API int kv_gather(void* k, void* v, int dtype, int64_t T, const int8mm_kv
   const int st = check_kv(kv, false);
   if (st != INT8MM_OK) return st;
   if (!row_type(dtype, kv)) return INT8MM_EINVAL;
-  if (T < 0 || T > kMaxCount || !table_shape(table_rows, table_width, kv->page_size)) return INT8MM_ESHAPE;
+  if (T < 0 || T > kMaxTokens || !table_shape(table_rows, table_width, kv->page_size)) return INT8MM_ESHAPE;
   if (T == 0) return INT8MM_OK;
   if (k == nullptr || v == nullptr || rows == nullptr || positions == nullptr) return INT8MM_EINVAL;
   if (table == nullptr && table_rows > 0 && table_width > 0) return INT8MM_EINVAL;
@@ -228,7 +231,7 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   if (st != INT8MM_OK) return st;
   if (!row_type(dtype, kv)) return INT8MM_EINVAL;
   if (B < 0 || q_heads < 1 || q_heads > 65536 || q_heads % kv->kv_heads != 0 ||
-      B * q_heads > ((int64_t)1 << 24) || max_len < 0 || max_len >= ((int64_t)1 << 31) || window < 0 ||
+      B > kMaxCount || B * q_heads >= ((int64_t)1 << 24) || max_len < 0 || max_len >= ((int64_t)1 << 31) || window < 0 ||
       !table_shape(table_rows, table_width, kv->page_size))
     return INT8MM_ESHAPE;
   if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return INT8MM_EINVAL;
@@ -336,7 +339,7 @@ INT8MM_API int kv_pages_free(int32_t num_pages, int32_t* table, int64_t table_ro
                              int64_t table_width, int32_t* lengths, int32_t* refcount,
                              const int32_t* rows, int64_t n, hipStream_t stream) {
   if (num_pages < 0 || num_pages > INT8MM_KV_MAX_PAGES) return INT8MM_ESHAPE;
-  if (n < 0 || n > kMaxCount || !table_shape(table_rows, table_width, 1)) return INT8MM_ESHAPE;
+  if (n < 0 || n > kMaxFreed || !table_shape(table_rows, table_width, 1)) return INT8MM_ESHAPE;
   if (n == 0) return INT8MM_OK;
   if (table == nullptr || lengths == nullptr || rows == nullptr || (refcount == nullptr && num_pages > 0))
     return INT8MM_EINVAL;

@@ -24,6 +24,8 @@ from .binding import INT8MM_ESHAPE, Int8mmError, _check, _check_out, _require
 
 INT8MM_F16, INT8MM_BF16, INT8MM_I8 = 0, 1, 2
 INT4_MAX_K = 1 << 20
+INT4_MAX_N = 1 << 24
+INT4_MAX_M = 1 << 21
 INT8MM_KV_MAX_PAGES = 1 << 22
 INT8MM_KV_MAX_PAGE_SIZE = 1024
 INT8MM_KV_MAX_HEAD_DIM = 256

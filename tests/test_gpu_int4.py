@@ -123,6 +123,19 @@ def test_strided_and_unaligned_rows(lib, M, K):
     assert torch.equal(lib.int4_linear(X[:, 3:3 + K], w), lib.int4_linear(X[:, 3:3 + K].contiguous(), w))
 
 
+def test_prepare_more_groups_than_one_launch_has_waves(lib):
+    """2^26 groups and some: the weight repeats, and so does what is stored."""
+    N, K, small = (1 << 17) + 16, 1 << 14, 32
+    W = torch.randn((small, K), device="cuda", generator=torch.Generator("cuda").manual_seed(3)).half()
+    want = lib.int4_prepare_weight(W, group_size=32)
+    got = lib.int4_prepare_weight(W.repeat((N + small - 1) // small, 1)[:N], group_size=32)
+    for a, b in ((got.Wq, want.Wq), (got.params, want.params)):
+        b = b.view(2, -1)
+        a = a.view(-1, b.shape[1])
+        assert a.shape[0] == N // 16
+        assert bool((a[0::2] == b[0]).all()) and bool((a[1::2] == b[1]).all())
+
+
 def test_rows_do_not_depend_on_each_other(lib):
     # a row's result is the same alone, among others, and beside rows of NaN
     g = rng(5)

@@ -299,6 +299,24 @@ def test_compact(lib, S, P, width, ps, in_place, cache):
     assert all(torch.equal(a, b) for a, b in zip(_tensors(kv), kept))
 
 
+def test_pool_without_pages(lib):
+    k = torch.empty((1, 0, 2, 16, 64), dtype=torch.float16, device="cuda")
+    kv = lib.PagedKV(k, torch.empty((1, 0, 2, 64, 16), dtype=torch.float16, device="cuda"))
+    table, n, ref = torch.full((2, 3), 5, **INT), torch.zeros(2, **INT), torch.zeros(0, **INT)
+    t, r, live = lib.kv_pages_compact(kv, table, ref)
+    assert int(live) == 0 and t.tolist() == [[-1] * 3] * 2 and r.numel() == 0
+    status = lib.kv_pages_reserve(table, n, ref, _i32([0, 1]), _i32([0, 1]), 16)
+    assert status.tolist() == [lib.INT8MM_KV_DONE, lib.INT8MM_KV_NO_PAGES] and n.tolist() == [0, 0]
+    assert lib.kv_pages_fork(kv, table, n, ref, _i32([0]), _i32([1])).tolist() == [lib.INT8MM_KV_DONE]
+    one = kv.layer(0)
+    kk, vv = lib.kv_gather(one, table, _i32([0]), _i32([0]))
+    assert not kk.any() and not vv.any()
+    lib.kv_append(kk, vv, one, table, _i32([0]), _i32([0]))
+    out, lse = lib.kv_attention(torch.ones((2, 4, 64), dtype=torch.float16, device="cuda"), one,
+                                table, _i32([5, 0]), return_lse=True)
+    assert not out.any() and bool((lse == -math.inf).all())
+
+
 def test_page_calls_replay_from_a_graph(lib):
     g = rng(36)
     kv, table, lengths, refc, pool = _world(lib, g, 8, 60, 6, 16, "f16")

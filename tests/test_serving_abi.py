@@ -50,7 +50,8 @@ def test_header_binding_and_library_agree(lib):
     for n in fns:
         assert hasattr(lib, n), n
     consts = dict(re.findall(r"#define (INT\w+) \(?(\d+(?: << \d+)?)\)?", src))
-    for n in ("INT8MM_F16", "INT8MM_BF16", "INT8MM_I8", "INT4_MAX_K", "INT8MM_KV_MAX_PAGES",
+    for n in ("INT8MM_F16", "INT8MM_BF16", "INT8MM_I8", "INT4_MAX_K", "INT4_MAX_N",
+              "INT4_MAX_M", "INT8MM_KV_MAX_PAGES",
               "INT8MM_KV_MAX_PAGE_SIZE", "INT8MM_KV_MAX_HEAD_DIM", "INT8MM_KV_DONE",
               "INT8MM_KV_NO_PAGES", "INT8MM_KV_BAD_ROW"):
         assert eval(consts[n]) == getattr(serving, n), n
@@ -195,6 +196,17 @@ def test_row_and_page_refusals(lib):
     assert comp(t=None) == EINVAL and comp(out=None) == EINVAL and comp(live=None) == EINVAL
     assert comp(ws=None) == EWORKSPACE and comp(nb=10) == EWORKSPACE
     assert lib.kv_pages_workspace_size(-1, 1) == 0 and lib.kv_pages_workspace_size(8, 16385) == 0
+
+
+def test_sizes_beyond_a_launch_are_refused(lib):
+    """A launch holds fewer than 2^32 threads."""
+    assert lib.int4_weight_bytes((1 << 24) + 1, 64) == -1
+    assert _lin(lib, N=(1 << 24) + 1) == ESHAPE and _lin(lib, M=(1 << 21) + 1) == ESHAPE
+    assert _att(lib, B=1 << 22, Hq=4) == ESHAPE and _att(lib, B=1 << 62, Hq=4) == ESHAPE
+    assert lib.kv_append(FAKE, FAKE, 0, (1 << 28) + 1, 128, 64, 128, 64, _kv(), FAKE, 2, 4, FAKE,
+                         FAKE, None) == ESHAPE
+    assert lib.kv_gather(FAKE, FAKE, 0, (1 << 28) + 1, _kv(), FAKE, 2, 4, FAKE, FAKE, None) == ESHAPE
+    assert lib.kv_pages_free(8, FAKE, 2, 4, FAKE, FAKE, FAKE, (1 << 23) + 1, None) == ESHAPE
 
 
 # ---------------------------------------------- the reference, on its own terms
