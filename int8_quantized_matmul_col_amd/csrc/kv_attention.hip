@@ -28,10 +28,11 @@
 // workgroups (two on every CU), which find their sequences from the lengths;
 // a workgroup's 4 waves take its chunks in turn.  So very different lengths
 // cost nothing (64 sequences of 1..8192 tokens, int8: 150 us with pieces of
-// one length, 103 us so), and one long sequence is split as well.  Waves join
-// in LDS, cut sequences in a second kernel, each in a fixed order.  Where no
+// one length, 103 to 110 so, 5.1 TB/s), and one long sequence is split as well
+// (131071 tokens: 62 us; 384 workgroups take 73, 768 take 66).  Waves join in
+// LDS, cut sequences in a second kernel, each in a fixed order.  Where no
 // sequence can be longer than 256 tokens each is one workgroup's, and there is
-// no second kernel (12.3 instead of 17.5 us for one of 200).
+// no second kernel (one of 200: 11 us, 16 with one, most of it the launches).
 #include "device_common.h"
 #include "serving_launch.h"
 
@@ -627,12 +628,21 @@ hipError_t run(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Head sizes that are whole 32-dim steps (int8: 64) have instances without
+// idle registers and tiles: an int8 cache of 8 x 8192 tokens, 8 kv heads of
+// 192 / 256 dims, is read at 3.8 / 4.2 TB/s so, 3.2 / 3.8 with the general
+// one; 17 sequences of up to 1000 tokens of 6 x 96 dims take 19.1 us, 20.2 with
+// the general one.  Other sizes, and 32 and 160 dims, lose up to the same.
 template <int CT, bool QBF>
 hipError_t pick(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
-  if (pg.D == 64) return run<CT, QBF, 2, true>(a, pg, s);
-  if (pg.D == 128) return run<CT, QBF, 4, true>(a, pg, s);
-  if (pg.D < 128) return run<CT, QBF, 4, false>(a, pg, s);
-  return run<CT, QBF, 8, false>(a, pg, s);
+  switch (pg.D) {
+    case 64: return run<CT, QBF, 2, true>(a, pg, s);
+    case 96: if constexpr (CT != kI8) return run<CT, QBF, 3, true>(a, pg, s); break;
+    case 128: return run<CT, QBF, 4, true>(a, pg, s);
+    case 192: return run<CT, QBF, 6, true>(a, pg, s);
+    case 256: return run<CT, QBF, 8, true>(a, pg, s);
+  }
+  return pg.D < 128 ? run<CT, QBF, 4, false>(a, pg, s) : run<CT, QBF, 8, false>(a, pg, s);
 }
 
 }  // namespace
