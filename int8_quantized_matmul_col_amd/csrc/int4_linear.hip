@@ -250,12 +250,11 @@ __global__ __launch_bounds__(64 * max_waves(P)) void k_int4_few(
 // and alignment takes this one path.  Where few channels leave CUs idle K is
 // split over workgroups too (blockIdx.z), and a second kernel adds their sums.
 //
-// 64 x 8192 x 28672 takes 53 us, of which 28 are the matrix instructions and
+// 64 x 8192 x 28672 takes 50 us, of which 28 are the matrix instructions and
 // the groups' scales alone (1.1 of the 1.2 PFLOP/s that a large library product
-// reaches here), 10 the codes and LDS, the rest the loads; 48 x 5120 x 13811 25
-// us, 64 x 4096 x 11008 20.
+// reaches here), 10 the codes and LDS, the rest the loads; 48 x 5120 x 13811 in
+// groups of 32 26 us (33 with K in two parts), 64 x 4096 x 11008 20.
 constexpr int kManyWaves = 8;
-constexpr int kStages = 3;  // weights in flight: two steps ahead
 
 template <bool BF16, bool ZEROS, int GS, int MT, int P>
 __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
@@ -263,6 +262,11 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
     const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ params, int N,
     const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y, float* __restrict__ part) {
   using G = Group<BF16, ZEROS, GS>;
+  // X is requested two steps ahead and the weight three, where the registers
+  // allow (64 x 8192 x 28672, groups of 128: 52.7 -> 50 us, 32 rows 38.5 -> 35;
+  // with two channel tiles and narrow groups they would spill: one and two)
+  constexpr bool kDeep = P == 1 || GS == 4;
+  constexpr int kStages = kDeep ? 4 : 3, kAhead = kDeep ? 2 : 1;
   constexpr int kChunk = MT * 2 * 4 * 64;  // 16-byte units of one step's X
   constexpr int kSums = kManyWaves * P * MT * 256 * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kChunk * 16 > kSums ? 2 * kChunk * 16 : kSums];
@@ -286,32 +290,32 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
 
   // staging: this thread's chunk of 8 k in rows row0 + 16 i
   const int c = threadIdx.x & 31, row0 = threadIdx.x >> 5;
-  v4u hold[MT];
-  auto fetch = [&](int step) __attribute__((always_inline)) {
+  v4u hold[kAhead][MT];
+  auto fetch = [&](int h, int step) __attribute__((always_inline)) {
     const int k = step * 256 + c * 8;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int m = m0 + row0 + 16 * i;
-      hold[i] = v4u{0, 0, 0, 0};
+      hold[h][i] = v4u{0, 0, 0, 0};
       if (m >= M || k >= K) continue;
       const uint16_t* p = X + (int64_t)m * ldx + k;
       if (vec) {
-        hold[i] = *reinterpret_cast<const v4u*>(p);
+        hold[h][i] = *reinterpret_cast<const v4u*>(p);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t a = k + 2 * e < K ? p[2 * e] : 0u;
           const uint32_t b = k + 2 * e + 1 < K ? p[2 * e + 1] : 0u;
-          hold[i][e] = a | (b << 16);
+          hold[h][i][e] = a | (b << 16);
         }
       }
     }
   };
-  auto stage = [&](int buf) __attribute__((always_inline)) {
+  auto stage = [&](int h, int buf) __attribute__((always_inline)) {
     const int t = c >> 4, sq = c & 15;  // tile of the step, (32-k step, quarter)
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      xs[buf * kChunk + ((t * MT + i) * 4 + (sq >> 2)) * 64 + (sq & 3) * 16 + (row0 ^ sq)] = hold[i];
+      xs[buf * kChunk + ((t * MT + i) * 4 + (sq >> 2)) * 64 + (sq & 3) * 16 + (row0 ^ sq)] = hold[h][i];
   };
 
   v4u w[kStages][P];
@@ -384,10 +388,12 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
   // weight read in its place is finite.
   const int last = step1 - 1;
   if (step0 < step1) {
-    fetch(step0);
+    fetch(0, step0);
+    load_w(0, step0);
+    if (kDeep) fetch(kAhead - 1, min(step0 + 1, last));
 #pragma unroll
-    for (int st = 0; st < kStages - 1; ++st) load_w(st, min(step0 + st, last));
-    stage(0);
+    for (int st = 1; st < kStages - 1; ++st) load_w(st, min(step0 + st, last));
+    stage(0, 0);
     sync();
     for (int t = step0; t < step1; t += kStages) {
 #pragma unroll
@@ -395,11 +401,11 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
         if (st > 0 && t + st > last) break;
         const int now = t + st, buf = (now - step0) & 1;
         // X first: loads return in order, and waiting for X must not wait for
-        // the weight of two steps on
-        fetch(min(now + 1, last));
+        // the weight of steps further on
+        fetch(st % kAhead, min(now + kAhead, last));
         load_w((st + kStages - 1) % kStages, min(now + kStages - 1, last));
         compute(st, buf);
-        stage(buf ^ 1);  // (read last a step ago, before the barrier there)
+        stage((st + 1) % kAhead, buf ^ 1);  // (read last a step ago, before the barrier there)
         sync();
       }
     }
@@ -652,7 +658,7 @@ hipError_t run_many(const Int4Args& a, hipStream_t s) {
 }
 
 // Two channel tiles a wave halve the reads of X, but need twice the channels
-// to fill the GPU (64 x 8192 x 28672: 53 us against 60 with one; 64 x 4096 x
+// to fill the GPU (64 x 8192 x 28672: 50 us against 58 with one; 64 x 4096 x
 // 11008: 26.5 against 20.3).
 template <bool BF16, bool ZEROS, int GS, int MT>
 hipError_t pick_many(const Int4Args& a, hipStream_t s) {
