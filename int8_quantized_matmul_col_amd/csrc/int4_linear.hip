@@ -658,11 +658,12 @@ hipError_t run_many(const Int4Args& a, hipStream_t s) {
 }
 
 // Two channel tiles a wave halve the reads of X, but need twice the channels
-// to fill the GPU (64 x 8192 x 28672: 50 us against 58 with one; 64 x 4096 x
-// 11008: 26.5 against 20.3).
+// to fill the GPU (64 x 8192 x 28672: 50 us against 57 with one; 64 x 4096 x
+// 11008: 26.5 against 20.3).  bfloat16's 64 rows in groups of 32 have no
+// registers for it (64 x 8192 x 28672: 186 us spilling, 97 with one).
 template <bool BF16, bool ZEROS, int GS, int MT>
 hipError_t pick_many(const Int4Args& a, hipStream_t s) {
-  if constexpr (MT > 1)
+  if constexpr (MT > 1 && !(BF16 && GS == 1 && MT == 4))
     if (a.N >= 128 * 200) return run_many<BF16, ZEROS, GS, MT, 2>(a, s);
   return run_many<BF16, ZEROS, GS, MT, 1>(a, s);
 }

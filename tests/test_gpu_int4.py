@@ -54,6 +54,8 @@ SHAPES = [
     # K in parts, many channels, tiles of K that end inside a step
     (20, 5300, 70, 64), (64, 5200, 33, 128), (3, 5251, 40, 32), (40, 140, 25700, 128),
     (18, 250, 16, 32), (64, 383, 130, 64),
+    (64, 1100, 25650, 32), (24, 1300, 25630, 64), (48, 1288, 25601, 128), (30, 2600, 70, 32),
+    (64, 2304, 100, 128),
 ]
 
 
