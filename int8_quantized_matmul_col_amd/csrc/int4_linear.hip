@@ -242,8 +242,8 @@ __global__ __launch_bounds__(64 * max_waves(P)) void k_int4_few(
 
 // ------------------------------------------- more rows, or any alignment
 //
-// 8 waves share X: 4 groups of P channel tiles times the 2 tiles of K of a
-// step.  A step's X, up to 64 rows of 512 contiguous bytes, goes through
+// 4 * KS waves share X: 4 groups of P channel tiles times the KS tiles of K of
+// a step.  A step's X, up to 64 rows of KS * 256 contiguous bytes, goes through
 // registers into LDS in operand order, the next step's while this one is
 // multiplied; a chunk's place is exclusive-ored with its k so that neither side
 // has bank conflicts.  Rows past M and k past K are zeros there, so every shape
@@ -253,21 +253,23 @@ __global__ __launch_bounds__(64 * max_waves(P)) void k_int4_few(
 // 64 x 8192 x 28672 takes 50 us, of which 28 are the matrix instructions and
 // the groups' scales alone (1.1 of the 1.2 PFLOP/s that a large library product
 // reaches here), 10 the codes and LDS, the rest the loads; 48 x 5120 x 13811 in
-// groups of 32 26 us (33 with K in two parts), 64 x 4096 x 11008 20.
-constexpr int kManyWaves = 8;
-
-template <bool BF16, bool ZEROS, int GS, int MT, int P>
-__global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
+// groups of 32 takes 21.5 to 23 us (24 to 26 with 8 waves, whose LDS reads,
+// codes and matrix instructions hide one another less; 33 with K in two parts),
+// 64 x 4096 x 11008 17.7.
+template <bool BF16, bool ZEROS, int GS, int MT, int P, int KS>
+__global__ __launch_bounds__(256 * KS) void k_int4_many(
     const uint16_t* __restrict__ X, int M, int K, int64_t ldx, int vec,
     const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ params, int N,
     const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y, float* __restrict__ part) {
   using G = Group<BF16, ZEROS, GS>;
   // X is requested two steps ahead and the weight three, where the registers
   // allow (64 x 8192 x 28672, groups of 128: 52.7 -> 50 us, 32 rows 38.5 -> 35;
-  // with two channel tiles and narrow groups they would spill: one and two)
-  constexpr bool kDeep = P == 1 || GS == 4;
+  // with two channel tiles and narrow groups, or 16 waves, they would spill:
+  // one and two)
+  constexpr bool kDeep = KS == 2 && (P == 1 || GS == 4);
   constexpr int kStages = kDeep ? 4 : 3, kAhead = kDeep ? 2 : 1;
-  constexpr int kChunk = MT * 2 * 4 * 64;  // 16-byte units of one step's X
+  constexpr int kManyWaves = 4 * KS;
+  constexpr int kChunk = MT * KS * 4 * 64;  // 16-byte units of one step's X
   constexpr int kSums = kManyWaves * P * MT * 256 * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kChunk * 16 > kSums ? 2 * kChunk * 16 : kSums];
   v4u* xs = reinterpret_cast<v4u*>(lds);        // [2][tile][MT][step][64]
@@ -277,10 +279,10 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, qd = lane >> 4;
   const int pg = wave & 3, ks = wave >> 2;
-  const int nt = (K + kInt4TileK - 1) / kInt4TileK, pairs = (nt + 1) / 2;
+  const int nt = (K + kInt4TileK - 1) / kInt4TileK, steps = (nt + KS - 1) / KS;
   // this workgroup's steps
-  const int step0 = (int)((int64_t)blockIdx.z * pairs / gridDim.z);
-  const int step1 = (int)((int64_t)(blockIdx.z + 1) * pairs / gridDim.z);
+  const int step0 = (int)((int64_t)blockIdx.z * steps / gridDim.z);
+  const int step1 = (int)((int64_t)(blockIdx.z + 1) * steps / gridDim.z);
   const int m0 = blockIdx.y * (16 * MT);
   const int panels = (N + 15) / 16, panel0 = blockIdx.x * (4 * P) + pg * P;
   int64_t first[P];
@@ -289,10 +291,10 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
   const Nibbles nib = nibbles<BF16>();
 
   // staging: this thread's chunk of 8 k in rows row0 + 16 i
-  const int c = threadIdx.x & 31, row0 = threadIdx.x >> 5;
+  const int c = threadIdx.x % (16 * KS), row0 = threadIdx.x / (16 * KS);
   v4u hold[kAhead][MT];
   auto fetch = [&](int h, int step) __attribute__((always_inline)) {
-    const int k = step * 256 + c * 8;
+    const int k = step * (KS * kInt4TileK) + c * 8;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int m = m0 + row0 + 16 * i;
@@ -321,7 +323,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
   v4u w[kStages][P];
   typename G::Par par[kStages][P];
   auto load_w = [&](int st, int step) __attribute__((always_inline)) {
-    const int t = min(step * 2 + ks, nt - 1);
+    const int t = min(step * KS + ks, nt - 1);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int64_t tile = first[p] + t;
@@ -384,8 +386,8 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
 
-  // The second tile of the last step may lie past K: its X is zero, and the
-  // weight read in its place is finite.
+  // The later tiles of the last step may lie past K: their X is zero, and the
+  // weight read in their place is finite.
   const int last = step1 - 1;
   if (step0 < step1) {
     fetch(0, step0);
@@ -411,7 +413,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
     }
   }
 
-  // the waves' partial sums: the two halves of K, in order
+  // the waves' partial sums: the KS shares of K, in order
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -428,7 +430,9 @@ __global__ __launch_bounds__(64 * kManyWaves) void k_int4_many(
     if (n >= N) continue;
     const int wv = nl / (16 * P), p = nl / 16 % P;
     const int at = (((wv * P + p) * MT + (m >> 4)) * 4 + (m & 3)) * 64 + ((m & 15) >> 2) * 16 + (nl & 15);
-    float y = red[at] + red[at + 4 * P * MT * 256];
+    float y = red[at];
+#pragma unroll
+    for (int h = 1; h < KS; ++h) y += red[at + h * 4 * P * MT * 256];
     if (part != nullptr) {
       part[((int64_t)blockIdx.z * M + m0 + m) * N + n] = y;
     } else {
@@ -641,12 +645,12 @@ hipError_t pick_few(const Int4Args& a, hipStream_t s) {
   return run_few<BF16, ZEROS, GS, 4>(a, s);
 }
 
-template <bool BF16, bool ZEROS, int GS, int MT, int P>
+template <bool BF16, bool ZEROS, int GS, int MT, int P, int KS>
 hipError_t run_many(const Int4Args& a, hipStream_t s) {
   const int z = int4_k_parts(a.M, a.K, a.N);
   const dim3 grid((a.N + 64 * P - 1) / (64 * P), (a.M + 16 * MT - 1) / (16 * MT), z);
   const int vec = a.K % 8 == 0 && (a.ldx % 8 == 0 || a.M == 1) && (reinterpret_cast<uintptr_t>(a.X) & 15) == 0;
-  hipLaunchKernelGGL((k_int4_many<BF16, ZEROS, GS, MT, P>), grid, dim3(64 * kManyWaves), 0, s, a.X,
+  hipLaunchKernelGGL((k_int4_many<BF16, ZEROS, GS, MT, P, KS>), grid, dim3(256 * KS), 0, s, a.X,
                      a.M, a.K, a.ldx, vec, a.Wq, a.params, a.N, a.bias, a.Y,
                      z > 1 ? a.part : nullptr);
   const hipError_t e = hipGetLastError();
@@ -659,13 +663,19 @@ hipError_t run_many(const Int4Args& a, hipStream_t s) {
 
 // Two channel tiles a wave halve the reads of X, but need twice the channels
 // to fill the GPU (64 x 8192 x 28672: 50 us against 57 with one; 64 x 4096 x
-// 11008: 26.5 against 20.3).  bfloat16's 64 rows in groups of 32 have no
+// 11008: 26.5 against 17.7).  bfloat16's 64 rows in groups of 32 have no
 // registers for it (64 x 8192 x 28672: 186 us spilling, 97 with one).
+//
+// Four tiles of K a step, 16 waves, where their 128 registers do (48 x 5120 x
+// 13811 in groups of 32 25 -> 22.8 us, 64 x 4096 x 16000 21.5 -> 20, never
+// slower from K = 512 on), otherwise two and 8 waves (64 x 4096 x 11008
+// bfloat16 in groups of 32: 27.5 us, 121 spilling with 16).
 template <bool BF16, bool ZEROS, int GS, int MT>
 hipError_t pick_many(const Int4Args& a, hipStream_t s) {
   if constexpr (MT > 1 && !(BF16 && GS == 1 && MT == 4))
-    if (a.N >= 128 * 200) return run_many<BF16, ZEROS, GS, MT, 2>(a, s);
-  return run_many<BF16, ZEROS, GS, MT, 1>(a, s);
+    if (a.N >= 128 * 200) return run_many<BF16, ZEROS, GS, MT, 2, 2>(a, s);
+  constexpr bool wide = BF16 ? MT <= 2 || (MT == 3 && GS == 4) : MT <= 3 || GS > 1;
+  return run_many<BF16, ZEROS, GS, MT, 1, wide ? 4 : 2>(a, s);
 }
 
 template <bool BF16, bool ZEROS, int GS>
