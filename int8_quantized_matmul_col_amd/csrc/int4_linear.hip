@@ -661,10 +661,11 @@ hipError_t run_many(const Int4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Two channel tiles a wave halve the reads of X, but need twice the channels
-// to fill the GPU (64 x 8192 x 28672: 50 us against 57 with one; 64 x 4096 x
-// 11008: 26.5 against 17.7).  bfloat16's 64 rows in groups of 32 have no
-// registers for it (64 x 8192 x 28672: 186 us spilling, 97 with one).
+// One channel tile a wave as long as one round of workgroups covers Y (64 x
+// 4096 x 11008: 17.7 us, 26.5 with two), else two, which also halve the reads of
+// X (64 x 4096 x 20000: 26.3 us, 33.8 with one; 64 x 8192 x 28672: 50 and 57).
+// bfloat16's 64 rows in groups of 32 have no registers for it (64 x 8192 x
+// 28672: 186 us spilling, 97 with one).
 //
 // Four tiles of K a step, 16 waves, where their 128 registers do (48 x 5120 x
 // 13811 in groups of 32 25 -> 22.8 us, 64 x 4096 x 16000 21.5 -> 20, never
@@ -673,7 +674,8 @@ hipError_t run_many(const Int4Args& a, hipStream_t s) {
 template <bool BF16, bool ZEROS, int GS, int MT>
 hipError_t pick_many(const Int4Args& a, hipStream_t s) {
   if constexpr (MT > 1 && !(BF16 && GS == 1 && MT == 4))
-    if (a.N >= 128 * 200) return run_many<BF16, ZEROS, GS, MT, 2, 2>(a, s);
+    if ((int64_t)((a.N + 63) / 64) * ((a.M + 63) / 64) > kCus)
+      return run_many<BF16, ZEROS, GS, MT, 2, 2>(a, s);
   constexpr bool wide = BF16 ? MT <= 2 || (MT == 3 && GS == 4) : MT <= 3 || GS > 1;
   return run_many<BF16, ZEROS, GS, MT, 1, wide ? 4 : 2>(a, s);
 }
