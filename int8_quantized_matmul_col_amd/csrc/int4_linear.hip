@@ -704,12 +704,14 @@ bool int4_few_rows(const uint16_t* X, int64_t M, int64_t K, int64_t ldx) {
   return M <= 16 && K % 8 == 0 && (ldx % 8 == 0 || M == 1) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
 }
 
-// Parts of K of the kernel for many rows: up to one round of workgroups, at
-// least 10 steps each (24 x 11008 x 4096: 15.1 us in 4 parts, 30 in one; 20 x
-// 4096 x 4096: 12.2 in one, 13.6 in 2).
+// Parts of K of the kernel for many rows: up to one round of workgroups, of at
+// least 20 tiles for up to 32 rows and 10 for 64, whose tiles take twice as long
+// (24 x 4096 x 4096: 11.5 us in one, 13.9 in 2; 60 x 4096 x 4096 in groups of
+// 32: 22.2 in one, 15.6 in 3; 24 x 11008 x 4096: 14.7 in 4, 18.1 in 2).
 int int4_k_parts(int64_t M, int64_t K, int64_t N) {
   const int64_t groups = ((N + 63) / 64) * ((M + 63) / 64);
-  const int64_t most = int4_tiles_k(K) / 20;
+  const int64_t row_tiles = M <= 32 ? 2 : M <= 48 ? 3 : 4;
+  const int64_t most = int4_tiles_k(K) * row_tiles / 40;
   int64_t z = groups > 0 ? kCus / groups : 1;
   if (z > most) z = most;
   return (int)(z < 1 ? 1 : z);
