@@ -18,11 +18,14 @@
 // and output cancels, so the maximum need not be exact.
 //
 // Precision: scores, maxima, sums and outputs are fp32.  A probability goes
-// to the matrix cores as two numbers of the operand type, its rounding and
-// the rest (16 or more bits together): the cores are far from bound, and the
-// result then differs from fp32 by its final rounding only.  int8 codes are
-// exact operands; the key's scale multiplies the fp32 score, the value's the
-// fp32 probability.
+// to the matrix cores as numbers of the operand type that add up to it: three
+// of bfloat16 (also for int8 values), which hold all its 24 bits, or two of
+// float16.  The cores are far from bound: 64 sequences of up to 8192 tokens,
+// int8, take 106 us with two bfloat16 parts and 108.5 with three, a bfloat16
+// cache the same with either.  Of the outputs 0.44% (131071 tokens, bfloat16)
+// and 2.3% (the int8 ones) were not the exact result's rounding with two, 0.05%
+// and 0.3% with three.  int8 codes are exact operands; the key's scale
+// multiplies the fp32 score, the value's the fp32 probability.
 //
 // The batch's tokens, one sequence after the other, are dealt out evenly to 512
 // workgroups (two on every CU), which find their sequences from the lengths;
@@ -67,24 +70,31 @@ __device__ __forceinline__ v4f mfma32(const v4u& a, const v4u& b, const v4f& c) 
                                                   __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// Two probabilities as a pair of the operand type from below and the pair of
-// what is left.  Both parts of a positive number are positive, so that an
-// infinite value stays one (its product with a remainder of 0, or with one of
-// the other sign, would be NaN).  float16's lower part comes off 2^-12 lower,
-// for a remainder of 2^-12 or more that float16 can hold.
-template <bool BF16>
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  constexpr uint32_t kBelow = BF16 ? 1u : 4096u;
-  const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), kBelow);
-  const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), kBelow);
+// Two probabilities as pairs of the operand type, each from below and then the
+// next of what is left: three of bfloat16 hold fp32's 24 bits, two of float16
+// 22.  All parts of a positive number are positive, so that an infinite value
+// stays one (its product with a remainder of 0, or with one of the other sign,
+// would be NaN).  float16's lower part comes off 2^-12 lower, for a remainder
+// of 2^-12 or more that float16 can hold.
+__device__ __forceinline__ uint32_t bf16_below(float& a, float& b) {
+  const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), 1u);
+  const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), 1u);
+  a -= __uint_as_float(ua & 0xffff0000u);
+  b -= __uint_as_float(ub & 0xffff0000u);
+  return __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+}
+template <bool BF16, int PARTS>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[PARTS]) {
   if constexpr (BF16) {
-    hi = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
-    const v2f l = {a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u)};
-    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(l, v2b));
+#pragma unroll
+    for (int i = 0; i < PARTS - 1; ++i) part[i] = bf16_below(a, b);
+    part[PARTS - 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2b));
   } else {
+    const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), 4096u);
+    const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), 4096u);
     const v2h h = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(ua), __uint_as_float(ub)));
-    hi = __builtin_bit_cast(uint32_t, h);
-    lo = f2h2(a - (float)h[0], b - (float)h[1]);
+    part[0] = __builtin_bit_cast(uint32_t, h);
+    part[1] = f2h2(a - (float)h[0], b - (float)h[1]);
   }
 }
 
@@ -187,6 +197,7 @@ template <int CT, bool QBF, int NK, bool EXACT>
 __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(KvAttentionArgs a, Pages pg) {
   constexpr bool I8 = CT == kI8;
   constexpr bool PBF = CT != kF16;      // type of the P x V operands
+  constexpr int kParts = PBF ? 3 : 2;   // that hold a probability
   constexpr int CH = I8 ? 64 : 32;      // tokens per chunk
   constexpr int SUB = CH / 4;           // consecutive tokens a lane feeds to P x V
   constexpr int NT = CH / 16;           // score tiles
@@ -462,29 +473,38 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
         for (int i = 0; i < DT; ++i) vr[i] &= keep;
       }
 
-      // P^T operand, in two parts
-      v4u ph[NT / 2], pl[NT / 2];
+      // P^T operand, in parts
+      v4u p[NT / 2][kParts];
 #pragma unroll
       for (int u = 0; u < NT / 2; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t hi, lo;
-          split2<PBF>(s[2 * u + e / 2][2 * (e & 1)], s[2 * u + e / 2][2 * (e & 1) + 1], hi, lo);
-          ph[u][e] = hi;
-          pl[u][e] = lo;
-        }
+          uint32_t x[kParts];
+          split<PBF>(s[2 * u + e / 2][2 * (e & 1)], s[2 * u + e / 2][2 * (e & 1) + 1], x);
 #pragma unroll
-      for (int i = 0; i < DT; ++i) {
+          for (int i = 0; i < kParts; ++i) p[u][i][e] = x[i];
+        }
+      // (two output tiles at a time: an instruction does not wait for the one
+      // before it; int8, 256 dims: 66 -> 63.8 us for 8 x 8192 tokens of 8 heads)
+#pragma unroll
+      for (int i = 0; i < DT; i += 2) {
         if constexpr (I8) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const v4u x = codes8<true>(vr[i][2 * u], vr[i][2 * u + 1]);
-            o[i] = mfma32<true>(x, ph[u], o[i]);
-            o[i] = mfma32<true>(x, pl[u], o[i]);
+            const v4u y = codes8<true>(vr[i + 1][2 * u], vr[i + 1][2 * u + 1]);
+#pragma unroll
+            for (int e = 0; e < kParts; ++e) {
+              o[i] = mfma32<true>(x, p[u][e], o[i]);
+              o[i + 1] = mfma32<true>(y, p[u][e], o[i + 1]);
+            }
           }
         } else {
-          o[i] = mfma32<PBF>(vr[i], ph[0], o[i]);
-          o[i] = mfma32<PBF>(vr[i], pl[0], o[i]);
+#pragma unroll
+          for (int e = 0; e < kParts; ++e) {
+            o[i] = mfma32<PBF>(vr[i], p[0][e], o[i]);
+            o[i + 1] = mfma32<PBF>(vr[i + 1], p[0][e], o[i + 1]);
+          }
         }
       }
       if (c + kWaves < chunks) load_v();
