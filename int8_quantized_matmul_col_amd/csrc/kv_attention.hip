@@ -20,8 +20,9 @@
 // Precision: scores, maxima, sums and outputs are fp32.  A probability goes
 // to the matrix cores as numbers of the operand type that add up to it: three
 // of bfloat16 (also for int8 values), which hold all its 24 bits, or two of
-// float16.  The cores are far from bound: 64 sequences of up to 8192 tokens,
-// int8, take 106 us with two bfloat16 parts and 108.5 with three, a bfloat16
+// float16 with sums of their own, which hold 22 of those that are at least 2^-20
+// of the maximum and end at 2^-42 of it.  The cores are far from bound: 64 sequences of up to 8192 tokens,
+// int8, take 106 us with two bfloat16 parts and 107 with three, a bfloat16
 // cache the same with either.  Of the outputs 0.44% (131071 tokens, bfloat16)
 // and 2.3% (the int8 ones) were not the exact result's rounding with two, 0.05%
 // and 0.3% with three.  int8 codes are exact operands; the key's scale
@@ -71,11 +72,15 @@ __device__ __forceinline__ v4f mfma32(const v4u& a, const v4u& b, const v4f& c) 
 }
 
 // Two probabilities as pairs of the operand type, each from below and then the
-// next of what is left: three of bfloat16 hold fp32's 24 bits, two of float16
-// 22.  All parts of a positive number are positive, so that an infinite value
-// stays one (its product with a remainder of 0, or with one of the other sign,
-// would be NaN).  float16's lower part comes off 2^-12 lower, for a remainder
-// of 2^-12 or more that float16 can hold.
+// next of what is left: three of bfloat16 hold fp32's 24 bits.  float16's
+// second part is held times kRest: float16 ends at 2^-24, and so a probability
+// of 2^-15 or less of the maximum would keep fewer than 16 bits, one of 2^-30
+// next to none, where another token has the maximum and no value.  All parts of
+// a positive number are positive, so that an infinite value stays one (its
+// product with a remainder of 0, or with one of the other sign, would be NaN);
+// float16's first part is rounded from 2^-12 lower, for a remainder of 2^-12 or
+// more.
+constexpr float kRest = 4096.0f;  // probabilities reach 2^14, their rest 2^3.6
 __device__ __forceinline__ uint32_t bf16_below(float& a, float& b) {
   const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), 1u);
   const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), 1u);
@@ -94,7 +99,7 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[PARTS])
     const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), 4096u);
     const v2h h = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(ua), __uint_as_float(ub)));
     part[0] = __builtin_bit_cast(uint32_t, h);
-    part[1] = f2h2(a - (float)h[0], b - (float)h[1]);
+    part[1] = f2h2((a - (float)h[0]) * kRest, (b - (float)h[1]) * kRest);
   }
 }
 
@@ -203,9 +208,10 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
   constexpr int NT = CH / 16;           // score tiles
   constexpr int NKL = I8 ? NK / 2 : NK;  // 16-byte key loads per token row and lane
   constexpr int DT = NK * 2;            // output tiles of 16 dims
+  constexpr int DR = PBF ? 1 : DT;      // output tiles of float16's second part
   constexpr int EB = I8 ? 1 : 2;
-  // float16 probabilities are held times 2^6: at most 2^14, and numbers down
-  // to 2^-30 of the maximum keep full precision
+  // float16 probabilities are held times 2^6, at most 2^14 (kSlack): with kRest
+  // their bits end at 2^-42 of the maximum, and those from 2^-20 on keep 22
   constexpr float kBias = CT == kF16 ? 6.0f : 0.0f;
   const int D = EXACT ? NK * 32 : pg.D;
 
@@ -331,9 +337,11 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
     }
   }
 
-  v4f o[DT];
+  v4f o[DT], rest[DR];
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = v4f{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < DR; ++i) rest[i] = v4f{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;
 
   if (wave < chunks) {
@@ -375,12 +383,17 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
         vsc = pg.vs[pv * pg.vs_page + kvh * pg.ps + vslot + r];
       }
     };
+    const uint32_t vrow = r * pg.ps * EB;
     auto load_v = [&]() __attribute__((always_inline)) {
+      // tiles as scalar offsets, formed anew each time: as lanes' offsets kept
+      // over the loop they take 24 registers, which 256 dims of float16 lack
+      uint32_t tile = 16 * pg.ps * EB;
+      asm volatile("" : "+s"(tile));
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        int d = i * 16 + r;
-        if (!EXACT) d = min(d, D - 1);  // rows past head_dim are not stored
-        vr[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(vptr + (int64_t)d * pg.ps * EB));
+        // (tiles past head_dim, which are not stored, read its last one)
+        const uint32_t at = (EXACT ? i : min(i, D / 16 - 1)) * tile;
+        vr[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(vptr + at + vrow));
       }
     };
 
@@ -445,6 +458,9 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
         l *= f;
 #pragma unroll
         for (int i = 0; i < DT; ++i) o[i] *= f;
+        if constexpr (!PBF)
+#pragma unroll
+          for (int i = 0; i < DT; ++i) rest[i] *= f;
       }
       const float base = m == -INFINITY ? 0.0f : m - kBias;
 #pragma unroll
@@ -499,11 +515,17 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
               o[i + 1] = mfma32<true>(y, p[u][e], o[i + 1]);
             }
           }
-        } else {
+        } else if constexpr (PBF) {
 #pragma unroll
           for (int e = 0; e < kParts; ++e) {
-            o[i] = mfma32<PBF>(vr[i], p[0][e], o[i]);
-            o[i + 1] = mfma32<PBF>(vr[i + 1], p[0][e], o[i + 1]);
+            o[i] = mfma32<true>(vr[i], p[0][e], o[i]);
+            o[i + 1] = mfma32<true>(vr[i + 1], p[0][e], o[i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = i; j < i + 2; ++j) {
+            o[j] = mfma32<false>(vr[j], p[0][0], o[j]);
+            rest[j] = mfma32<false>(vr[j], p[0][1], rest[j]);
           }
         }
       }
@@ -517,7 +539,11 @@ __global__ __launch_bounds__(64 * kWaves, NK <= 4 ? 2 : 1) void k_kv_attention(K
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) so[((wave * DT + i) * 4 + e) * 64 + lane] = o[i][e];
+    for (int e = 0; e < 4; ++e) {
+      float x = o[i][e];
+      if constexpr (!PBF) x += rest[i][e] * (1.0f / kRest);
+      so[((wave * DT + i) * 4 + e) * 64 + lane] = x;
+    }
   if (qd == 0) {
     sm[wave * 16 + r] = m;
     sl[wave * 16 + r] = l;

@@ -1,5 +1,7 @@
 """What kv_attention's probabilities carry into the sum over the values: values
-that cancel, so that the result's own rounding hides nothing."""
+that cancel, so that the result's own rounding hides nothing, and a token that
+dominates the softmax with a value of 0, so that what is left has small
+probabilities."""
 
 import math
 
@@ -87,3 +89,38 @@ def test_values_that_cancel(lib, cache, dtype):
     bound = U16[t] * np.abs(rest) + _error(T, 1.0, i8) * size + TINY[t]
     d = np.abs(got - rest)
     assert not (d > bound).any(), float((d / bound).max())
+
+
+@pytest.mark.parametrize("cache,dtype", TYPES)
+@pytest.mark.parametrize("below", [8, 11, 14, 16, 17, 18, 19])
+def test_small_probabilities_beside_a_token_without_value(lib, cache, dtype, below):
+    """One token's score is `below` above the others', and its value is 0."""
+    g = rng(52, below)
+    B, T = 64, 13
+    i8 = cache == "i8"
+    at = DTYPES.get(cache)
+    keys = np.full((B, T), -float(below)) + g.uniform(-0.5, 0.5, (B, T))
+    values = g.uniform(1e4, 6e4, (B, T, D)) * g.choice([-1, 1], (B, T, D))
+    keys[:, 3] = 0
+    ks = vs = np.ones((B, T))
+    if i8:
+        ks = np.full((B, T), 20.0)
+        keys = np.rint(keys * 127 / ks)
+        real = keys * ks / 127
+        vs = np.full((B, T), 6e4, np.float32)
+        values = np.rint(127 * values / 6e4)
+        held = values * vs[..., None].astype(np.float64) / 127
+    else:
+        keys = real = f64(dev(keys.astype(np.float32), at))
+        values = held = f64(dev(values.astype(np.float32), at))
+    values, held = values.copy(), held.copy()
+    values[:, 3] = held[:, 3] = 0
+    p = _probabilities(real)[..., None]
+    want, size = (p * held).sum(1), (p * np.abs(held)).sum(1)
+    got, t = _attend(lib, cache, dtype, keys, ks, values, vs)
+    # float16 operands end at 2^-24: with the factors 2^6 and 2^12 at 2^-42 of
+    # the largest probability, half of it in rounding
+    end = 2.0 ** -43 * np.abs(held).sum(1) if cache == "f16" else 0.0
+    bound = U16[t] * np.abs(want) + _error(T, below + 0.5, i8) * size + end + TINY[t]
+    d = np.abs(got - want)
+    assert not (d > bound * (1 + 2.0 ** -8)).any(), float((d / bound).max())
