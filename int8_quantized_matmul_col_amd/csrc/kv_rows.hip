@@ -103,7 +103,9 @@ __device__ __forceinline__ float group_absmax(const v4u& x) {
 // Codes of 8 values of scale a: r = 127/a and one fma a value where the result
 // is provably the same (see quant8_fast, whose bound holds for any two
 // floats), the division where a value lies near a tie or 127/a is no finite
-// number (a below 2^-121, infinite or NaN).
+// number (a below 2^-121, infinite or NaN).  The division forms 127 x, which
+// passes fp32's range for large bfloat16 numbers: there x and a are both taken
+// 2^-8 smaller, which leaves the quotient as it is.
 template <bool BF16>
 __device__ __forceinline__ v2u quantize(const v4u& x, float a) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
@@ -119,8 +121,9 @@ __device__ __forceinline__ v2u quantize(const v4u& x, float a) {
   }
   // (asked of the wave: the compiler would otherwise divide always and select)
   if (__any(dev > kTieGuard || !(r <= 3.0e38f) || (r == 0.0f && a > 0.0f))) {
+    const float f = BF16 && a > 0x1p120f ? 0x1p-8f : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = quant_code(value<BF16>(half_of(x, e)), a);
+    for (int e = 0; e < 8; ++e) q[e] = quant_code(f * value<BF16>(half_of(x, e)), f * a);
   }
   const uint2 p = pack8_i8(q);
   return v2u{p.x, p.y};

@@ -1,0 +1,33 @@
+"""What callers may pass to the serving operators: finite values of any size."""
+
+import numpy as np
+import pytest
+import torch
+
+from serving_cases import dev, f64
+from test_gpu_kv_cache import INT, _i32, _pool
+
+pytestmark = pytest.mark.gpu
+
+
+def test_large_finite_rows_of_an_int8_cache(lib):
+    """127 x passes fp32's range from 2.7e36 on; the code does not.  127 x / a =
+    10.5 lies on a tie, and ties send the codes through the division."""
+    a, x = 254 * 2.0 ** 120, 21 * 2.0 ** 120
+    kv = _pool(lib, 1, 1, 16, 64, "i8")
+    row = np.zeros((3, 64))
+    row[0, :8] = a, x, a / 3, -a / 5, 1e36, -1e30, 1.0, 0.0
+    row[1, :4] = 1, 0.5, -0.25, 0.1           # a row beside it
+    row[2, :4] = a, a / 3, -a / 7, a / 2
+    k = dev(row.astype(np.float32), torch.bfloat16).view(3, 1, 64)
+    rows, pos = torch.zeros(3, **INT), torch.arange(3, **INT)
+    lib.kv_append(k, k, kv, _i32([0]).view(1, 1), rows, pos)
+    held = f64(k)[:, 0]
+    top = np.abs(held).max(-1, keepdims=True)
+    want = np.rint(127 * held / top)
+    for got, scale in ((kv.k[0, 0, :3], kv.k_scale), (kv.v[0, 0, :, :3].t(), kv.v_scale)):
+        assert np.array_equal(f64(got), want)
+        assert np.array_equal(f64(scale)[0, 0, :3], top[:, 0])
+    out = lib.kv_gather(kv, _i32([0]).view(1, 1), rows, pos, dtype=torch.bfloat16)
+    for t in out:
+        assert torch.isfinite(t).all()
