@@ -18,9 +18,9 @@
  *
  * Limits (ESHAPE beyond): table_rows <= 2^30, table_width * page_size <= 2^30,
  * 1024 kv heads, 65536 query heads, 4096 layers, 2^30 bytes for a page's keys
- * in 16 bits; 2^28 tokens for a kv_append or kv_gather, B * q_heads < 2^24 for
- * a kv_attention, 16384 rows or pairs for a kv_pages_reserve or _fork, 2^23
- * rows for a kv_pages_free, 2^30 pairs for a kv_pages_copy.
+ * in 16 bits; 2^28 - 32 tokens for a kv_append or kv_gather, B * q_heads <
+ * 2^24 for a kv_attention, 16384 rows or pairs for a kv_pages_reserve or _fork,
+ * 2^23 rows for a kv_pages_free, 2^30 pairs for a kv_pages_copy.
  */
 #ifndef INT8MM_SERVING_H
 #define INT8MM_SERVING_H

@@ -22,10 +22,10 @@ namespace {
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr int kTok = 32;        // tokens per workgroup
+constexpr int kTok = kKvRowsTokens;  // per workgroup
 // Threads where a row has LN lanes: one pass up to 128 dims, two beyond (with
 // 256 threads 4000 int8 tokens of 8 x 256 dims take 32.7 us both ways, 30.2 so).
-constexpr int threads_of(int LN) { return kTok * LN < 512 ? kTok * LN : 512; }
+constexpr int threads_of(int LN) { return kTok * LN < kKvRowsThreads ? kTok * LN : kKvRowsThreads; }
 constexpr int kMaxD = INT8MM_KV_MAX_HEAD_DIM;
 
 struct Rows {

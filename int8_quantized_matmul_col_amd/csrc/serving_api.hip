@@ -12,7 +12,8 @@ constexpr size_t kAlign = 256;
 constexpr int64_t kMaxCount = (int64_t)1 << 30;  // int32 indexing in the kernels
 constexpr int64_t kMaxNamed = 16384;             // rows or pairs of one reserve or fork
 // a launch holds fewer than 2^32 threads
-constexpr int64_t kMaxTokens = (int64_t)1 << 28;
+constexpr int64_t kMaxTokens = (((int64_t)1 << 32) - 1) / i8mm::kKvRowsThreads * i8mm::kKvRowsTokens;
+static_assert(kMaxTokens == ((int64_t)1 << 28) - 32, "the limit that the header states");
 constexpr int64_t kMaxFreed = (int64_t)1 << 23;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

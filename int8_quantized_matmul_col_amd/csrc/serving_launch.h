@@ -40,6 +40,8 @@ bool int4_few_rows(const uint16_t* X, int64_t M, int64_t K, int64_t ldx);
 int int4_k_parts(int64_t M, int64_t K, int64_t N);
 
 // ---- key-value pages
+// Tokens, and the most threads, of a workgroup that writes or reads rows.
+constexpr int kKvRowsTokens = 32, kKvRowsThreads = 512;
 hipError_t launch_kv_append(const uint16_t* k, const uint16_t* v, bool bf16, int T, int64_t kts,
                             int64_t khs, int64_t vts, int64_t vhs, const int8mm_kv& kv,
                             const int32_t* table, int table_rows, int table_width,

@@ -259,3 +259,20 @@ def test_reference_pool_keeps_its_counts():
             for x in row[:used]:
                 count[x] += 1
         assert count == p.ref
+
+
+def test_token_counts_at_the_limit_of_a_launch(lib):
+    """The largest documented count is the last whose grid has fewer than 2^32
+    threads (32 tokens a workgroup of up to 512)."""
+    last = (1 << 28) - 32
+    assert -(-last // 32) * 512 < 1 << 32 <= -(-(last + 1) // 32) * 512
+    text = re.sub(r"\s+\*?\s*", " ", open(HEADER).read())
+    assert "2^28 - 32 tokens for a kv_append or kv_gather" in text
+    for T in (last + 1, 1 << 28):
+        assert lib.kv_append(FAKE, FAKE, 0, T, 128, 64, 128, 64, _kv(), FAKE, 2, 4, FAKE, FAKE,
+                             None) == ESHAPE
+        assert lib.kv_gather(FAKE, FAKE, 0, T, _kv(), FAKE, 2, 4, FAKE, FAKE, None) == ESHAPE
+    # up to there the arguments are looked at
+    assert lib.kv_append(FAKE, FAKE, 0, last, 128, 64, 128, 64, _kv(), FAKE, 2, 4, FAKE, FAKE + 2,
+                         None) == EINVAL
+    assert lib.kv_gather(FAKE, FAKE, 0, last, _kv(), FAKE, 2, 4, FAKE, FAKE + 2, None) == EINVAL
