@@ -4,6 +4,11 @@
 it holds the prepared 4-bit weight and the bias, nothing else, and its forward
 is one call.  Its place is a decode step, where the weight's bytes are what a
 layer costs; rows are taken 64 at a time.
+
+The prepared bytes do not say what they are (group_size 64 without and 128 with
+zero points, 250 and 256 inputs take the same number of them), so the state
+dict has the layer's format beside them, and a state of another format is not
+loaded.  A state without one (saved before there was any) is taken as it is.
 """
 
 from __future__ import annotations
@@ -35,6 +40,32 @@ class Int4Linear(torch.nn.Module):
         (quantized now)."""
         w = serving.int4_prepare_weight(linear.weight.detach().contiguous(), group_size, symmetric)
         return cls(w, linear.bias)
+
+    @property
+    def _format(self) -> dict:
+        return dict(in_features=self.in_features, out_features=self.out_features,
+                    group_size=self.group_size, zeros=bool(self.zeros))
+
+    def get_extra_state(self) -> torch.Tensor:
+        return torch.tensor(list(self._format.values()), dtype=torch.int64)
+
+    def set_extra_state(self, state) -> None:
+        pass  # compared before anything is loaded
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys,
+                              unexpected_keys, error_msgs):
+        key = prefix + "_extra_state"
+        if key in state_dict:
+            names, saved = self._format.keys(), state_dict[key].tolist()
+            if saved != [int(x) for x in self._format.values()]:
+                error_msgs.append(
+                    f"{prefix[:-1] or 'Int4Linear'}: the state is of {dict(zip(names, saved))}, "
+                    f"the layer of {self._format}")
+                return
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys,
+                                      unexpected_keys, error_msgs)
+        if key in missing_keys:
+            missing_keys.remove(key)
 
     @property
     def weight4(self) -> serving.Int4Weight:
