@@ -447,10 +447,11 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
         raise ValueError(f"{Hq} query heads do not divide over {kv.kv_heads} kv heads")
     sb, sh, sd = q.stride()
     if sd != 1 or sb % 8 or sh % 8 or q.data_ptr() % 16:
+        # (contiguous() leaves a view alone whose odd strides are of single rows)
         q = q.contiguous()
         if q.data_ptr() % 16:
-            q = q.clone()
-        sb, sh, _ = q.stride()
+            q = q.clone(memory_format=torch.contiguous_format)
+        sb, sh = Hq * D, D
     _check_table(table, dev)
     S, width = table.shape
     _indexes(lengths, "lengths", dev, (S,))

@@ -1,13 +1,29 @@
-"""What callers may pass to the serving operators: finite values of any size."""
+"""What callers may pass to the serving operators: views whose distances do not
+matter, finite values of any size."""
 
 import numpy as np
 import pytest
 import torch
 
-from serving_cases import dev, f64
+from serving_cases import Cache, dev, f64, rng
 from test_gpu_kv_cache import INT, _i32, _pool
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,Hq", [(1, 4), (1, 1), (3, 1)])
+def test_a_distance_that_is_never_used(lib, B, Hq):
+    """A dimension of size one may have any stride (a slice of wider rows), and
+    torch calls such a view contiguous."""
+    g = rng(71, B, Hq)
+    c = Cache(lib, g, [40, 17, 300][:B], 1, 64, 16, "f16")
+    q = dev(g.standard_normal((B, Hq, 64)).astype(np.float32), torch.float16)
+    want = lib.kv_attention(q, c.kv, c.table, c.len)
+    buf = torch.zeros(4096, dtype=torch.float16, device="cuda")
+    view = buf.as_strided((B, Hq, 64), (257 if B == 1 else Hq * 64, 257 if Hq == 1 else 64, 1))
+    view.copy_(q)
+    assert view.is_contiguous() and (view.stride(0) % 8 or view.stride(1) % 8)
+    assert torch.equal(lib.kv_attention(view, c.kv, c.table, c.len), want)
 
 
 def test_large_finite_rows_of_an_int8_cache(lib):
