@@ -140,6 +140,14 @@ def _indexes(t, name: str, device, shape=None) -> None:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _check_workspace(ws, device) -> None:
+    """A caller's workspace: its bytes follow one another on `device` (the
+    library looks at its size and alignment)."""
+    _on(ws, "workspace", device)
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 # ------------------------------------------------------------ 4-bit weights
 
 class Int4Weight(NamedTuple):
@@ -262,6 +270,8 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
         n = _lib().int4_linear_workspace_size(M, K, N)
         if n:
             workspace = X.new_empty((n // 4,), dtype=torch.float32)
+    elif workspace is not None:
+        _check_workspace(workspace, dev)
     _call("int4_linear", dev.index, X.data_ptr(), dt, M, K, ldx, w.Wq.data_ptr(), w.params.data_ptr(), N,
           w.group_size, w.zeros, None if bias is None else bias.data_ptr(), Y.data_ptr(),
           None if workspace is None else workspace.data_ptr(),
@@ -470,6 +480,8 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
         n = _lib().kv_attention_workspace_size(B, Hq, kv.kv_heads, D, max_len)
         if n:
             workspace = table.new_empty((n // 4,))
+    else:
+        _check_workspace(workspace, dev)
     _call("kv_attention", kv.index, q.data_ptr(), dt, B, Hq, sb, sh, kv._ref,
           table.data_ptr(), S, width, lengths.data_ptr(),
           None if rows is None else rows.data_ptr(), max_len,
@@ -489,6 +501,7 @@ def _pages_args(table, lengths, refcount, num_pages, device) -> None:
 
 def _pages_workspace(num_pages: int, n: int, device, workspace) -> torch.Tensor:
     if workspace is not None:
+        _check_workspace(workspace, device)
         return workspace
     size = _lib().kv_pages_workspace_size(num_pages, n)
     if size == 0:

@@ -47,3 +47,33 @@ def test_large_finite_rows_of_an_int8_cache(lib):
     out = lib.kv_gather(kv, _i32([0]).view(1, 1), rows, pos, dtype=torch.bfloat16)
     for t in out:
         assert torch.isfinite(t).all()
+
+
+def test_workspaces_that_are_none(lib):
+    """A workspace on the host, or one whose elements share memory."""
+    n = 1 << 22
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    c = Cache(lib, rng(72), [5], 2, 64, 16, "f16")
+    q = torch.ones((1, 4, 64), dtype=torch.float16, device="cuda")
+    codes = torch.zeros((64, 8192), dtype=torch.uint8, device="cuda")
+    w = lib.int4_pack_weight(codes, torch.ones((64, 64), dtype=torch.float16, device="cuda"), None, 128)
+    X = torch.zeros((20, 8192), dtype=torch.float16, device="cuda")
+    table, lengths = torch.full((3, 2), -1, **INT), torch.zeros(3, **INT)
+    kv, ref = _pool(lib, 4, 2, 16, 64, "f16"), torch.zeros(4, **INT)
+    a, b = _i32([0]), _i32([1])
+    wide = c.table.repeat(1, 5000)
+    for ws, error in ((torch.zeros(n, dtype=torch.uint8), ValueError), (one.expand(n), ValueError),
+                      (n, TypeError)):
+        for call in (lambda: lib.int4_linear(X, w, workspace=ws),
+                     lambda: lib.kv_attention(q, c.kv, wide, c.len, workspace=ws),
+                     lambda: lib.kv_pages_reserve(table, lengths, ref, a, b, 16, workspace=ws),
+                     lambda: lib.kv_pages_fork(kv, table, lengths, ref, a, b, workspace=ws),
+                     lambda: lib.kv_pages_compact(kv, table, ref, workspace=ws)):
+            with pytest.raises(error):
+                call()
+    # and one of the right kind is taken
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    assert not lib.int4_linear(X, w, workspace=ws).any()
+    assert torch.equal(lib.kv_attention(q, c.kv, wide, c.len, workspace=ws),
+                       lib.kv_attention(q, c.kv, wide, c.len))
+    assert lib.kv_pages_reserve(table, lengths, ref, a, b, 16, workspace=ws).tolist() == [0]
