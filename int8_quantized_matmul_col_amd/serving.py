@@ -15,6 +15,7 @@ kernels and there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -161,9 +162,15 @@ class Int4Weight(NamedTuple):
     zeros: bool
 
 
-def _int4_buffers(N: int, K: int, group: int, zeros: bool, device) -> Tuple:
+@functools.lru_cache(maxsize=None)
+def _int4_bytes(N: int, K: int, group: int, zeros: bool) -> Tuple[int, int]:
+    """int4_weight_bytes and int4_param_bytes (-1 where there is no such weight)."""
     lib = _lib()
-    nw, np_ = lib.int4_weight_bytes(N, K), lib.int4_param_bytes(N, K, group, int(zeros))
+    return lib.int4_weight_bytes(N, K), lib.int4_param_bytes(N, K, group, int(zeros))
+
+
+def _int4_buffers(N: int, K: int, group: int, zeros: bool, device) -> Tuple:
+    nw, np_ = _int4_bytes(N, K, group, zeros)
     if nw < 0 or np_ < 0:
         raise Int8mmError("int4_weight_bytes", INT8MM_ESHAPE)
     return (torch.empty((nw,), dtype=torch.uint8, device=device),
@@ -233,6 +240,20 @@ def int4_unpack_weight(w: Int4Weight) -> Tuple:
             (par[..., 1] - 1024).to(torch.uint8).contiguous() if w.zeros else None)
 
 
+def _check_weight(w: Int4Weight, device) -> None:
+    """Whether a weight's buffers lie on `device` and are what its fields say."""
+    for t, name in ((w.Wq, "Wq"), (w.params, "params")):
+        _require(t, torch.uint8, name, device)
+    sizes = _int4_bytes(*w[2:])
+    if min(sizes) < 0:
+        raise Int8mmError("int4_linear", INT8MM_ESHAPE)
+    if (w.Wq.numel(), w.params.numel()) != sizes:
+        raise ValueError(
+            f"the weight's buffers have {w.Wq.numel()} and {w.params.numel()} bytes, not the "
+            f"{sizes[0]} and {sizes[1]} of {w.out_features} x {w.in_features} codes in groups of "
+            f"{w.group_size}{' with zero points' if w.zeros else ''}")
+
+
 def int4_linear_workspace_size(M: int, K: int, N: int) -> int:
     return int(_lib().int4_linear_workspace_size(int(M), int(K), int(N)))
 
@@ -242,28 +263,36 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
     (rows may be strided), bias [N] of the same type or None.  Returns [M][N]
     of X's type, rounded once.  Meant for few rows (M up to 64 reads the weight
     once)."""
-    dt = _row_dtype(X, "X")
-    _on(X, "X")
-    dev = X.device
-    if X.dim() != 2 or X.shape[1] != w.in_features:
-        raise ValueError(f"X has shape {tuple(X.shape)}, expected [M][{w.in_features}]")
-    if w.Wq.device != dev:
-        raise ValueError(f"the weight is on {w.Wq.device}, expected {dev}")
-    M, K = X.shape
-    N = w.out_features
+    dt = _DTYPES.get(X.dtype)
+    index = X.get_device()
+    if dt is None or index < 0:
+        _row_dtype(X, "X")
+        _on(X, "X")
+    Wq, params, N, K, group, zeros = w
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"X has shape {tuple(shape)}, expected [M][{K}]")
+    # the buffers are read by what the fields say: one look at what is nearly
+    # always right
+    if not (Wq.__class__ is params.__class__ is torch.Tensor
+            and Wq.get_device() == params.get_device() == index
+            and (Wq.numel(), params.numel()) == _int4_bytes(N, K, group, zeros)
+            and Wq.is_contiguous() and params.is_contiguous()):
+        _check_weight(w, X.device)
+    M = shape[0]
     if M > 0 and K > 1 and X.stride(1) != 1:
         raise ValueError("the rows of X must be contiguous")
     ldx = X.stride(0) if M > 1 else K
     if ldx < K:
         raise ValueError("the rows of X must not overlap")
     if bias is not None:
-        _require(bias, X.dtype, "bias", dev)
+        _require(bias, X.dtype, "bias", X.device)
         if bias.numel() != N:
             raise ValueError(f"bias has {bias.numel()} entries, expected {N}")
     if out is None:
         Y = X.new_empty((M, N))
     else:
-        _check_out(out, (M, N), X.dtype, "out", dev)
+        _check_out(out, (M, N), X.dtype, "out", X.device)
         Y = out
     # up to 16 rows on 16 bytes need no workspace
     if workspace is None and (M > 16 or K % 8 or ldx % 8 or X.data_ptr() % 16):
@@ -271,9 +300,9 @@ def int4_linear(X, w: Int4Weight, bias=None, out=None, workspace=None):
         if n:
             workspace = X.new_empty((n // 4,), dtype=torch.float32)
     elif workspace is not None:
-        _check_workspace(workspace, dev)
-    _call("int4_linear", dev.index, X.data_ptr(), dt, M, K, ldx, w.Wq.data_ptr(), w.params.data_ptr(), N,
-          w.group_size, w.zeros, None if bias is None else bias.data_ptr(), Y.data_ptr(),
+        _check_workspace(workspace, X.device)
+    _call("int4_linear", index, X.data_ptr(), dt, M, K, ldx, Wq.data_ptr(), params.data_ptr(), N,
+          group, zeros, None if bias is None else bias.data_ptr(), Y.data_ptr(),
           None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.nbytes)
     return Y

@@ -49,6 +49,29 @@ def test_large_finite_rows_of_an_int8_cache(lib):
         assert torch.isfinite(t).all()
 
 
+def test_buffers_that_are_not_the_weight(lib):
+    """Nothing is launched with buffers elsewhere, or smaller than the sizes say."""
+    codes = torch.zeros((40, 300), dtype=torch.uint8, device="cuda")
+    w = lib.int4_pack_weight(codes, torch.ones((40, 5), dtype=torch.float16, device="cuda"), None, 64)
+    X = torch.zeros((2, 300), dtype=torch.float16, device="cuda")
+    assert not lib.int4_linear(X, w).any()
+    small = w.Wq[:1024]
+    for bad in (dict(Wq=w.Wq.cpu()), dict(params=w.params.cpu()), dict(Wq=small),
+                dict(Wq=small[:1].expand(w.Wq.shape)), dict(params=w.params[:-2]),
+                dict(params=w.params[::2]), dict(out_features=4096), dict(group_size=32),
+                dict(zeros=True), dict(group_size=64, zeros=True)):
+        with pytest.raises(ValueError):
+            lib.int4_linear(X, w._replace(**bad))
+    with pytest.raises(ValueError):
+        lib.int4_linear(torch.zeros((2, 400), dtype=torch.float16, device="cuda"),
+                        w._replace(in_features=400))
+    for group in (0, -64, 48, 96):
+        with pytest.raises((ValueError, lib.Int8mmError)):
+            lib.int4_linear(X, w._replace(group_size=group))
+    with pytest.raises(TypeError):
+        lib.int4_linear(X, w._replace(params=None))
+
+
 def test_workspaces_that_are_none(lib):
     """A workspace on the host, or one whose elements share memory."""
     n = 1 << 22
