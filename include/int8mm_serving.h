@@ -199,9 +199,12 @@ INT8MM_API size_t kv_attention_workspace_size(int64_t B, int64_t q_heads, int64_
  * No visible token (L <= 0, a row out of range, scores that are all -inf):
  * out 0, lse -inf.  Tokens in pages whose id is out of range are not visible.
  * What the pages hold outside [lo, L) does not matter, NaN included; inside
- * it, infinities and NaN propagate.  Sums, maxima and scores are fp32; a
- * result does not depend on what else is in the batch, except through the
- * split that B, max_len and the head counts choose.
+ * it, infinities and NaN propagate.  Sums, maxima and scores are fp32.
+ * Where max_len is above 256 (and the window, if there is one, above 193), the
+ * places at which sequences are cut into parts go by the head counts, B,
+ * max_len and the lengths of all rows of the call, so another sequence's length
+ * may change how this one's sums are rounded.  What other sequences hold never
+ * does, and the same call gives the same bits again.
  * Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.
  */
 INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads,

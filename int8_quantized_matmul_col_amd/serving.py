@@ -473,7 +473,8 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
     c * tanh(s / c); max_len is an upper bound of the lengths that the host
     knows (default: what the table holds).  Returns out [B][q_heads][head_dim]
     of q's type, with return_lse also log-sum-exp float32 [B][q_heads].  A
-    sequence without visible tokens gives 0 and -inf."""
+    sequence without visible tokens gives 0 and -inf.  Above 256 visible tokens
+    other rows' lengths may change how a row's sums are rounded."""
     _one_layer(kv)
     dev = kv.device
     dt = kv.row_dtype(q.dtype, "q")

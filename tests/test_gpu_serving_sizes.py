@@ -98,6 +98,11 @@ def test_a_sequence_beside_others(lib, cache, dtype):
         t[pages] = t[pages].flip(0)
     out, lse = attend(lengths)
     assert torch.equal(out[0], first[0][0]) and torch.equal(lse[0], first[1][0])
+    # up to 256 tokens nothing is cut, and the bits are the same beside any others
+    rows = _i32([2, 0, 3])
+    short = [lib.kv_attention(q[:3], c.kv, c.table, _i32(n), rows=rows, max_len=256)
+             for n in ([200, 0, 150, 0], [256, 0, 150, 7])]
+    assert torch.equal(short[0][0], short[1][0])
 
 
 PAGES = [  # pages of several slices, whole and ragged
