@@ -105,7 +105,10 @@ INT8MM_API size_t int4_linear_workspace_size(int64_t M, int64_t K, int64_t N);
  * Meant for the few rows of a decode step: rows are taken 64 at a time, and
  * each 64 read the weight once.  An infinity or NaN in X (or in a scale) makes
  * what depends on it infinite or NaN, which of the two is unspecified, and
- * nothing else.  M == 0 or N == 0: nothing to do.  K == 0: Y = bias, or 0.  Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.
+ * nothing else.  In bfloat16 rows finite numbers of 2^113 or more may do the
+ * same: the sums are formed with codes 128 larger, and the rest comes off them.
+ * M == 0 or N == 0: nothing to do.  K == 0: Y = bias, or 0.  Errors: EINVAL,
+ * ESHAPE, EWORKSPACE, EHIP.
  */
 INT8MM_API int int4_linear(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx,
                            const void* Wq, const void* params, int64_t N, int64_t group, int zeros,

@@ -10,10 +10,13 @@
 // Codes become MFMA operands without a table or a convert: a nibble or-ed
 // into the mantissa of a fixed exponent is an exact number.  float16 rows:
 // 1024 + q (or 1024 + 16 q), of which one packed add (fma) makes q - 8, exact.
-// bfloat16 rows: 128 + q, and the constant comes off the group's sum, as z
-// does in both types: sum x (c + q) - (c + z) sum x, with sum x from one more
-// MFMA against ones.  Products of the codes are exact and sums are fp32; the
-// group's scale multiplies the fp32 sum, so nothing is rounded before Y.
+// bfloat16 rows: 128 + q, and the constant comes off the group's sum with z:
+// sum x (128 + q) - (128 + z) sum x, with sum x from one more MFMA against ones.
+// Products of the codes are exact, sums are fp32 and the group's scale
+// multiplies the fp32 sum: the one rounding to fewer bits is Y's.  The offset
+// costs a sum about 4 of fp32's 24 bits, since its terms x (128 + q) are up to
+// 18 times (143 / 8) those of the result, whose rounding keeps 8; and it ends
+// the range where 128 terms of 143 |x| pass fp32's, above |x| = 2^113.
 #include <type_traits>
 
 #include "device_common.h"

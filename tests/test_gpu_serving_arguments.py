@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from serving_cases import Cache, dev, f64, rng
+from test_gpu_int4 import _case, _check
 from test_gpu_kv_cache import INT, _i32, _pool
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,19 @@ def test_workspaces_that_are_none(lib):
     assert torch.equal(lib.kv_attention(q, c.kv, wide, c.len, workspace=ws),
                        lib.kv_attention(q, c.kv, wide, c.len))
     assert lib.kv_pages_reserve(table, lengths, ref, a, b, 16, workspace=ws).tolist() == [0]
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M", [3, 20])
+def test_large_bfloat16_rows_of_a_4_bit_product(lib, M, zeros):
+    """The stated range: any bfloat16 number below 2^113."""
+    g = rng(73, M)
+    for group, K in ((32, 256), (128, 256), (256, 1024)):
+        X, codes, scales, z = _case(g, M, K, 70, group, zeros, "bf16")
+        top = float(np.float32(2.0 ** 113 * (1 - 2.0 ** -8)))
+        X = torch.where(X > 0, top, -top).to(torch.bfloat16)
+        X[0] = X[0].abs()
+        w = lib.int4_pack_weight(dev(codes), dev(scales), None if z is None else dev(z), group)
+        Y = lib.int4_linear(X, w)
+        assert torch.isfinite(Y).all() and float(X.abs().max()) < 2.0 ** 113
+        _check(Y, X, codes, scales, z, group)
