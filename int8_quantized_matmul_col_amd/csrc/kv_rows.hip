@@ -105,7 +105,9 @@ __device__ __forceinline__ float group_absmax(const v4u& x) {
 // floats), the division where a value lies near a tie or 127/a is no finite
 // number (a below 2^-121, infinite or NaN).  The division forms 127 x, which
 // passes fp32's range for large bfloat16 numbers: there x and a are both taken
-// 2^-8 smaller, which leaves the quotient as it is.
+// 2^-8 smaller, which leaves the quotient as it is (a branch of its own: 4000
+// tokens of 8 x 128 dims 12.45 us, 12.65 with the factor in every division,
+// 12.2 without).
 template <bool BF16>
 __device__ __forceinline__ v2u quantize(const v4u& x, float a) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
@@ -121,9 +123,14 @@ __device__ __forceinline__ v2u quantize(const v4u& x, float a) {
   }
   // (asked of the wave: the compiler would otherwise divide always and select)
   if (__any(dev > kTieGuard || !(r <= 3.0e38f) || (r == 0.0f && a > 0.0f))) {
-    const float f = BF16 && a > 0x1p120f ? 0x1p-8f : 1.0f;
+    if (BF16 && __any(a > 0x1p120f)) {
+      const float f = a > 0x1p120f ? 0x1p-8f : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = quant_code(f * value<BF16>(half_of(x, e)), f * a);
+      for (int e = 0; e < 8; ++e) q[e] = quant_code(f * value<BF16>(half_of(x, e)), f * a);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = quant_code(value<BF16>(half_of(x, e)), a);
+    }
   }
   const uint2 p = pack8_i8(q);
   return v2u{p.x, p.y};
