@@ -253,12 +253,13 @@ __global__ __launch_bounds__(64 * max_waves(P)) void k_int4_few(
 // and alignment takes this one path.  Where few channels leave CUs idle K is
 // split over workgroups too (blockIdx.z), and a second kernel adds their sums.
 //
-// 64 x 8192 x 28672 takes 50 us, of which 28 are the matrix instructions and
+// 64 x 8192 x 28672 takes 50.5 us, of which 28 are the matrix instructions and
 // the groups' scales alone (1.1 of the 1.2 PFLOP/s that a large library product
 // reaches here), 10 the codes and LDS, the rest the loads; 48 x 5120 x 13811 in
-// groups of 32 takes 21.5 to 23 us (24 to 26 with 8 waves, whose LDS reads,
-// codes and matrix instructions hide one another less; 33 with K in two parts),
-// 64 x 4096 x 11008 17.7.
+// groups of 32 takes 22 to 23 us, 64 x 4096 x 11008 18.3.  Every wave forms
+// bfloat16's sums of X for itself, one matrix instruction for each useful one
+// with one channel tile: 64 x 8192 x 28672 takes 58 us in bfloat16, and 95 in
+// groups of 32 (58 in float16).
 template <bool BF16, bool ZEROS, int GS, int MT, int P, int KS>
 __global__ __launch_bounds__(256 * KS) void k_int4_many(
     const uint16_t* __restrict__ X, int M, int K, int64_t ldx, int vec,
@@ -632,9 +633,10 @@ hipError_t run_few(const Int4Args& a, hipStream_t s) {
 
 // P tiles of channels per wave, so that one round of workgroups covers N with
 // one on every CU: X is read once per workgroup, from the L2, and that is what
-// small P costs; large P leaves CUs idle (1 x 8192 x 28672: 23.5 us with 7 and
-// 256 workgroups, 27.3 with 4, 32 with 1; 1 x 11008 x 4096: 9.7 us with 1, 17.1
-// with 4).
+// small P costs; large P leaves CUs idle (1 x 8192 x 28672: 24.5 us with 7 and
+// 256 workgroups, 26.9 with 4, 34.3 with 1, 16 rows 26.4 and 70.2 with 1; 1 x
+// 11008 x 4096: 8.1 us with 1, 15.1 with 4).  Where that would be 6, 7 are taken:
+// an instance with 6 would take 20.2 us for 1 x 8192 x 22000, this one 21.3.
 template <bool BF16, bool ZEROS, int GS>
 hipError_t pick_few(const Int4Args& a, hipStream_t s) {
   const int P = ((a.N + 15) / 16 + kCus - 1) / kCus;
@@ -665,15 +667,18 @@ hipError_t run_many(const Int4Args& a, hipStream_t s) {
 }
 
 // One channel tile a wave as long as one round of workgroups covers Y (64 x
-// 4096 x 11008: 17.7 us, 26.5 with two), else two, which also halve the reads of
-// X (64 x 4096 x 20000: 26.3 us, 33.8 with one; 64 x 8192 x 28672: 50 and 57).
-// bfloat16's 64 rows in groups of 32 have no registers for it (64 x 8192 x
-// 28672: 186 us spilling, 97 with one).
+// 4096 x 11008: 18.5 us, 25.5 with two; 48 x 5120 x 13811 in groups of 32: 22.3
+// and 33), else two, which also halve the reads of X (64 x 4096 x 20000: 27.7
+// us, 35 with one; 64 x 8192 x 28672: 51 and 63; 1000 x 4096 x 11008: 155 and
+// 186).  bfloat16's 64 rows in groups of 32 have no registers for it (64 x 8192
+// x 28672: 186 us spilling, 95 with one).
 //
-// Four tiles of K a step, 16 waves, where their 128 registers do (48 x 5120 x
-// 13811 in groups of 32 25 -> 22.8 us, 64 x 4096 x 16000 21.5 -> 20, never
-// slower from K = 512 on), otherwise two and 8 waves (64 x 4096 x 11008
-// bfloat16 in groups of 32: 27.5 us, 121 spilling with 16).
+// Four tiles of K a step, 16 waves, where their 128 registers do (with two and 8
+// waves, whose LDS reads, codes and matrix instructions hide one another less,
+// 48 x 5120 x 13811 in groups of 32 takes 25.5 us instead of 23.2, 64 x 4096 x
+// 16000 21 instead of 20, 20 x 3333 x 5000 32.2 instead of 24.7; up to K = 1024
+// the two are within 2%), otherwise two and 8 waves (64 x 4096 x 11008 bfloat16
+// in groups of 32: 27 us, 121 spilling with 16).
 template <bool BF16, bool ZEROS, int GS, int MT>
 hipError_t pick_many(const Int4Args& a, hipStream_t s) {
   if constexpr (MT > 1 && !(BF16 && GS == 1 && MT == 4))
@@ -708,9 +713,13 @@ bool int4_few_rows(const uint16_t* X, int64_t M, int64_t K, int64_t ldx) {
 }
 
 // Parts of K of the kernel for many rows: up to one round of workgroups, of at
-// least 20 tiles for up to 32 rows and 10 for 64, whose tiles take twice as long
-// (24 x 4096 x 4096: 11.5 us in one, 13.9 in 2; 60 x 4096 x 4096 in groups of
-// 32: 22.2 in one, 15.6 in 3; 24 x 11008 x 4096: 14.7 in 4, 18.1 in 2).
+// least 20 tiles for up to 32 rows, 14 for 48 and 10 for 64, whose tiles take
+// longer.  Microseconds, the part count that this gives first:
+//   24 x 4096 x 4096   1: 10.8, 3: 12.2     24 x 11008 x 4096  4: 14, 2: 17.6, 1: 25.3
+//   48 x 2048 x 4096   1: 8.4, 2: 11.6      48 x 4096 x 4096   2: 12.2, 1: 14.4, 4: 12
+//   48 x 8192 x 1024   4: 12, 2: 16.4, 1: 23.9, 9: 11.7
+//   64 x 2048 x 2048   1: 9.7, 3: 11.7      60 x 8192 x 1024   6: 13, 3: 16.2, 1: 28.3, 12: 13.9
+//   60 x 4096 x 4096 in groups of 32        3: 14.7, 1: 21, 4: 13.4
 int int4_k_parts(int64_t M, int64_t K, int64_t N) {
   const int64_t groups = ((N + 63) / 64) * ((M + 63) / 64);
   const int64_t row_tiles = M <= 32 ? 2 : M <= 48 ? 3 : 4;

@@ -4,7 +4,9 @@
 //
 // What bounds it: every key and value is read once from HBM; 4 flops per
 // element and query head, which the matrix cores have in plenty for up to 16
-// query heads on one kv head.
+// query heads on one kv head.  More are taken 16 at a time, and each 16 read the
+// cache again (4 x 32768 tokens of one kv head: 26 us for 16 query heads, 46 for
+// 64).
 //
 // One wave takes a chunk of 32 tokens (64 of an int8 cache) of one kv head at
 // a time.  Scores are K x Q^T tiles: the 16 rows are tokens, the 16 columns
@@ -21,18 +23,18 @@
 // to the matrix cores as numbers of the operand type that add up to it: three
 // of bfloat16 (also for int8 values), which hold all its 24 bits, or two of
 // float16 with sums of their own, which hold 22 of those that are at least 2^-20
-// of the maximum and end at 2^-42 of it.  The cores are far from bound: 64 sequences of up to 8192 tokens,
-// int8, take 106 us with two bfloat16 parts and 107 with three, a bfloat16
-// cache the same with either.  Of the outputs 0.44% (131071 tokens, bfloat16)
-// and 2.3% (the int8 ones) were not the exact result's rounding with two, 0.05%
-// and 0.3% with three.  int8 codes are exact operands; the key's scale
-// multiplies the fp32 score, the value's the fp32 probability.
+// of the maximum and end at 2^-42 of it.  The cores are far from bound: 64
+// sequences of up to 8192 tokens, int8, take 106 us with two bfloat16 parts and
+// 107 with three, a bfloat16 cache the same with either.  Of the outputs 0.44%
+// (131071 tokens, bfloat16) and 2.3% (the int8 ones) were not the exact result's
+// rounding with two, 0.05% and 0.3% with three.  int8 codes are exact operands;
+// the key's scale multiplies the fp32 score, the value's the fp32 probability.
 //
 // The batch's tokens, one sequence after the other, are dealt out evenly to 512
 // workgroups (two on every CU), which find their sequences from the lengths;
 // a workgroup's 4 waves take its chunks in turn.  So very different lengths
 // cost nothing (64 sequences of 1..8192 tokens, int8: 150 us with pieces of
-// one length, 103 to 110 so, 5.1 TB/s), and one long sequence is split as well
+// one length, 105 to 109 so, 5.2 TB/s), and one long sequence is split as well
 // (131071 tokens: 62 us; 384 workgroups take 73, 768 take 66).  Waves join in
 // LDS, cut sequences in a second kernel, each in a fixed order.  Where no
 // sequence can be longer than 256 tokens each is one workgroup's, and there is
@@ -676,7 +678,7 @@ hipError_t run(const KvAttentionArgs& a, const Pages& pg, hipStream_t s) {
 
 // Head sizes that are whole 32-dim steps (int8: 64) have instances without
 // idle registers and tiles: an int8 cache of 8 x 8192 tokens, 8 kv heads of
-// 192 / 256 dims, is read at 3.8 / 4.2 TB/s so, 3.2 / 3.8 with the general
+// 192 / 256 dims, is read at 3.8 / 4.1 TB/s so, 3.2 / 3.8 with the general
 // one; 17 sequences of up to 1000 tokens of 6 x 96 dims take 19.1 us, 20.2 with
 // the general one.  Other sizes, and 32 and 160 dims, lose up to the same.
 template <int CT, bool QBF>

@@ -3,13 +3,15 @@
 // device, so that a serving loop neither waits for the GPU nor copies them.
 //
 // Bound by HBM where pages move (each read and written once), else by the
-// launch: copy and free are one kernel, the others two.  The first of the two
-// snapshots which pages are free: one bit a page, a running count per 64-page
-// word and a count per 4096-page block.  From these any thread of the second
-// kernel finds the i-th free (or used) page by two binary searches, so pages
-// are handed out lowest id first without a list, a queue or an atomic, and
-// the result does not depend on timing.  Only reference counts use atomics
-// (integer additions, whose order does not matter).
+// launches (copy and free are one kernel, the others two) and, in reserve and
+// fork, by the plan: one workgroup compares every row named with every other
+// (32 pairs 6.7 us, 64 rows 13, of 16 us for the whole reserve call).  The first
+// of the two kernels snapshots which pages are free: one bit a page, a running
+// count per 64-page word and a count per 4096-page block.  From these any thread
+// of the second kernel finds the i-th free (or used) page by two binary
+// searches, so pages are handed out lowest id first without a list, a queue or
+// an atomic, and the result does not depend on timing.  Only reference counts
+// use atomics (integer additions, whose order does not matter).
 #include "device_common.h"
 #include "serving_launch.h"
 

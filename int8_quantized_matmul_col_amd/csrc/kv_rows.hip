@@ -2,13 +2,13 @@
 // reading them back as rows.
 //
 // Bound by HBM for a prompt (each element read and written once; 16000 tokens
-// of 8 x 128 dims to an int8 cache and back 50 us, 3.9 TB/s) and by the launch
-// for the tokens of one decode step (4.6 us on the GPU for 64).  A workgroup
-// takes up to 32 tokens of one kv head.  Keys are rows on both sides.  Values
-// are rows on one side and [dim][token] in the page, so they turn in LDS;
-// wherever 8 tokens of the workgroup lie side by side in a page (a prompt) they
-// are one 16-byte (int8: 8-byte) access, otherwise (a decode step) each token's
-// element is its own.
+// of 8 x 128 dims to an int8 cache and back 51 us, 3.9 TB/s) and by the launch
+// for the tokens of one decode step (4.2 us on the GPU for 64, 5.8 into an int8
+// cache).  A workgroup takes up to 32 tokens of one kv head.  Keys are rows on
+// both sides.  Values are rows on one side and [dim][token] in the page, so they
+// turn in LDS; wherever 8 tokens of the workgroup lie side by side in a page (a
+// prompt) they are one 16-byte (int8: 8-byte) access, otherwise (a decode step)
+// each token's element is its own.
 //
 // An int8 cache: a = max |x| over the token's dims of the head, code =
 // clamp(rne(127 x / a), -127, 127), the quantizer of the int8 matmul.
