@@ -78,10 +78,10 @@ __device__ __forceinline__ v4f mfma32(const v4u& a, const v4u& b, const v4f& c) 
 // second part is held times kRest: float16 ends at 2^-24, and so a probability
 // of 2^-15 or less of the maximum would keep fewer than 16 bits, one of 2^-30
 // next to none, where another token has the maximum and no value.  All parts of
-// a positive number are positive, so that an infinite value stays one (its
-// product with a remainder of 0, or with one of the other sign, would be NaN);
-// float16's first part is rounded from 2^-12 lower, for a remainder of 2^-12 or
-// more.
+// a positive number are positive (float16: down to 2^-30 of the maximum), so
+// that an infinite value stays one: its product with a part of 0, or with one
+// of the other sign, would be NaN.  float16's first part is rounded from 2^-12
+// lower, for a remainder of 2^-12 or more.
 constexpr float kRest = 4096.0f;  // probabilities reach 2^14, their rest 2^3.6
 __device__ __forceinline__ uint32_t bf16_below(float& a, float& b) {
   const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), 1u);

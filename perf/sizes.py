@@ -81,6 +81,15 @@ def gather_f16():
     return sets, {"bytes": 4 * 4000 * 8 * 128 * 2, "flops": 0}
 
 
+def pack_weight(N, K, group):
+    sets = []
+    for _ in range(3):
+        codes = torch.randint(0, 16, (N, K), device="cuda", dtype=torch.uint8)
+        scales = torch.rand((N, K // group), device="cuda").half()
+        sets.append(lambda c=codes, s=scales: mm.int4_pack_weight(c, s, None, group))
+    return sets, {"bytes": N * K * 3 // 2 + N * (K // group) * 4, "flops": 0}
+
+
 def prepare_weight(N, K, group, symmetric):
     w = [torch.randn((N, K), device="cuda").half() for _ in range(3)]
     return ([lambda x=x: mm.int4_prepare_weight(x, group, symmetric) for x in w],
@@ -106,6 +115,7 @@ def fork(cache):
 
 OTHERS = [
     ("gather prompt 4000 tokens 8 heads of 128 f16", gather_f16),
+    ("int4_pack_weight 28672x8192 g128", lambda: pack_weight(28672, 8192, 128)),
     ("int4_prepare_weight 28672x8192 g128", lambda: prepare_weight(28672, 8192, 128, True)),
     ("int4_prepare_weight 28672x8192 g32 zeros", lambda: prepare_weight(28672, 8192, 32, False)),
     ("reserve 64 rows of 2048 pages", lambda: reserve(64, 2048)),
