@@ -284,6 +284,52 @@ INT8MM_API int kv_pages_compact(const int8mm_kv* kv, const int32_t* table, int32
                                 int32_t* refcount_out, int32_t* n_live, void* workspace,
                                 size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------- queries and keys by position --
+ *
+ * A rotation turns pairs of a head's first rot_dim dims: pair i of a token at
+ * position p by the angle p * inv_freq[i] (radians).
+ */
+#define INT8MM_ROPE_MAX_DIM 256
+#define INT8MM_ROPE_HALF 0        /* pair i: dims i and rot_dim / 2 + i */
+#define INT8MM_ROPE_INTERLEAVED 1 /* pair i: dims 2 i and 2 i + 1 */
+
+/*
+ * rope_prepare -- frequencies (float64 [n], radians per position) as 64-bit
+ * fractions of a turn, round(inv_freq / (2 pi) * 2^64) modulo 2^64, which
+ * qk_rope takes: p times it, modulo 2^64, is the angle at any int32 p, also a
+ * negative one.  A frequency of 2^20 or more, or NaN, becomes 0.
+ * 0 <= n <= 128.  Errors: EINVAL, ESHAPE, EHIP.
+ */
+INT8MM_API int rope_prepare(const double* inv_freq, int64_t n, uint64_t* turns,
+                            hipStream_t stream);
+
+/*
+ * qk_rope -- each head's norm and the rotation, in one pass over queries and keys:
+ *
+ *   y = x * (mean over the head's dims of x^2 + eps)^(-1/2) * weight
+ *   (a, b) -> (factor (a cos - b sin), factor (b cos + a sin)) of each pair
+ *
+ *   q, k  [T][heads][head_dim] of `dtype` (F16 or BF16), any token and head
+ *         distances in elements; k_heads 0: no keys, k may be NULL.
+ *   positions [T] int32; turns [rot_dim / 2] of rope_prepare (NULL for 0).
+ *   q_weight, k_weight [head_dim] of `dtype`; NULL: no norm there.
+ *   q_out, k_out: the same shapes with distances of their own, heads apart from
+ *         one another.  Either may be its input, with the same distances;
+ *         otherwise outputs overlap nothing.
+ * head_dim even, 2 .. 256; rot_dim even, 0 .. head_dim; eps > 0 where there is
+ * a weight.  fp32 throughout, rounded once; squares beyond fp32 are no matter.
+ * T <= 2^22, T * (q_heads + k_heads) <= 2^28, 4096 heads each.
+ * T == 0 or no heads: nothing to do.  Errors: EINVAL, ESHAPE, EHIP.
+ */
+INT8MM_API int qk_rope(const void* q, const void* k, int dtype, int64_t T, int64_t q_heads,
+                       int64_t k_heads, int64_t head_dim, int64_t q_token_stride,
+                       int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                       const int32_t* positions, const uint64_t* turns, int64_t rot_dim,
+                       int layout, float factor, const void* q_weight, const void* k_weight,
+                       float eps, void* q_out, void* k_out, int64_t q_out_token_stride,
+                       int64_t q_out_head_stride, int64_t k_out_token_stride,
+                       int64_t k_out_head_stride, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

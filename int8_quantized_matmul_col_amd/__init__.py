@@ -52,6 +52,7 @@ from .binding import (  # noqa: F401
 from .kv_cache import PagedKVCache  # noqa: F401
 from .linear import Int8Linear, replace_linear_with_int8  # noqa: F401
 from .linear4 import Int4Linear  # noqa: F401
+from .rope import Rotary, qk_rope, rope_prepare, rotary, rotary_frequencies  # noqa: F401
 from .stats import outlier_stats, suggest_threshold  # noqa: F401
 from .serving import (  # noqa: F401
     INT8MM_KV_BAD_ROW,

@@ -1,0 +1,432 @@
+// Queries and keys turned by their positions, with each head's norm before it.
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w            (where there is a weight)
+//   (a, b) -> factor * (a cos - b sin, b cos + a sin),  angle = position * inv_freq
+//
+// over the pairs of the first rot_dim dims, in fp32, rounded once.
+//
+// Angles.  A position times a frequency is needed modulo one turn.  Frequencies
+// are kept as 64-bit fractions of a turn (rope_prepare), so that a 64-bit
+// integer product that wraps is the angle itself, off by at most 2^-33 turns at
+// any 32-bit position: no table by position, no reduction of large floats.  Its
+// upper 32 bits give the quadrant and the rest, and two short series the sine
+// and the cosine.  A token's rot_dim / 2 of them are formed once by a workgroup
+// and shared by all its heads through LDS.
+//
+// Work.  A lane takes two runs of VEC elements that pair up (16 bytes each where
+// sizes and alignment allow): the i-th of both halves, or two neighbouring ones
+// of the interleaved layout and of the dims behind rot_dim.  With norms the
+// lanes of one head are a power of two that reduce within themselves; without,
+// the runs of all heads follow one another and no lane is idle.  Halves, heads or
+// addresses of odd lengths take a plain kernel, a wave a head.
+#include "device_common.h"
+#include "serving_launch.h"
+
+namespace i8mm {
+
+namespace {
+
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;  // of a workgroup
+constexpr float kTurn32 = 1.46291807926715968e-9f;  // 2 pi / 2^32
+
+template <int VEC>
+struct Run {
+  uint32_t w[VEC / 2];
+};
+
+template <int VEC>
+__device__ __forceinline__ Run<VEC> load_run(const uint16_t* p) {
+  Run<VEC> r;
+  if constexpr (VEC == 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+  } else if constexpr (VEC == 4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x; r.w[1] = v.y;
+  } else {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ void store_run(uint16_t* p, const Run<VEC>& r) {
+  if constexpr (VEC == 8)
+    *reinterpret_cast<uint4*>(p) = uint4{r.w[0], r.w[1], r.w[2], r.w[3]};
+  else if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(p) = uint2{r.w[0], r.w[1]};
+  else
+    *reinterpret_cast<uint32_t*>(p) = r.w[0];
+}
+template <bool BF16>
+__device__ __forceinline__ float value(uint32_t w, int odd) {
+  if constexpr (BF16)
+    return __uint_as_float(odd ? w & 0xffff0000u : w << 16);
+  else
+    return h2f((uint16_t)(odd ? w >> 16 : w));
+}
+template <bool BF16, int VEC>
+__device__ __forceinline__ void widen(const Run<VEC>& r, float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) x[i] = value<BF16>(r.w[i / 2], i & 1);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  if constexpr (BF16)
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2b));
+  else
+    return f2h2(a, b);
+}
+template <bool BF16, int VEC>
+__device__ __forceinline__ Run<VEC> narrow(const float (&x)[VEC]) {
+  Run<VEC> r;
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) r.w[i] = round2<BF16>(x[2 * i], x[2 * i + 1]);
+  return r;
+}
+
+// Cosine and sine of a fraction of a turn (in 2^-64), times factor.
+__device__ __forceinline__ float2 turned(uint64_t phase, float factor) {
+  const uint32_t h = (uint32_t)(phase >> 32);
+  const uint32_t quarter = (h + 0x20000000u) >> 30;     // the nearest quarter turn
+  const float x = (float)(int32_t)(h - (quarter << 30)) * kTurn32;  // +- pi / 4
+  const float s = x * x;
+  // the series of sin and cos; what follows is below 2^-28 of 1 at pi / 4
+  float sn = __builtin_fmaf(s, 2.75573192e-6f, -1.98412698e-4f);
+  sn = __builtin_fmaf(s, sn, 8.33333333e-3f);
+  sn = __builtin_fmaf(s, sn, -1.66666667e-1f);
+  sn = __builtin_fmaf(s * x, sn, x);
+  float cs = __builtin_fmaf(s, -2.75573192e-7f, 2.48015873e-5f);
+  cs = __builtin_fmaf(s, cs, -1.38888889e-3f);
+  cs = __builtin_fmaf(s, cs, 4.16666667e-2f);
+  cs = __builtin_fmaf(s, cs, -0.5f);
+  cs = __builtin_fmaf(s, cs, 1.0f);
+  float c = quarter & 1 ? sn : cs, d = quarter & 1 ? cs : sn;
+  if (quarter == 1 || quarter == 2) c = -c;
+  if (quarter >= 2) d = -d;
+  return float2{c * factor, d * factor};
+}
+
+__device__ __forceinline__ float group_sum(float x, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+
+struct RopeShape {
+  int tokens;    // of a workgroup
+  int heads;     // of a workgroup (blockIdx.y: which), queries before keys
+  int units;     // runs' pairs of a head
+  int lanes;     // NORM: of a head, a power of two
+  uint32_t per;  // 2^32 / heads, rounded up
+};
+
+template <bool BF16, int VEC, bool INTER, bool NORM>
+__global__ __launch_bounds__(kThreads) void k_qk_rope(QkRopeArgs a, RopeShape g) {
+  extern __shared__ float2 turn[];  // [tokens][rot / 2]
+  const int t0 = blockIdx.x * g.tokens;
+  const int nt = min(g.tokens, a.T - t0);
+  const int half = a.rot / 2;
+  const int head0 = blockIdx.y * g.heads;
+  const int H = min(g.heads, a.q_heads + a.k_heads - head0);
+  const int pairs = nt * H;  // (token, head)
+
+  // this lane's first place, and what a step of the workgroup adds
+  int at, unit, step_at, step_unit;
+  if constexpr (NORM) {
+    at = threadIdx.x / g.lanes, unit = threadIdx.x & (g.lanes - 1);
+    step_at = kThreads / g.lanes, step_unit = 0;
+  } else {
+    at = threadIdx.x / g.units, unit = threadIdx.x % g.units;
+    step_at = kThreads / g.units, step_unit = kThreads % g.units;
+  }
+
+  struct Place {
+    int token, head, ea, eb, turn;  // ea, eb: the runs' first elements; turn: of its pairs, or -1
+    bool ok;
+  };
+  auto place = [&](int at, int unit) __attribute__((always_inline)) {
+    Place p;
+    p.ok = at < pairs && unit < g.units;
+    p.token = H == g.heads ? (int)__umulhi((uint32_t)at, g.per) : at / H;
+    if (g.heads == 1) p.token = at;  // (2^32 / 1 is not in 32 bits)
+    p.head = at - p.token * H + head0;
+    const int rotated = a.rot / (2 * VEC);
+    if (unit < rotated) {
+      p.ea = INTER ? unit * 2 * VEC : unit * VEC;
+      p.eb = INTER ? p.ea + VEC : half + p.ea;
+      p.turn = p.token * half + unit * VEC;
+    } else {
+      p.ea = unit * 2 * VEC;
+      p.eb = p.ea + VEC;
+      p.turn = -1;
+    }
+    return p;
+  };
+  auto source = [&](const Place& p) __attribute__((always_inline)) {
+    return p.head < a.q_heads
+               ? a.q + (int64_t)(t0 + p.token) * a.q_token + (int64_t)p.head * a.q_head
+               : a.k + (int64_t)(t0 + p.token) * a.k_token + (int64_t)(p.head - a.q_heads) * a.k_head;
+  };
+
+  Run<VEC> wa[2], wb[2];  // the weights of queries and of keys at this lane's dims
+  if constexpr (NORM) {
+    const Place p = place(at, min(unit, g.units - 1));
+    if (a.q_weight != nullptr) {
+      wa[0] = load_run<VEC>(a.q_weight + p.ea);
+      wb[0] = load_run<VEC>(a.q_weight + p.eb);
+    }
+    if (a.k_weight != nullptr) {
+      wa[1] = load_run<VEC>(a.k_weight + p.ea);
+      wb[1] = load_run<VEC>(a.k_weight + p.eb);
+    }
+  }
+
+  constexpr int kU = 2;  // places in flight
+  Place p[kU];
+  Run<VEC> ra[kU], rb[kU];
+  auto next = [&](int u) __attribute__((always_inline)) {
+    p[u] = place(at, unit);
+    if (p[u].ok) {
+      const uint16_t* x = source(p[u]);
+      ra[u] = load_run<VEC>(x + p[u].ea);
+      rb[u] = load_run<VEC>(x + p[u].eb);
+    }
+    at += step_at;
+    unit += step_unit;
+    if (!NORM && unit >= g.units) unit -= g.units, ++at;
+  };
+  // the first loads, before the angles
+#pragma unroll
+  for (int u = 0; u < kU; ++u) next(u);
+
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int token = i / half, j = i - token * half;
+    turn[i] = turned((uint64_t)(int64_t)a.positions[t0 + token] * a.turns[j], a.factor);
+  }
+  __syncthreads();
+
+  // (a wave's lanes leave together: the reduction needs all of a head's)
+  while (__any(p[0].ok)) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const Place c = p[u];
+      float x[VEC], y[VEC];
+      if (c.ok) {
+        widen<BF16>(ra[u], x);
+        widen<BF16>(rb[u], y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = y[i] = 0.0f;
+      }
+      next(u);
+      if constexpr (NORM) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ss = __builtin_fmaf(x[i], x[i], __builtin_fmaf(y[i], y[i], ss));
+        ss = group_sum(ss, g.lanes);
+        float rs = rsqrtf(__builtin_fmaf(ss, a.inv_dim, a.eps));
+        if (__any(!(ss < 1e38f))) {
+          // bfloat16 reaches squares beyond fp32: those of 2^-70 of the head
+          float low = 0.0f;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float p = x[i] * 0x1p-70f, q = y[i] * 0x1p-70f;
+            low = __builtin_fmaf(p, p, __builtin_fmaf(q, q, low));
+          }
+          low = group_sum(low, g.lanes);
+          if (!(ss < 1e38f)) rs = rsqrtf(low * a.inv_dim) * 0x1p-70f;
+        }
+        const int key = c.head >= a.q_heads;
+        if ((key ? a.k_weight : a.q_weight) != nullptr) {
+          float w[VEC], v[VEC];
+          widen<BF16>(key ? wa[1] : wa[0], w);
+          widen<BF16>(key ? wb[1] : wb[0], v);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            x[i] = x[i] * rs * w[i];
+            y[i] = y[i] * rs * v[i];
+          }
+        }
+      }
+      if (c.ok) {
+        if (c.turn >= 0) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float2 t = turn[c.turn + i];
+            if constexpr (!INTER) {
+              const float r = x[i] * t.x - y[i] * t.y;
+              y[i] = y[i] * t.x + x[i] * t.y;
+              x[i] = r;
+            } else {
+              // pairs 0 .. VEC / 2 - 1 lie in x, the others in y
+              float* z = i < VEC / 2 ? x : y;
+              const int e = 2 * i % VEC;
+              const float r = z[e] * t.x - z[e + 1] * t.y;
+              z[e + 1] = z[e + 1] * t.x + z[e] * t.y;
+              z[e] = r;
+            }
+          }
+        }
+        uint16_t* out = c.head < a.q_heads
+                            ? a.q_out + (int64_t)(t0 + c.token) * a.qo_token + (int64_t)c.head * a.qo_head
+                            : a.k_out + (int64_t)(t0 + c.token) * a.ko_token + (int64_t)(c.head - a.q_heads) * a.ko_head;
+        store_run<VEC>(out + c.ea, narrow<BF16>(x));
+        store_run<VEC>(out + c.eb, narrow<BF16>(y));
+      }
+    }
+  }
+}
+
+// Any even head_dim and rot_dim, any strides: a wave takes a head, a lane its
+// pairs lane and lane + 64.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void k_qk_rope_any(QkRopeArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int H = a.q_heads + a.k_heads, half = a.rot / 2;
+  const int64_t waves = (int64_t)gridDim.x * (kThreads / 64);
+  for (int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); at < (int64_t)a.T * H; at += waves) {
+    const int token = (int)(at / H), head = (int)(at % H);
+    const bool key = head >= a.q_heads;
+    const uint16_t* in = key ? a.k + token * a.k_token + (head - a.q_heads) * a.k_head
+                             : a.q + token * a.q_token + head * a.q_head;
+    uint16_t* out = key ? a.k_out + token * a.ko_token + (head - a.q_heads) * a.ko_head
+                        : a.q_out + token * a.qo_token + head * a.qo_head;
+    const uint16_t* w = key ? a.k_weight : a.q_weight;
+    const uint64_t pos = (uint64_t)(int64_t)a.positions[token];
+    float x[2], y[2], ss = 0.0f, low = 0.0f;
+    int ea[2], eb[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = lane + 64 * u;
+      const bool split = i < half && !a.interleaved;
+      ea[u] = split ? i : 2 * i;
+      eb[u] = split ? half + i : 2 * i + 1;
+      x[u] = y[u] = 0.0f;
+      if (2 * i < a.D) {
+        x[u] = value<BF16>(in[ea[u]], 0);
+        y[u] = value<BF16>(in[eb[u]], 0);
+      }
+      ss = __builtin_fmaf(x[u], x[u], __builtin_fmaf(y[u], y[u], ss));
+      const float p = x[u] * 0x1p-70f, q = y[u] * 0x1p-70f;
+      low = __builtin_fmaf(p, p, __builtin_fmaf(q, q, low));
+    }
+    float rs = 1.0f;
+    if (w != nullptr) {
+      ss = group_sum(ss, 64);
+      low = group_sum(low, 64);
+      rs = ss < 1e38f ? rsqrtf(__builtin_fmaf(ss, a.inv_dim, a.eps)) : rsqrtf(low * a.inv_dim) * 0x1p-70f;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = lane + 64 * u;
+      if (2 * i >= a.D) continue;
+      if (w != nullptr) {
+        x[u] = x[u] * rs * value<BF16>(w[ea[u]], 0);
+        y[u] = y[u] * rs * value<BF16>(w[eb[u]], 0);
+      }
+      if (i < half) {
+        const float2 t = turned(pos * a.turns[i], a.factor);
+        const float r = x[u] * t.x - y[u] * t.y;
+        y[u] = y[u] * t.x + x[u] * t.y;
+        x[u] = r;
+      }
+      const uint32_t r = round2<BF16>(x[u], y[u]);
+      out[ea[u]] = (uint16_t)r;
+      out[eb[u]] = (uint16_t)(r >> 16);
+    }
+  }
+}
+
+// inv_freq in radians -> 64-bit fractions of a turn, to the nearest but for
+// what 1 / (2 pi) in 107 bits leaves.
+__global__ void k_rope_prepare(const double* __restrict__ inv_freq, int n, uint64_t* __restrict__ turns) {
+#pragma clang fp contract(off)  // (p rounded, and what that took)
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+  const double x = inv_freq[i];
+  if (!(fabs(x) < 0x1p20)) {  // (the host cannot see it; the header names the range)
+    turns[i] = 0;
+    return;
+  }
+  const double p = x * kHi;
+  const double e = fma(x, kHi, -p) + x * kLo;
+  // whole turns do not matter: the upper part is exact in 64 bits after them
+  const double f = p - floor(p);
+  const double scaled = f * 0x1p32;
+  const double top = floor(scaled);
+  const double rest = (scaled - top) * 0x1p32 + e * 0x1p64;
+  turns[i] = ((uint64_t)top << 32) + (uint64_t)(int64_t)rint(rest);
+}
+
+template <bool BF16, int VEC, bool INTER, bool NORM>
+hipError_t run(const QkRopeArgs& a, hipStream_t s) {
+  const int H = a.q_heads + a.k_heads;
+  RopeShape g;
+  g.units = a.D / (2 * VEC);
+  g.lanes = 1;
+  while (g.lanes < g.units) g.lanes *= 2;
+  const int64_t work = (int64_t)H * (NORM ? g.lanes : g.units);  // lanes that a token takes
+  // Enough tokens a workgroup for four of its steps, as long as 1024 workgroups
+  // remain (four on every CU); a token of more than 16 steps is dealt to several.
+  int tokens = 1;
+  while (tokens < kMaxTokens && tokens * work < 4 * kThreads && a.T / (2 * tokens) >= 1024) tokens *= 2;
+  g.tokens = tokens;
+  int parts = 1;
+  if (tokens == 1) parts = (int)((work + 16 * kThreads - 1) / (16 * kThreads));
+  g.heads = (H + parts - 1) / parts;
+  g.per = (uint32_t)((((uint64_t)1 << 32) + g.heads - 1) / g.heads);
+  const dim3 grid((unsigned)((a.T + tokens - 1) / tokens), (unsigned)((H + g.heads - 1) / g.heads));
+  const size_t lds = (size_t)tokens * (a.rot / 2) * sizeof(float2);
+  hipLaunchKernelGGL((k_qk_rope<BF16, VEC, INTER, NORM>), grid, dim3(kThreads), lds, s, a, g);
+  return hipGetLastError();
+}
+
+template <bool BF16, int VEC>
+hipError_t pick(const QkRopeArgs& a, hipStream_t s) {
+  const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
+  if (a.interleaved) return norm ? run<BF16, VEC, true, true>(a, s) : run<BF16, VEC, true, false>(a, s);
+  return norm ? run<BF16, VEC, false, true>(a, s) : run<BF16, VEC, false, false>(a, s);
+}
+
+template <bool BF16>
+hipError_t pick(const QkRopeArgs& a, int vec, hipStream_t s) {
+  switch (vec) {
+    case 8: return pick<BF16, 8>(a, s);
+    case 4: return pick<BF16, 4>(a, s);
+    case 2: return pick<BF16, 2>(a, s);
+  }
+  int64_t blocks = ((int64_t)a.T * (a.q_heads + a.k_heads) + kThreads / 64 - 1) / (kThreads / 64);
+  if (blocks > 1 << 16) blocks = 1 << 16;
+  hipLaunchKernelGGL(k_qk_rope_any<BF16>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rope_prepare(const double* inv_freq, int n, uint64_t* turns, hipStream_t s) {
+  hipLaunchKernelGGL(k_rope_prepare, dim3((n + 63) / 64), dim3(64), 0, s, inv_freq, n, turns);
+  return hipGetLastError();
+}
+
+hipError_t launch_qk_rope(const QkRopeArgs& a, bool bf16, hipStream_t s) {
+  // the longest run that sizes, strides and addresses allow
+  auto fits = [&](int v) {
+    if ((a.D - a.rot) % (2 * v) != 0 || (a.interleaved ? a.rot % (2 * v) : a.rot / 2 % v) != 0) return false;
+    const int64_t strides[] = {a.q_token, a.q_head, a.k_token, a.k_head, a.qo_token, a.qo_head, a.ko_token, a.ko_head};
+    for (const int64_t x : strides)
+      if (x % v != 0) return false;
+    const void* ptrs[] = {a.q, a.k, a.q_out, a.k_out, a.q_weight, a.k_weight};
+    for (const void* x : ptrs)
+      if (reinterpret_cast<uintptr_t>(x) % (2 * v) != 0) return false;
+    return true;
+  };
+  int vec = 8;
+  while (vec > 1 && !fits(vec)) vec /= 2;
+  return bf16 ? pick<true>(a, vec, s) : pick<false>(a, vec, s);
+}
+
+}  // namespace i8mm

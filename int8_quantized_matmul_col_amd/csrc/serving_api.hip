@@ -99,6 +99,18 @@ int64_t head_groups(int64_t q_heads, int64_t kv_heads) {
   return kv_heads * ((group + i8mm::kKvHeadTile - 1) / i8mm::kKvHeadTile);
 }
 
+// ------------------------------------------- queries and keys by position
+
+// Whether the heads of an output [T][heads][D] lie apart.
+bool rows_apart(int64_t T, int64_t heads, int64_t D, int64_t token, int64_t head) {
+  if (heads == 0) return true;
+  if (T > 1 && token < D) return false;
+  if (heads > 1 && head < D) return false;
+  if (T <= 1 || heads <= 1) return true;
+  // one distance steps over all of the other's
+  return token >= head ? token >= head * (heads - 1) + D : head >= token * (T - 1) + D;
+}
+
 }  // namespace
 
 extern "C" {
@@ -367,6 +379,78 @@ INT8MM_API int kv_pages_compact(const int8mm_kv* kv, const int32_t* table, int32
   return status_of(i8mm::launch_kv_pages_compact(*kv, table, table_out, (int)table_rows,
                                                  (int)table_width, refcount, refcount_out, n_live,
                                                  workspace, stream));
+}
+
+INT8MM_API int rope_prepare(const double* inv_freq, int64_t n, uint64_t* turns,
+                            hipStream_t stream) {
+  if (n < 0 || n > INT8MM_ROPE_MAX_DIM / 2) return INT8MM_ESHAPE;
+  if (n == 0) return INT8MM_OK;
+  if (inv_freq == nullptr || turns == nullptr || !aligned(inv_freq, 8) || !aligned(turns, 8))
+    return INT8MM_EINVAL;
+  return status_of(i8mm::launch_rope_prepare(inv_freq, (int)n, turns, stream));
+}
+
+INT8MM_API int qk_rope(const void* q, const void* k, int dtype, int64_t T, int64_t q_heads,
+                       int64_t k_heads, int64_t head_dim, int64_t q_token_stride,
+                       int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                       const int32_t* positions, const uint64_t* turns, int64_t rot_dim,
+                       int layout, float factor, const void* q_weight, const void* k_weight,
+                       float eps, void* q_out, void* k_out, int64_t q_out_token_stride,
+                       int64_t q_out_head_stride, int64_t k_out_token_stride,
+                       int64_t k_out_head_stride, hipStream_t stream) {
+  if (dtype != INT8MM_F16 && dtype != INT8MM_BF16) return INT8MM_EINVAL;
+  if (layout != INT8MM_ROPE_HALF && layout != INT8MM_ROPE_INTERLEAVED) return INT8MM_EINVAL;
+  if (head_dim < 2 || head_dim > INT8MM_ROPE_MAX_DIM || head_dim % 2 != 0 || rot_dim < 0 ||
+      rot_dim > head_dim || rot_dim % 2 != 0)
+    return INT8MM_ESHAPE;
+  if (T < 0 || T > ((int64_t)1 << 22) || q_heads < 0 || q_heads > 4096 || k_heads < 0 ||
+      k_heads > 4096 || T * (q_heads + k_heads) > ((int64_t)1 << 28))
+    return INT8MM_ESHAPE;
+  if (!isfinite(factor)) return INT8MM_EINVAL;
+  if ((q_weight != nullptr || k_weight != nullptr) && !(eps > 0.0f && isfinite(eps))) return INT8MM_EINVAL;
+  if (T == 0 || q_heads + k_heads == 0) return INT8MM_OK;
+  if (positions == nullptr || !aligned(positions, 4)) return INT8MM_EINVAL;
+  if (rot_dim > 0 && (turns == nullptr || !aligned(turns, 8))) return INT8MM_EINVAL;
+  if (q_heads > 0 && (q == nullptr || q_out == nullptr)) return INT8MM_EINVAL;
+  if (k_heads > 0 && (k == nullptr || k_out == nullptr)) return INT8MM_EINVAL;
+  const void* ptrs[] = {q, k, q_out, k_out, q_weight, k_weight};
+  for (const void* p : ptrs)
+    if (!aligned(p, 2)) return INT8MM_EINVAL;
+  i8mm::QkRopeArgs a{};
+  // distances that are never stepped do not count
+  auto token = [&](int64_t x, int64_t heads) { return T > 1 && heads > 0 ? x : 0; };
+  auto head = [&](int64_t x, int64_t heads) { return heads > 1 ? x : 0; };
+  a.q_token = token(q_token_stride, q_heads);
+  a.k_token = token(k_token_stride, k_heads);
+  a.qo_token = token(q_out_token_stride, q_heads);
+  a.ko_token = token(k_out_token_stride, k_heads);
+  a.q_head = head(q_head_stride, q_heads);
+  a.k_head = head(k_head_stride, k_heads);
+  a.qo_head = head(q_out_head_stride, q_heads);
+  a.ko_head = head(k_out_head_stride, k_heads);
+  if (!rows_apart(T, q_heads, head_dim, a.qo_token, a.qo_head) ||
+      !rows_apart(T, k_heads, head_dim, a.ko_token, a.ko_head))
+    return INT8MM_EINVAL;
+  if (q_heads > 0 && q == q_out && (a.q_token != a.qo_token || a.q_head != a.qo_head)) return INT8MM_EINVAL;
+  if (k_heads > 0 && k == k_out && (a.k_token != a.ko_token || a.k_head != a.ko_head)) return INT8MM_EINVAL;
+  a.q = q_heads > 0 ? static_cast<const uint16_t*>(q) : nullptr;
+  a.k = k_heads > 0 ? static_cast<const uint16_t*>(k) : nullptr;
+  a.q_out = q_heads > 0 ? static_cast<uint16_t*>(q_out) : nullptr;
+  a.k_out = k_heads > 0 ? static_cast<uint16_t*>(k_out) : nullptr;
+  a.q_weight = q_heads > 0 ? static_cast<const uint16_t*>(q_weight) : nullptr;
+  a.k_weight = k_heads > 0 ? static_cast<const uint16_t*>(k_weight) : nullptr;
+  a.positions = positions;
+  a.turns = turns;
+  a.T = (int)T;
+  a.q_heads = (int)q_heads;
+  a.k_heads = (int)k_heads;
+  a.D = (int)head_dim;
+  a.rot = (int)rot_dim;
+  a.interleaved = layout == INT8MM_ROPE_INTERLEAVED;
+  a.factor = factor;
+  a.eps = eps;
+  a.inv_dim = 1.0f / (float)head_dim;
+  return status_of(i8mm::launch_qk_rope(a, dtype == INT8MM_BF16, stream));
 }
 
 }  // extern "C"

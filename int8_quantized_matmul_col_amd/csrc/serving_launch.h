@@ -77,6 +77,24 @@ struct KvAttentionArgs {
 hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm_kv& kv,
                                hipStream_t s);
 
+// ---- queries and keys by their positions
+struct QkRopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  const uint16_t* q_weight;  // or null: no norm
+  const uint16_t* k_weight;
+  const int32_t* positions;
+  const uint64_t* turns;
+  int64_t q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head;  // elements
+  int T, q_heads, k_heads, D, rot;
+  bool interleaved;
+  float factor, eps, inv_dim;
+};
+hipError_t launch_rope_prepare(const double* inv_freq, int n, uint64_t* turns, hipStream_t s);
+hipError_t launch_qk_rope(const QkRopeArgs& a, bool bf16, hipStream_t s);
+
 size_t kv_pages_workspace(int64_t num_pages, int64_t n);
 hipError_t launch_kv_pages_copy(const int8mm_kv& kv, const int32_t* src, const int32_t* dst, int n,
                                 hipStream_t s);

@@ -74,6 +74,9 @@ SIGNATURES = {
     "kv_pages_fork": (_INT, [_KV, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     "kv_pages_free": (_INT, [_I32, _P, _I64, _I64, _P, _P, _P, _I64, _P]),
     "kv_pages_compact": (_INT, [_KV, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "rope_prepare": (_INT, [_P, _I64, _P, _P]),
+    "qk_rope": (_INT, [_P, _P, _INT] + [_I64] * 8 + [_P, _P, _I64, _INT, _F, _P, _P, _F, _P, _P]
+                + [_I64] * 4 + [_P]),
 }
 
 _fns: Optional[ctypes.CDLL] = None

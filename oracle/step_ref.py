@@ -1,0 +1,43 @@
+"""CPU reference of the operators around a decode step's attention, numpy
+float64 and whole numbers (test infrastructure).  Nothing here shares code
+with the package.
+"""
+
+from __future__ import annotations
+
+import math
+from fractions import Fraction
+
+import numpy as np
+
+# 1 / (2 pi), to 60 digits
+_INV_2PI = Fraction("0.159154943091895335768883763372514362034459645740456448747667")
+FAR = 64.0  # a token less likely than the likeliest by e^-64 is never drawn
+
+
+# -------------------------------------------- queries and keys by position
+
+def angles(positions, inv_freq):
+    """cos, sin [T][n] of position * frequency, reduced in rational numbers."""
+    turns = [[float(Fraction(float(f)) * int(p) * _INV_2PI % 1) for f in inv_freq]
+             for p in positions]
+    a = 2 * math.pi * np.array(turns, np.float64).reshape(len(positions), len(inv_freq))
+    return np.cos(a), np.sin(a)
+
+
+def rope(x, positions, inv_freq, layout, factor, weight, eps):
+    """x float64 [T][H][D] -> (y, mag): the rotated heads, and |a| + |b| of each
+    result's pair after the norm (times factor where it is turned)."""
+    x = x.astype(np.float64)
+    rot = 2 * len(inv_freq)
+    if weight is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * weight
+    y, mag = x.copy(), np.abs(x)
+    cos, sin = angles(positions, inv_freq)
+    for i in range(rot // 2):
+        m, n = (i, rot // 2 + i) if layout == "half" else (2 * i, 2 * i + 1)
+        c, s = cos[:, i, None], sin[:, i, None]
+        y[..., m] = factor * (x[..., m] * c - x[..., n] * s)
+        y[..., n] = factor * (x[..., n] * c + x[..., m] * s)
+        mag[..., m] = mag[..., n] = abs(factor) * (np.abs(x[..., m]) + np.abs(x[..., n]))
+    return y, mag

@@ -1,0 +1,210 @@
+"""qk_rope against the definition in 64 bits: layouts, parts of a head, norms,
+scaled frequencies, strides, in place, far positions."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import serving_cases as sc
+from oracle import step_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def check(got, x, pos, inv, layout, factor, w, eps):
+    """The head's sum of squares has D terms, its root halves their error; the
+    root, the weight, the two products and their sum round once each; cosine
+    and sine are off by at most 3 u32 (the angle's two roundings, at most
+    pi / 4 of them, the series and its last rounding), the factor rounds again."""
+    D = x.shape[-1]
+    want, mag = ref.rope(sc.f64(x), pos, inv, layout, factor,
+                         None if w is None else sc.f64(w), eps)
+    err = mag * ((D / 2 + 12) * sc.U32)
+    bound = sc.U16[x.dtype] * (np.abs(want) + err) + err + sc.TINY[x.dtype]
+    d = np.abs(sc.f64(got) - want)
+    bad = ~(d <= bound)
+    assert not bad.any(), (np.argwhere(bad)[:4], d[bad][:4], bound[bad][:4])
+
+
+def rows(g, T, H, D, t, scale=1.5):
+    return sc.dev((scale * g.standard_normal((T, H, D))).astype(np.float32), t)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,dtype", [
+    (1, 1, 1, 128, 128, "f16"), (1, 16, 2, 128, 128, "bf16"), (3, 5, 5, 64, 64, "bf16"),
+    (7, 8, 1, 80, 80, "f16"), (7, 8, 1, 80, 40, "f16"), (33, 4, 4, 80, 20, "bf16"),
+    (5, 6, 2, 96, 48, "f16"), (5, 6, 2, 192, 64, "bf16"), (4, 3, 3, 256, 256, "f16"),
+    (4, 3, 3, 256, 250, "bf16"), (2, 3, 1, 2, 2, "f16"), (2, 3, 1, 6, 4, "bf16"),
+    (3, 4, 2, 18, 10, "f16"), (3, 4, 2, 128, 0, "bf16"), (2, 300, 7, 256, 128, "f16"),
+    (2, 70, 70, 254, 126, "f16"), (5000, 2, 1, 64, 64, "bf16"), (2100, 9, 3, 16, 16, "f16"),
+])
+def test_rope(lib, T, Hq, Hk, D, rot, dtype, norm, layout):
+    g = sc.rng(1, T, Hq, D, rot)
+    t = sc.DTYPES[dtype]
+    q, k = rows(g, T, Hq, D, t), rows(g, T, Hk, D, t)
+    wq, wk = [sc.dev(g.uniform(0.5, 1.5, D).astype(np.float32), t) for _ in range(2)]
+    pos = np.unique(g.integers(0, 1 << 20, T)) if T < 100 else g.integers(0, 40, T)
+    pos = np.resize(pos, T).astype(np.int32)
+    r = lib.rotary(rot, theta=1e5, layout=layout, attention_factor=1.25)
+    inv = lib.rotary_frequencies(rot, 1e5).tolist()
+    a, b = lib.qk_rope(q, k, sc.dev(pos), r, wq if norm else None, wk if norm else None, eps=1e-5)
+    assert a.is_contiguous() and b.is_contiguous() and a.dtype == b.dtype == t
+    part = slice(None)
+    if T > 100:  # the slow reference on some of the tokens, the ends among them
+        part = np.r_[0:8, T // 2:T // 2 + 8, T - 8:T]
+    ix = torch.arange(T, device="cuda")[part]
+    for got, x, w in ((a, q, wq), (b, k, wk)):
+        check(got[ix], x[ix], pos[part], inv, layout, 1.25, w if norm else None, 1e-5)
+
+
+@pytest.mark.parametrize("norm", ["q", "k"])
+def test_norm_of_one_side(lib, norm):
+    g = sc.rng(2)
+    q, k = rows(g, 6, 4, 64, torch.float16), rows(g, 6, 2, 64, torch.float16)
+    w = sc.dev(g.uniform(0.5, 1.5, 64).astype(np.float32), torch.float16)
+    pos = np.arange(6, dtype=np.int32)
+    r, inv = lib.rotary(64), lib.rotary_frequencies(64).tolist()
+    kw = {norm + "_weight": w}
+    a, b = lib.qk_rope(q, k, sc.dev(pos), r, eps=1e-6, **kw)
+    check(a, q, pos, inv, "half", 1.0, w if norm == "q" else None, 1e-6)
+    check(b, k, pos, inv, "half", 1.0, w if norm == "k" else None, 1e-6)
+
+
+def test_far_and_negative_positions(lib):
+    """The angle at any 32-bit position; turning back by the negative one."""
+    g = sc.rng(3)
+    pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 999999937, -131071], np.int32)
+    q = rows(g, 8, 2, 128, torch.float16)
+    r, inv = lib.rotary(128, theta=5e5), lib.rotary_frequencies(128, 5e5).tolist()
+    a, none = lib.qk_rope(q, None, sc.dev(pos), r)
+    assert none is None
+    check(a, q, pos, inv, "half", 1.0, None, 1e-6)
+    assert torch.equal(a[0], q[0])
+
+
+def test_given_frequencies(lib):
+    """Of any sign and size below 2^20, whole turns among them."""
+    g = sc.rng(4)
+    inv = [0.0, 1.0, -0.5, math.pi, 2 * math.pi, 1e-9, 1048575.75, -77777.7]
+    q = rows(g, 5, 3, 16, torch.bfloat16)
+    pos = np.array([0, 3, 1 << 20, -5, 2 ** 31 - 1], np.int32)
+    r = lib.rotary(16, layout="interleaved", inv_freq=inv)
+    a, _ = lib.qk_rope(q, None, sc.dev(pos), r)
+    check(a, q, pos, inv, "interleaved", 1.0, None, 1e-6)
+
+
+@pytest.mark.parametrize("scaling,kw", [("linear", {}), ("ntk", {}), (
+    "parts", dict(original_len=4096, low=1.0, high=32.0))])
+def test_scaled_frequencies(lib, scaling, kw):
+    g = sc.rng(5)
+    q = rows(g, 4, 2, 64, torch.float16)
+    pos = np.array([0, 17, 100000, 4000000], np.int32)
+    r = lib.rotary(64, scaling=scaling, factor=8.0, **kw)
+    inv = lib.rotary_frequencies(64, scaling=scaling, factor=8.0, **kw).tolist()
+    a, _ = lib.qk_rope(q, None, sc.dev(pos), r)
+    check(a, q, pos, inv, "half", 1.0, None, 1e-6)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_strides_and_in_place(lib, norm):
+    """Slices of a fused projection, heads before tokens, odd distances and
+    addresses; outputs of their own strides; the inputs as outputs."""
+    g = sc.rng(6)
+    T, Hq, Hk, D = 37, 6, 2, 64
+    r, inv = lib.rotary(64), lib.rotary_frequencies(64).tolist()
+    w = sc.dev(g.uniform(0.5, 1.5, D).astype(np.float32), torch.float16) if norm else None
+    pos = np.arange(100, 100 + T, dtype=np.int32)
+    p = sc.dev(pos)
+
+    def fused(pad, lead):
+        f = rows(g, T, Hq + 2 * Hk, D + pad, torch.float16)[..., lead:lead + D]
+        return f[:, :Hq], f[:, Hq:Hq + Hk]
+    for pad, lead in ((0, 0), (8, 8), (4, 4), (2, 2), (3, 1)):
+        q, k = fused(pad, lead)
+        want = lib.qk_rope(q.contiguous(), k.contiguous(), p, r, w, w)
+        check(want[0], q, pos, inv, "half", 1.0, w, 1e-6)
+        got = lib.qk_rope(q, k, p, r, w, w)
+        # other runs, other sums: bits may differ where squares are summed
+        if not norm:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        check(got[0], q, pos, inv, "half", 1.0, w, 1e-6)
+        check(got[1], k, pos, inv, "half", 1.0, w, 1e-6)
+        # heads first, as another attention takes them
+        oq = torch.empty((Hq, T, D), dtype=q.dtype, device="cuda").transpose(0, 1)
+        ok = torch.empty((Hk, T, D), dtype=q.dtype, device="cuda").transpose(0, 1)
+        lib.qk_rope(q, k, p, r, w, w, out=(oq, ok))
+        assert torch.equal(oq, got[0]) and torch.equal(ok, got[1])
+        # in place; what lies beside is left alone
+        rest = torch.as_strided(q, (q.storage_offset(),), (1,), 0).clone()
+        a, b = lib.qk_rope(q, k, p, r, w, w, out=(q, k))
+        assert a is q and b is k
+        assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+        assert torch.equal(torch.as_strided(q, (q.storage_offset(),), (1,), 0), rest)
+
+
+def test_broadcast_input_and_no_tokens(lib):
+    g = sc.rng(7)
+    r, inv = lib.rotary(32), lib.rotary_frequencies(32).tolist()
+    one = rows(g, 1, 1, 32, torch.bfloat16)
+    q = one.expand(9, 4, 32)
+    pos = np.arange(9, dtype=np.int32)
+    a, _ = lib.qk_rope(q, None, sc.dev(pos), r)
+    check(a, q.contiguous(), pos, inv, "half", 1.0, None, 1e-6)
+    a, b = lib.qk_rope(q[:0], q[:0], sc.dev(pos[:0]), r)
+    assert a.shape == b.shape == (0, 4, 32)
+
+
+def test_extreme_values(lib):
+    """Squares beyond fp32 and below it; zeros; an infinity or NaN spoils its
+    head (or its pair) and nothing else."""
+    r = lib.rotary(16)
+    g = sc.rng(8)
+    x = g.standard_normal((6, 2, 16)).astype(np.float32)
+    x[0] *= 1e38
+    x[1] *= 1e-30
+    x[2] = 0
+    for D in (16,):
+        q = sc.dev(x, torch.bfloat16)
+        w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+        pos = np.arange(6, dtype=np.int32)
+        inv = lib.rotary_frequencies(16).tolist()
+        for odd in (False, True):  # the plain kernel as well
+            src = q if not odd else torch.empty((6, 2, 17), dtype=q.dtype, device="cuda")[..., 1:]
+            if odd:
+                src.copy_(q)
+            a, _ = lib.qk_rope(src, None, sc.dev(pos), r, w, eps=1e-6)
+            check(a, q, pos, inv, "half", 1.0, w, 1e-6)
+            bad = src.clone()
+            bad[3, 0, 5], bad[4, 1, 2] = float("nan"), float("inf")
+            b, _ = lib.qk_rope(bad, None, sc.dev(pos), r, w, eps=1e-6)
+            keep = torch.ones((6, 2), dtype=torch.bool, device="cuda")
+            keep[3, 0] = keep[4, 1] = False
+            assert torch.equal(b[keep], a[keep])
+            assert b[3, 0].isnan().all() and b[4, 1].isnan().any()
+
+
+def test_other_stream_and_graph(lib):
+    g = sc.rng(9)
+    q, k = rows(g, 20, 4, 64, torch.float16), rows(g, 20, 2, 64, torch.float16)
+    w = torch.ones(64, dtype=torch.float16, device="cuda")
+    p = torch.arange(20, dtype=torch.int32, device="cuda")
+    r = lib.rotary(64)
+    oq, ok = torch.empty_like(q), torch.empty_like(k)
+    lib.qk_rope(q, k, p, r, w, w, out=(oq, ok))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        lib.qk_rope(q, k, p, r, w, w, out=(oq, ok))
+    for i in range(3):
+        q.copy_(rows(g, 20, 4, 64, torch.float16))
+        p.add_(1000)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = lib.qk_rope(q, k, p, r, w, w)
+        assert torch.equal(oq, want[0]) and torch.equal(ok, want[1])

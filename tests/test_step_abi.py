@@ -1,0 +1,103 @@
+"""Host-only checks of the operators around a decode step's attention (no GPU,
+no kernel is launched): bad arguments are refused with the documented
+statuses before anything is enqueued, and the references on their own terms."""
+
+import math
+import os
+
+import numpy as np
+import pytest
+
+from int8_quantized_matmul_col_amd import binding, rope, serving
+from oracle import step_ref as ref
+
+FAKE = 0x7F0000000000  # never dereferenced
+OK, EINVAL, ESHAPE, EWORKSPACE = (binding.INT8MM_OK, binding.INT8MM_EINVAL, binding.INT8MM_ESHAPE,
+                                  binding.INT8MM_EWORKSPACE)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.LIB_PATH):
+        from int8_quantized_matmul_col_amd import build
+        build.build()
+    return serving._lib()
+
+
+# -------------------------------------------- queries and keys by position
+
+def _rope(lib, q=FAKE, k=FAKE, dt=0, T=3, Hq=4, Hk=2, D=64, qs=(256, 64), ks=(128, 64), p=FAKE,
+          turns=FAKE, rot=64, layout=0, factor=1.0, wq=None, wk=None, eps=1e-6, qo=FAKE + 4096,
+          ko=FAKE + 8192, qos=(256, 64), kos=(128, 64)):
+    return lib.qk_rope(q, k, dt, T, Hq, Hk, D, *qs, *ks, p, turns, rot, layout, factor, wq, wk,
+                       eps, qo, ko, *qos, *kos, None)
+
+
+def test_rope_refusals(lib):
+    for n in ("q", "k", "p", "turns", "qo", "ko"):
+        assert _rope(lib, **{n: None}) == EINVAL, n
+    for n in ("q", "k", "qo", "ko", "wq", "wk"):
+        assert _rope(lib, **{n: FAKE + 1}) == EINVAL, n
+    assert _rope(lib, p=FAKE + 2) == EINVAL and _rope(lib, turns=FAKE + 4) == EINVAL
+    assert _rope(lib, dt=2) == EINVAL and _rope(lib, layout=2) == EINVAL
+    for kw in (dict(D=0), dict(D=258), dict(D=65, rot=64), dict(rot=66), dict(rot=-2), dict(rot=31),
+               dict(T=-1), dict(T=(1 << 22) + 1), dict(Hq=-1), dict(Hk=-1), dict(Hq=4097),
+               dict(Hk=4097), dict(T=1 << 20, Hq=300)):
+        assert _rope(lib, **kw) == ESHAPE, kw
+    for bad in (math.nan, math.inf):
+        assert _rope(lib, factor=bad) == EINVAL and _rope(lib, wq=FAKE, eps=bad) == EINVAL
+    assert _rope(lib, wk=FAKE, eps=0.0) == EINVAL and _rope(lib, wk=FAKE, eps=-1.0) == EINVAL
+    # outputs that overlap themselves, or their input with other distances
+    assert _rope(lib, qos=(256, 63)) == EINVAL and _rope(lib, qos=(63, 256)) == EINVAL
+    assert _rope(lib, qos=(200, 64)) == EINVAL and _rope(lib, kos=(0, 64)) == EINVAL
+    assert _rope(lib, qo=FAKE, qos=(512, 64)) == EINVAL
+    assert _rope(lib, ko=FAKE, kos=(64, 192)) == EINVAL
+    assert _rope(lib, T=0) == OK and _rope(lib, Hq=0, Hk=0) == OK
+    assert lib.rope_prepare(None, 4, FAKE, None) == EINVAL
+    assert lib.rope_prepare(FAKE + 4, 4, FAKE, None) == EINVAL
+    assert lib.rope_prepare(FAKE, 129, FAKE, None) == ESHAPE
+    assert lib.rope_prepare(FAKE, -1, FAKE, None) == ESHAPE
+    assert lib.rope_prepare(None, 0, None, None) == OK
+
+
+def test_frequencies():
+    f = rope.rotary_frequencies
+    assert f(0).numel() == 0 and f(2).tolist() == [1.0]
+    plain = f(64, 1e4)
+    assert np.allclose(plain, [1e4 ** (-i / 32) for i in range(32)], rtol=1e-15)
+    assert np.allclose(f(64, 1e4, "linear", 4.0), plain / 4)
+    ntk = f(64, 1e4, "ntk", 4.0)
+    assert ntk[0] == 1 and math.isclose(ntk[-1], plain[-1] / 4, rel_tol=1e-12)
+    parts = f(64, 1e4, "parts", 8.0, original_len=2048, low=1.0, high=32.0)
+    turns = 2048 * plain / (2 * math.pi)
+    assert np.allclose(parts[turns >= 32], plain[turns >= 32])
+    assert np.allclose(parts[turns <= 1], plain[turns <= 1] / 8)
+    mid = (turns > 1) & (turns < 32)
+    assert mid.any() and ((parts > plain / 8) & (parts < plain))[mid].all()
+    for bad in (dict(rot_dim=3), dict(rot_dim=258), dict(rot_dim=-2), dict(rot_dim=8, theta=0.0),
+                dict(rot_dim=8, factor=math.inf), dict(rot_dim=8, scaling="other"),
+                dict(rot_dim=8, scaling="parts")):
+        with pytest.raises(ValueError):
+            f(**bad)
+    with pytest.raises(ValueError):
+        rope.rotary(8, layout="pairs")
+    with pytest.raises(ValueError):
+        rope.rotary(8, inv_freq=[1.0, 2.0])
+    with pytest.raises(ValueError):
+        rope.rotary(4, inv_freq=[1.0, 2.0 ** 20])
+    with pytest.raises(ValueError):
+        rope.rotary(4, attention_factor=math.nan)
+
+
+def test_reference_rope():
+    g = np.random.default_rng(1)
+    x = g.standard_normal((3, 2, 8))
+    inv = [1.0, 0.3]
+    for layout in ("half", "interleaved"):
+        y, _ = ref.rope(x, [0, 5, 100], inv, layout, 1.0, None, 1e-6)
+        assert np.array_equal(y[0], x[0]) and np.array_equal(y[..., 4:], x[..., 4:])
+        assert np.allclose((y * y).sum(-1), (x * x).sum(-1))
+    m, n = (0, 2)
+    y, _ = ref.rope(x, [0, 5, 100], inv, "half", 1.0, None, 1e-6)
+    z = (x[2, 1, m] + 1j * x[2, 1, n]) * np.exp(1j * 100.0)
+    assert np.allclose([z.real, z.imag], [y[2, 1, m], y[2, 1, n]])
