@@ -19,7 +19,8 @@
  * Limits (ESHAPE beyond): table_rows <= 2^30, table_width * page_size <= 2^30,
  * 1024 kv heads, 65536 query heads, 4096 layers, 2^30 bytes for a page's keys
  * in 16 bits; 2^28 - 32 tokens for a kv_append or kv_gather, B * q_heads <
- * 2^24 for a kv_attention, 16384 rows or pairs for a kv_pages_reserve or _fork,
+ * 2^24 for a kv_attention, 16384 rows or pairs for a kv_pages_reserve, _extend
+ * or _fork,
  * 2^23 rows for a kv_pages_free, 2^30 pairs for a kv_pages_copy.
  */
 #ifndef INT8MM_SERVING_H
@@ -217,11 +218,10 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
                             float scale, int64_t window, float softcap, void* out, float* lse,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* Workspace of kv_pages_reserve, kv_pages_fork and kv_pages_compact for a
- * pool of num_pages and n rows or pairs (256-byte aligned). */
+/* Workspace of kv_pages_reserve, _extend, _fork and _compact for a pool of num_pages and n rows or pairs (256-byte aligned). */
 INT8MM_API size_t kv_pages_workspace_size(int64_t num_pages, int64_t n);
 
-/* Per-row results of kv_pages_reserve and kv_pages_fork (on the device). */
+/* Per-row results of kv_pages_reserve, _extend and _fork (on the device). */
 #define INT8MM_KV_DONE 0
 #define INT8MM_KV_NO_PAGES 1 /* not enough free pages: the row is unchanged */
 #define INT8MM_KV_BAD_ROW 2  /* a row out of range, in use, or named twice */
@@ -249,6 +249,27 @@ INT8MM_API int kv_pages_reserve(int32_t num_pages, int32_t page_size, int32_t* t
                                 int32_t* refcount, const int32_t* rows,
                                 const int32_t* new_lengths, int64_t n, int32_t* status,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kv_pages_extend -- a batch of n requests, of which request i brings counts[i]
+ * tokens (a prompt, a part of one, or one new token) to the sequence in row
+ * rows[i]: pages and lengths as kv_pages_reserve, and where each token goes.
+ * Tokens follow one another, request after request, in maps of `total` entries
+ * (what a step feeds, known to the host; 0 .. 2^28 - 32):
+ *   starts [n + 1]     where each request's tokens begin, and where the last end;
+ *   token_rows [total], positions [total]   what kv_append takes, -1 for tokens
+ *                      of a request whose status is not DONE, and behind the last.
+ *   status [n]         as kv_pages_reserve; BAD_ROW also for a negative count
+ *                      (which takes no place) and where the tokens of the
+ *                      requests so far are more than total.
+ * All int32, on the device.
+ */
+INT8MM_API int kv_pages_extend(int32_t num_pages, int32_t page_size, int32_t* table,
+                               int64_t table_rows, int64_t table_width, int32_t* lengths,
+                               int32_t* refcount, const int32_t* rows, const int32_t* counts,
+                               int64_t n, int64_t total, int32_t* status, int32_t* starts,
+                               int32_t* token_rows, int32_t* positions, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
 
 /*
  * kv_pages_fork -- children[i] becomes a sequence with the tokens of

@@ -58,6 +58,7 @@ from .serving import (  # noqa: F401
     INT8MM_KV_BAD_ROW,
     INT8MM_KV_DONE,
     INT8MM_KV_NO_PAGES,
+    BatchPlan,
     Int4Weight,
     PagedKV,
     int4_linear,
@@ -71,6 +72,7 @@ from .serving import (  # noqa: F401
     kv_gather,
     kv_pages_compact,
     kv_pages_copy,
+    kv_pages_extend,
     kv_pages_fork,
     kv_pages_free,
     kv_pages_reserve,

@@ -194,6 +194,78 @@ __global__ __launch_bounds__(kScanThreads) void k_pages_plan(Rows r, Snapshot s)
     plan_rows<FORK>(r, s, sh, names);
 }
 
+// kv_pages_extend's plan, beside the scan as plan_rows: the first naming of a
+// row counts, rows grow by counts b[i], and starts[i] are the counts' running
+// sum.  plan[i] keeps the present length, which the second kernel's token maps
+// need after others have changed it, or -1.  Names are compared four at a time
+// (as one 16-byte LDS read).
+struct Extend {
+  int32_t* starts;      // [n + 1]
+  int32_t* token_rows;  // [total]
+  int32_t* positions;   // [total]
+  int total;
+};
+__device__ void plan_extend(const Rows& r, const Extend& x, const Snapshot& s, uint32_t* part,
+                            int32_t* names) {
+  uint32_t taken = 0, tokens = 0;
+  const int64_t room = (int64_t)r.table_width << r.lps;
+  for (int i0 = 0; i0 < r.n; i0 += kScanThreads) {
+    const int i = i0 + threadIdx.x;
+    const int own = i < r.n ? r.a[i] : -1;
+    const int count = i < r.n ? r.b[i] : 0;
+    bool ok = (unsigned)own < (unsigned)r.table_rows;
+    const int64_t have = ok ? r.lengths[own] : 0;
+    for (int j0 = 0; j0 <= i0; j0 += kScanThreads) {
+      __syncthreads();
+      names[threadIdx.x] = j0 + (int)threadIdx.x < r.n ? r.a[j0 + threadIdx.x] : -1;
+      __syncthreads();
+      // in this thread's own part only the names before it
+      const int top = j0 < i0 ? kScanThreads : min(kScanThreads, r.n - j0);
+      const int mine = j0 < i0 ? kScanThreads : (int)threadIdx.x;
+      bool twice = false;
+#pragma unroll 4
+      for (int j = 0; j < top; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(names + j);
+        twice |= (v.x == own && j < mine) | (v.y == own && j + 1 < mine) |
+                 (v.z == own && j + 2 < mine) | (v.w == own && j + 3 < mine);
+      }
+      if (twice) ok = false;
+    }
+    const uint32_t add = count > 0 ? min((uint32_t)count, kSat) : 0;
+    const uint32_t end = sat_add(tokens, block_scan(add, part));
+    const int64_t want = have + count;
+    ok = ok && count >= 0 && have >= 0 && want <= room && end <= (uint32_t)x.total;
+    uint32_t need = 0;
+    if (ok) {
+      const int64_t ps = (int64_t)1 << r.lps;
+      need = (uint32_t)(((want + ps - 1) >> r.lps) - ((have + ps - 1) >> r.lps));
+      if (need > kSat) need = kSat;
+    }
+    const uint32_t upto = sat_add(taken, block_scan(need, part));
+    if (i < r.n) {
+      s.plan[i] = ok ? (int)have : -1;
+      s.need[i] = need;
+      s.first[i] = upto >= kSat ? kSat : upto - need;
+      x.starts[i + 1] = (int)min(end, (uint32_t)x.total);
+    }
+    __syncthreads();
+    if (threadIdx.x == kScanThreads - 1) part[16] = upto, part[17] = end;
+    __syncthreads();
+    taken = part[16];
+    tokens = part[17];
+  }
+  if (threadIdx.x == 0) x.starts[0] = 0;
+}
+
+__global__ __launch_bounds__(kScanThreads) void k_pages_plan_extend(Rows r, Extend x, Snapshot s) {
+  __shared__ uint32_t sh[64];
+  __shared__ __attribute__((aligned(16))) int32_t names[kScanThreads];
+  if ((int)blockIdx.x < (int)gridDim.x - 1)
+    scan_pages(r.refcount, r.num_pages, blockIdx.x, s, sh);
+  else
+    plan_extend(r, x, s, sh, names);
+}
+
 // ------------------------------------------------- reading the snapshot
 
 // pre[b] = free pages before block b, b = 0 .. blocks; every thread calls it.
@@ -364,6 +436,64 @@ __global__ __launch_bounds__(kThreads) void k_pages_reserve(Rows r, Snapshot s, 
   if (threadIdx.x == 0) r.lengths[row] = want;
 }
 
+// Workgroups 0 .. n-1: the pages, length and status of request i.  The others:
+// kTokens tokens each of the batch's maps, found by binary search in starts.
+constexpr int kTokens = 1024, kStartsLds = 2048;
+__global__ __launch_bounds__(kThreads) void k_pages_extend(Rows r, Extend x, Snapshot s, int blocks) {
+  __shared__ uint32_t pre[kMaxBlocks + 1];
+  __shared__ uint32_t part[kThreads / 64];
+  __shared__ int32_t starts[kStartsLds];
+  const int i = blockIdx.x;
+  auto done = [&](int i, uint32_t first, uint32_t need) {
+    return need == 0 || sat_add(first, need) <= pre[blocks];
+  };
+  if (i < r.n) {
+    const int have = s.plan[i];
+    const uint32_t first = s.first[i], need = s.need[i];
+    const int row = r.a[i], count = r.b[i];
+    if (have >= 0 && need > 0) load_prefix(s, blocks, pre, part);
+    const bool ok = have >= 0 && done(i, first, need);
+    if (threadIdx.x == 0) {
+      r.status[i] = have < 0 ? INT8MM_KV_BAD_ROW : ok ? INT8MM_KV_DONE : INT8MM_KV_NO_PAGES;
+      if (ok) r.lengths[row] = have + count;
+    }
+    if (!ok) return;
+    const int64_t at = (int64_t)row * r.table_width + (((int64_t)have + (1 << r.lps) - 1) >> r.lps);
+    for (uint32_t j = threadIdx.x; j < need; j += kThreads) {
+      const int page = select_page<true>(s, pre, blocks, first + j);
+      r.table[at + j] = page;
+      r.refcount[page] = 1;
+    }
+    return;
+  }
+  const bool near = r.n + 1 <= kStartsLds;
+  if (near)
+    for (int j = threadIdx.x; j <= r.n; j += kThreads) starts[j] = x.starts[j];
+  load_prefix(s, blocks, pre, part);  // (ends with a barrier)
+  const int64_t t0 = (int64_t)(i - r.n) * kTokens;
+#pragma unroll
+  for (int u = 0; u < kTokens / kThreads; ++u) {
+    const int64_t t64 = t0 + u * kThreads + threadIdx.x;
+    if (t64 >= x.total) break;
+    const int t = (int)t64;
+    int lo = 0, hi = r.n;  // the last request that starts at t or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((near ? starts[mid] : x.starts[mid]) <= t) lo = mid; else hi = mid - 1;
+    }
+    int row = -1, pos = -1;
+    if (lo < r.n) {  // (r.n: t lies behind the last)
+      const int have = s.plan[lo];
+      if (have >= 0 && done(lo, s.first[lo], s.need[lo])) {
+        row = r.a[lo];
+        pos = have + t - (near ? starts[lo] : x.starts[lo]);
+      }
+    }
+    x.token_rows[t] = row;
+    x.positions[t] = pos;
+  }
+}
+
 // Workgroups of pair i: they share the `per` slices of the partly filled page,
 // the first also writes the child's row.
 __global__ __launch_bounds__(kThreads) void k_pages_fork(Rows r, Snapshot s, int blocks, Copier c,
@@ -517,6 +647,24 @@ hipError_t launch_kv_pages_reserve(int num_pages, int page_size, int32_t* table,
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_pages_reserve, dim3(n), dim3(kThreads), 0, s, r, sn, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_pages_extend(int num_pages, int page_size, int32_t* table, int table_rows,
+                                  int table_width, int32_t* lengths, int32_t* refcount,
+                                  const int32_t* rows, const int32_t* counts, int n, int total,
+                                  int32_t* status, int32_t* starts, int32_t* token_rows,
+                                  int32_t* positions, void* ws, hipStream_t s) {
+  const Snapshot sn = carve(ws, num_pages, n, nullptr);
+  const int blocks = blocks_of(num_pages);
+  const Rows r{table, lengths, refcount, rows, counts, status,
+               table_rows, table_width, n, num_pages, __builtin_ctz(page_size)};
+  const Extend x{starts, token_rows, positions, total};
+  hipLaunchKernelGGL(k_pages_plan_extend, dim3(blocks + 1), dim3(kScanThreads), 0, s, r, x, sn);
+  const hipError_t e = hipGetLastError();
+  const int grid = n + (total + kTokens - 1) / kTokens;
+  if (e != hipSuccess || grid == 0) return e;
+  hipLaunchKernelGGL(k_pages_extend, dim3(grid), dim3(kThreads), 0, s, r, x, sn, blocks);
   return hipGetLastError();
 }
 

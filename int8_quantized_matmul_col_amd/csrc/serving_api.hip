@@ -326,6 +326,31 @@ INT8MM_API int kv_pages_reserve(int32_t num_pages, int32_t page_size, int32_t* t
                                                  new_lengths, (int)n, status, workspace, stream));
 }
 
+INT8MM_API int kv_pages_extend(int32_t num_pages, int32_t page_size, int32_t* table,
+                               int64_t table_rows, int64_t table_width, int32_t* lengths,
+                               int32_t* refcount, const int32_t* rows, const int32_t* counts,
+                               int64_t n, int64_t total, int32_t* status, int32_t* starts,
+                               int32_t* token_rows, int32_t* positions, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  if (num_pages < 0 || num_pages > INT8MM_KV_MAX_PAGES || page_size < 16 ||
+      page_size > INT8MM_KV_MAX_PAGE_SIZE || (page_size & (page_size - 1)) != 0)
+    return INT8MM_ESHAPE;
+  if (n < 0 || n > kMaxNamed || total < 0 || total > kMaxTokens ||
+      !table_shape(table_rows, table_width, page_size))
+    return INT8MM_ESHAPE;
+  if (starts == nullptr || (total > 0 && (token_rows == nullptr || positions == nullptr))) return INT8MM_EINVAL;
+  if (n > 0 && (table == nullptr || lengths == nullptr || rows == nullptr || counts == nullptr ||
+                status == nullptr || (refcount == nullptr && num_pages > 0)))
+    return INT8MM_EINVAL;
+  const void* ptrs[] = {table, lengths, refcount, rows, counts, status, starts, token_rows, positions};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return INT8MM_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, i8mm::kv_pages_workspace(num_pages, n))) return INT8MM_EWORKSPACE;
+  return status_of(i8mm::launch_kv_pages_extend(
+      n > 0 ? num_pages : 0, page_size, table, (int)table_rows, (int)table_width, lengths, refcount,
+      rows, counts, (int)n, (int)total, status, starts, token_rows, positions, workspace, stream));
+}
+
 INT8MM_API int kv_pages_fork(const int8mm_kv* kv, int32_t* table, int64_t table_rows,
                              int64_t table_width, int32_t* lengths, int32_t* refcount,
                              const int32_t* parents, const int32_t* children, int64_t n,

@@ -102,6 +102,11 @@ hipError_t launch_kv_pages_reserve(int num_pages, int page_size, int32_t* table,
                                    int table_width, int32_t* lengths, int32_t* refcount,
                                    const int32_t* rows, const int32_t* new_lengths, int n,
                                    int32_t* status, void* ws, hipStream_t s);
+hipError_t launch_kv_pages_extend(int num_pages, int page_size, int32_t* table, int table_rows,
+                                  int table_width, int32_t* lengths, int32_t* refcount,
+                                  const int32_t* rows, const int32_t* counts, int n, int total,
+                                  int32_t* status, int32_t* starts, int32_t* token_rows,
+                                  int32_t* positions, void* ws, hipStream_t s);
 hipError_t launch_kv_pages_fork(const int8mm_kv& kv, int32_t* table, int table_rows,
                                 int table_width, int32_t* lengths, int32_t* refcount,
                                 const int32_t* parents, const int32_t* children, int n,

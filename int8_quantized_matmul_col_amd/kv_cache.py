@@ -4,14 +4,14 @@
 of every layer, a table of page ids and a length for each of ``max_seqs``
 rows, and a reference count for each page.  A decode step is
 
-    cache.reserve(rows, new_lengths)                     # pages for the new tokens
+    plan = cache.extend(rows, counts, total)             # pages for the new tokens
     for i, layer in enumerate(model):
-        cache.append(i, k, v, rows, positions)
+        cache.append(i, k, v, plan.token_rows, plan.positions)
         out = cache.attend(i, q, rows)
 
 with nothing copied to the host.  Which row belongs to which request, and
-whether the pool has room, is the caller's to know: ``reserve`` and ``fork``
-return a status per row on the device.
+whether the pool has room, is the caller's to know: ``reserve``, ``extend`` and
+``fork`` return a status per row on the device.
 """
 
 from __future__ import annotations
@@ -55,6 +55,12 @@ class PagedKVCache:
         """kv_pages_reserve: room for new_lengths[i] tokens in row rows[i]."""
         return serving.kv_pages_reserve(self.table, self.lengths, self.refcount, rows, new_lengths,
                                         self.page_size)
+
+    def extend(self, rows, counts, total: int) -> serving.BatchPlan:
+        """kv_pages_extend: room for counts[i] more tokens in row rows[i], and
+        where each of the batch's `total` tokens goes."""
+        return serving.kv_pages_extend(self.table, self.lengths, self.refcount, rows, counts, total,
+                                       self.page_size)
 
     def append(self, layer: int, k, v, rows, positions) -> None:
         """kv_append: token i of k, v to positions[i] of row rows[i]."""

@@ -71,6 +71,8 @@ SIGNATURES = {
     "kv_pages_copy": (_INT, [_KV, _P, _P, _I64, _P]),
     "kv_pages_reserve": (_INT, [_I32, _I32, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ,
                                 _P]),
+    "kv_pages_extend": (_INT, [_I32, _I32, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P,
+                               _P, _P, _SZ, _P]),
     "kv_pages_fork": (_INT, [_KV, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     "kv_pages_free": (_INT, [_I32, _P, _I64, _I64, _P, _P, _P, _I64, _P]),
     "kv_pages_compact": (_INT, [_KV, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
@@ -568,6 +570,45 @@ def kv_pages_reserve(table, lengths, refcount, rows, new_lengths, page_size: int
           lengths.data_ptr(), refcount.data_ptr(), rows.data_ptr(), new_lengths.data_ptr(), n,
           status.data_ptr(), ws.data_ptr(), ws.nbytes)
     return status
+
+
+class BatchPlan(NamedTuple):
+    """What kv_pages_extend returns, int32 on the GPU: status [n] of each
+    request, starts [n + 1] of their tokens, and each token's table row and
+    position [total] (-1 where there is none)."""
+    status: torch.Tensor
+    starts: torch.Tensor
+    token_rows: torch.Tensor
+    positions: torch.Tensor
+
+
+def kv_pages_extend(table, lengths, refcount, rows, counts, total: int, page_size: int,
+                    workspace=None) -> BatchPlan:
+    """A batch of requests, request i with counts[i] tokens for the sequence in
+    table row rows[i] (int32 [n]): the rows get the pages they lack and their
+    new lengths, as kv_pages_reserve, and the batch's tokens, one request after
+    the other, their rows and positions for kv_append.  total: the tokens of
+    the batch, known to the host; a larger one leaves entries of -1 at the end,
+    and requests that pass it are INT8MM_KV_BAD_ROW."""
+    dev = table.device
+    _pages_args(table, lengths, refcount, None, dev)
+    if refcount.dim() != 1:
+        raise ValueError("refcount must be 1-D")
+    _indexes(rows, "rows", dev)
+    if rows.dim() != 1:
+        raise ValueError("rows must be 1-D")
+    _indexes(counts, "counts", dev, rows.shape)
+    n, P, total = rows.numel(), refcount.numel(), int(total)
+    if total < 0:
+        raise ValueError("total must not be negative")
+    maps = rows.new_empty((2 * n + 1 + 2 * total,))
+    ws = _pages_workspace(P, n, dev, workspace)
+    at = maps.data_ptr()
+    _call("kv_pages_extend", dev.index, P, page_size, table.data_ptr(), table.shape[0],
+          table.shape[1], lengths.data_ptr(), refcount.data_ptr(), rows.data_ptr(),
+          counts.data_ptr(), n, total, at, at + 4 * n, at + 4 * (2 * n + 1),
+          at + 4 * (2 * n + 1 + total), ws.data_ptr(), ws.nbytes)
+    return BatchPlan(*maps.split((n, n + 1, total, total)))
 
 
 def kv_pages_fork(kv: PagedKV, table, lengths, refcount, parents, children, workspace=None):

@@ -41,3 +41,38 @@ def rope(x, positions, inv_freq, layout, factor, weight, eps):
         y[..., n] = factor * (x[..., n] * c + x[..., m] * s)
         mag[..., m] = mag[..., n] = abs(factor) * (np.abs(x[..., m]) + np.abs(x[..., n]))
     return y, mag
+
+
+# --------------------------------------------- the pages of a batch's tokens
+
+def extend(table, lengths, refcount, rows, counts, total, page_size):
+    """kv_pages_extend on lists, one request after the other; changes table,
+    lengths and refcount, returns (status, starts, token_rows, positions)."""
+    free = [p for p, c in enumerate(refcount) if c <= 0]
+    status, starts, token_rows, positions = [], [0], [-1] * total, [-1] * total
+    named, taken, sure, at = set(), 0, True, 0
+    for row, count in zip(rows, counts):
+        begin, at = at, at + max(count, 0)
+        starts.append(min(at, total))
+        ok = 0 <= row < len(table) and row not in named and count >= 0 and at <= total
+        named.add(row)
+        if ok:
+            have = lengths[row]
+            ok = have >= 0 and have + count <= len(table[row]) * page_size
+        if not ok:
+            status.append(2)
+            continue
+        old, new = -(-have // page_size), -(-(have + count) // page_size)
+        sure = sure and taken + new - old <= len(free)
+        taken += new - old
+        if new > old and not sure:
+            status.append(1)
+            continue
+        for i in range(old, new):
+            table[row][i] = free[taken - new + i]
+            refcount[table[row][i]] = 1
+        lengths[row] = have + count
+        status.append(0)
+        for t in range(begin, at):
+            token_rows[t], positions[t] = row, have + t - begin
+    return status, starts, token_rows, positions

@@ -101,3 +101,30 @@ def test_reference_rope():
     y, _ = ref.rope(x, [0, 5, 100], inv, "half", 1.0, None, 1e-6)
     z = (x[2, 1, m] + 1j * x[2, 1, n]) * np.exp(1j * 100.0)
     assert np.allclose([z.real, z.imag], [y[2, 1, m], y[2, 1, n]])
+
+
+# --------------------------------------------- the pages of a batch's tokens
+
+def test_extend_refusals(lib):
+    def ext(P=8, ps=16, t=FAKE, tr=2, tw=4, l=FAKE, c=FAKE, r=FAKE, k=FAKE, n=2, total=5, st=FAKE,
+            starts=FAKE, tok=FAKE, pos=FAKE, ws=FAKE, nb=1 << 20):
+        return lib.kv_pages_extend(P, ps, t, tr, tw, l, c, r, k, n, total, st, starts, tok, pos,
+                                   ws, nb, None)
+    for kw in (dict(ps=20), dict(ps=8), dict(ps=2048), dict(P=-1), dict(P=(1 << 22) + 1),
+               dict(n=-1), dict(n=16385), dict(total=-1), dict(total=(1 << 28) - 31), dict(tr=-1),
+               dict(tw=1 << 28)):
+        assert ext(**kw) == ESHAPE, kw
+    for n in ("t", "l", "c", "r", "k", "st", "starts", "tok", "pos"):
+        assert ext(**{n: None}) == EINVAL, n
+        assert ext(**{n: FAKE + 2}) == EINVAL, n
+    assert ext(ws=None) == EWORKSPACE and ext(ws=FAKE + 64) == EWORKSPACE
+    assert ext(nb=100) == EWORKSPACE
+
+
+def test_reference_extend():
+    table, n, c = [[4, -1, -1], [-1] * 3], [10, 0], [0, 0, 0, 0, 1]
+    got = ref.extend(table, n, c, [1, 0, 1], [20, 7, 1], 30, 16)
+    assert got[0] == [0, 0, 2] and got[1] == [0, 20, 27, 28]
+    assert got[2] == [1] * 20 + [0] * 7 + [-1] * 3
+    assert got[3] == list(range(20)) + list(range(10, 17)) + [-1] * 3
+    assert table == [[4, 2, -1], [0, 1, -1]] and n == [17, 20] and c == [1, 1, 1, 0, 1]
