@@ -35,7 +35,8 @@ extern "C" {
 /* Element types of the serving operators. */
 #define INT8MM_F16 0
 #define INT8MM_BF16 1
-#define INT8MM_I8 2 /* caches only */
+#define INT8MM_I8 2  /* caches only */
+#define INT8MM_F32 3 /* logits only */
 
 /* ------------------------------------------------------- 4-bit weights --
  *
@@ -350,6 +351,41 @@ INT8MM_API int qk_rope(const void* q, const void* k, int dtype, int64_t T, int64
                        float eps, void* q_out, void* k_out, int64_t q_out_token_stride,
                        int64_t q_out_head_stride, int64_t k_out_token_stride,
                        int64_t k_out_head_stride, hipStream_t stream);
+
+/* --------------------------------------------------------- the next tokens --
+ *
+ * sample_tokens -- draws one token of each row of logits.  With z = logit / T
+ * and w = exp(z - max z), 0 for those e^-64 or less; tokens in order by logit,
+ * larger first, and equal ones by index, lower first:
+ *
+ *   top-k   keeps the first k (k <= 0: all);
+ *   top-p   keeps of these the ones before which less than p of their mass lies,
+ *           the first one always (p >= 1: all);
+ *   min-p   keeps of these the ones with w >= min(min_p, 1) (min_p <= 0: all);
+ *   token = the lowest index at which the running sum of the kept weights, in
+ *           index order, exceeds u times their sum.
+ *
+ * T <= 0: the first of the largest logits (greedy).  A row with a NaN or +inf
+ * logit, with none above -inf, or with T NaN gives -1; a NaN p or min_p keeps
+ * all.  u is taken into [0, 1 - 2^-24]; NaN is 0.  Sums are exact to about 2^-36 of
+ * each weight, whole numbers whose order does not matter: a row's token depends
+ * on nothing but its logits, u and filters.
+ *
+ *   logits [B][V], F16, BF16 or INT8MM_F32, rows row_stride elements apart (any
+ *          distance, 0 too).  u [B].
+ *   temperature, top_k, top_p, min_p [B], each or NULL: then the value after it
+ *          counts for all rows.
+ *   tokens [B] int32 out.
+ * 0 <= V <= 2^20, B <= 65535, B * V <= 2^34.  Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.
+ */
+#define INT8MM_SAMPLE_MAX_V (1 << 20)
+INT8MM_API size_t sample_tokens_workspace_size(int64_t B, int64_t V);
+INT8MM_API int sample_tokens(const void* logits, int dtype, int64_t B, int64_t V,
+                             int64_t row_stride, const float* u, const float* temperature,
+                             float temperature_all, const int32_t* top_k, int32_t top_k_all,
+                             const float* top_p, float top_p_all, const float* min_p,
+                             float min_p_all, int32_t* tokens, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

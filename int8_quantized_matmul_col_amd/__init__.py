@@ -53,6 +53,7 @@ from .kv_cache import PagedKVCache  # noqa: F401
 from .linear import Int8Linear, replace_linear_with_int8  # noqa: F401
 from .linear4 import Int4Linear  # noqa: F401
 from .rope import Rotary, qk_rope, rope_prepare, rotary, rotary_frequencies  # noqa: F401
+from .sampling import sample_tokens, sample_tokens_workspace_size  # noqa: F401
 from .stats import outlier_stats, suggest_threshold  # noqa: F401
 from .serving import (  # noqa: F401
     INT8MM_KV_BAD_ROW,

@@ -111,6 +111,14 @@ bool rows_apart(int64_t T, int64_t heads, int64_t D, int64_t token, int64_t head
   return token >= head ? token >= head * (heads - 1) + D : head >= token * (T - 1) + D;
 }
 
+// ---------------------------------------------------------- the next tokens
+
+bool sample_shape(int64_t B, int64_t V) {
+  return B >= 0 && B <= 65535 && V >= 0 && V <= INT8MM_SAMPLE_MAX_V && B * V <= ((int64_t)1 << 34);
+}
+size_t sample_heads(int64_t B, int64_t S) { return align_up((size_t)(B * S) * sizeof(i8mm::SampleHead)); }
+static_assert(INT8MM_SAMPLE_MAX_V + 7 <= i8mm::kSampleMaxChunks * i8mm::kSampleChunk, "");
+
 }  // namespace
 
 extern "C" {
@@ -476,6 +484,48 @@ INT8MM_API int qk_rope(const void* q, const void* k, int dtype, int64_t T, int64
   a.eps = eps;
   a.inv_dim = 1.0f / (float)head_dim;
   return status_of(i8mm::launch_qk_rope(a, dtype == INT8MM_BF16, stream));
+}
+
+INT8MM_API size_t sample_tokens_workspace_size(int64_t B, int64_t V) {
+  if (!sample_shape(B, V)) return 0;
+  const int64_t S = i8mm::sample_chunks(V);
+  return sample_heads(B, S) + align_up((size_t)(B * S) * i8mm::kSampleBins * 8);
+}
+
+INT8MM_API int sample_tokens(const void* logits, int dtype, int64_t B, int64_t V,
+                             int64_t row_stride, const float* u, const float* temperature,
+                             float temperature_all, const int32_t* top_k, int32_t top_k_all,
+                             const float* top_p, float top_p_all, const float* min_p,
+                             float min_p_all, int32_t* tokens, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  if (dtype != INT8MM_F16 && dtype != INT8MM_BF16 && dtype != INT8MM_F32) return INT8MM_EINVAL;
+  if (!sample_shape(B, V)) return INT8MM_ESHAPE;
+  if (B == 0) return INT8MM_OK;
+  if (u == nullptr || tokens == nullptr || (V > 0 && logits == nullptr)) return INT8MM_EINVAL;
+  if (!aligned(logits, dtype == INT8MM_F32 ? 4 : 2)) return INT8MM_EINVAL;
+  const void* ptrs[] = {u, temperature, top_k, top_p, min_p, tokens};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return INT8MM_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, sample_tokens_workspace_size(B, V))) return INT8MM_EWORKSPACE;
+  i8mm::SampleArgs a{};
+  a.logits = logits;
+  a.row_stride = B > 1 ? row_stride : 0;
+  a.u = u;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.temperature_all = temperature_all;
+  a.top_k_all = top_k_all;
+  a.top_p_all = top_p_all;
+  a.min_p_all = min_p_all;
+  a.tokens = tokens;
+  a.B = (int)B;
+  a.V = (int)V;
+  a.S = i8mm::sample_chunks(V);
+  a.heads = static_cast<i8mm::SampleHead*>(workspace);
+  a.bins = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + sample_heads(B, a.S));
+  return status_of(i8mm::launch_sample(a, dtype, stream));
 }
 
 }  // extern "C"

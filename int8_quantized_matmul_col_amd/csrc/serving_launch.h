@@ -95,6 +95,35 @@ struct QkRopeArgs {
 hipError_t launch_rope_prepare(const double* inv_freq, int n, uint64_t* turns, hipStream_t s);
 hipError_t launch_qk_rope(const QkRopeArgs& a, bool bf16, hipStream_t s);
 
+// ---- the next tokens
+constexpr int kSampleChunk = 8192;    // logits of a workgroup
+constexpr int kSampleBins = 520;      // 64-bit words that it leaves
+constexpr int kSampleMaxChunks = 136;  // of a row
+struct SampleHead {
+  float top;  // the chunk's maximum
+  int first;  // greedy: the first index that has it
+  int last;   // the last bin with a token, -1: none
+  int bad;    // an infinity or NaN
+};
+struct SampleArgs {
+  const void* logits;
+  int64_t row_stride;
+  const float* u;
+  const float* temperature;  // or null: the one of all rows
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all, top_p_all, min_p_all;
+  int32_t top_k_all;
+  int32_t* tokens;
+  SampleHead* heads;  // [B][S]
+  uint64_t* bins;     // [B][S][kSampleBins]
+  int B, V, S;
+};
+// Chunks of a row of V logits that begins anywhere within 16 bytes.
+inline int sample_chunks(int64_t V) { return V == 0 ? 0 : (int)((V + 7 + kSampleChunk - 1) / kSampleChunk); }
+hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t s);
+
 size_t kv_pages_workspace(int64_t num_pages, int64_t n);
 hipError_t launch_kv_pages_copy(const int8mm_kv& kv, const int32_t* src, const int32_t* dst, int n,
                                 hipStream_t s);

@@ -23,7 +23,7 @@ import torch
 from . import binding
 from .binding import INT8MM_ESHAPE, Int8mmError, _check, _check_out, _require
 
-INT8MM_F16, INT8MM_BF16, INT8MM_I8 = 0, 1, 2
+INT8MM_F16, INT8MM_BF16, INT8MM_I8, INT8MM_F32 = 0, 1, 2, 3
 INT4_MAX_K = 1 << 20
 INT4_MAX_N = 1 << 24
 INT4_MAX_M = 1 << 21
@@ -76,6 +76,9 @@ SIGNATURES = {
     "kv_pages_fork": (_INT, [_KV, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     "kv_pages_free": (_INT, [_I32, _P, _I64, _I64, _P, _P, _P, _I64, _P]),
     "kv_pages_compact": (_INT, [_KV, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "sample_tokens_workspace_size": (_SZ, [_I64, _I64]),
+    "sample_tokens": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _F, _P, _I32, _P, _F, _P, _F, _P,
+                             _P, _SZ, _P]),
     "rope_prepare": (_INT, [_P, _I64, _P, _P]),
     "qk_rope": (_INT, [_P, _P, _INT] + [_I64] * 8 + [_P, _P, _I64, _INT, _F, _P, _P, _F, _P, _P]
                 + [_I64] * 4 + [_P]),

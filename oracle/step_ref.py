@@ -76,3 +76,42 @@ def extend(table, lengths, refcount, rows, counts, total, page_size):
         for t in range(begin, at):
             token_rows[t], positions[t] = row, have + t - begin
     return status, starts, token_rows, positions
+
+
+# --------------------------------------------------------- the next tokens
+
+def sample(x, u, temperature, top_k, top_p, min_p):
+    """(token, margin) of one row of logits float64 [V]: margin is how near the
+    nearest decision was to its border, as a part of the mass it is about."""
+    x = np.asarray(x, np.float64)
+    if x.size == 0 or np.isnan(x).any() or x.max() in (math.inf, -math.inf) or temperature != temperature:
+        return -1, 1.0
+    if temperature <= 0:
+        return int(np.argmax(x)), 1.0
+    live = x > -math.inf
+    z = np.where(live, np.where(live, x, 0.0) / temperature, -math.inf)
+    d = np.where(live, z - z.max(), -math.inf).astype(np.longdouble)
+    w = np.where(d > -FAR, np.exp(d), np.longdouble(0))
+    order = np.lexsort((np.arange(x.size), -x))
+    if 0 < top_k < x.size:
+        order = order[:top_k]
+    margin = 1.0
+    if top_p < 1:
+        mass = np.concatenate(([np.longdouble(0)], np.cumsum(w[order])))
+        limit = np.longdouble(top_p) * mass[-1]
+        n = max(1, int((mass[:-1] < limit).sum()))
+        margin = min(margin, float(np.abs(mass[1:-1] - limit).min(initial=1.0) / mass[-1]))
+        order = order[:n]
+    if min_p > 0:
+        least = np.longdouble(min(min_p, 1.0))
+        if least < 1:
+            margin = min(margin, float(np.abs(w[order] / least - 1).min()))
+        order = order[w[order] >= least]
+    kept = np.sort(order)
+    mass = np.cumsum(w[kept])
+    u = min(max(u, 0.0), 1 - 2.0 ** -24) if u == u else 0.0
+    target = np.longdouble(u) * mass[-1]
+    if u > 0:
+        margin = min(margin, float(np.abs(mass - target).min() / mass[-1]))
+    i = int((mass <= target).sum())
+    return int(kept[i]), margin

@@ -128,3 +128,38 @@ def test_reference_extend():
     assert got[2] == [1] * 20 + [0] * 7 + [-1] * 3
     assert got[3] == list(range(20)) + list(range(10, 17)) + [-1] * 3
     assert table == [[4, 2, -1], [0, 1, -1]] and n == [17, 20] and c == [1, 1, 1, 0, 1]
+
+
+# --------------------------------------------------------- the next tokens
+
+def test_sample_refusals(lib):
+    need = lib.sample_tokens_workspace_size(3, 10000)
+    assert need >= 3 * 2 * 513 * 8
+    for bad in ((-1, 5), (5, -1), (65536, 5), (1, (1 << 20) + 1), (65535, 1 << 20)):
+        assert lib.sample_tokens_workspace_size(*bad) == 0, bad
+
+    def sam(x=FAKE, dt=3, B=3, V=10000, u=FAKE, t=None, k=None, p=None, m=None, out=FAKE, ws=FAKE,
+            nb=need):
+        return lib.sample_tokens(x, dt, B, V, V, u, t, 1.0, k, 0, p, 1.0, m, 0.0, out, ws, nb, None)
+    for kw in (dict(B=-1), dict(V=-1), dict(B=65536), dict(V=(1 << 20) + 1), dict(B=65535, V=1 << 20)):
+        assert sam(**kw) == ESHAPE, kw
+    for n in ("x", "u", "out"):
+        assert sam(**{n: None}) == EINVAL, n
+    for n in ("x", "u", "t", "k", "p", "m", "out"):
+        assert sam(**{n: FAKE + 2}) == EINVAL, n
+    assert sam(dt=2) == EINVAL and sam(dt=4) == EINVAL and sam(dt=0, x=FAKE + 1) == EINVAL
+    assert sam(ws=None) == EWORKSPACE and sam(ws=FAKE + 128) == EWORKSPACE
+    assert sam(nb=need - 1) == EWORKSPACE and sam(B=0) == OK
+
+
+def test_reference_sample():
+    x = np.log([0.1, 0.4, 0.2, 0.3])
+    pick = lambda u, **kw: ref.sample(x, u, kw.get("t", 1.0), kw.get("k", 0), kw.get("p", 1.0),
+                                      kw.get("m", 0.0))[0]
+    assert [pick(u) for u in (0.0, 0.05, 0.11, 0.49, 0.51, 0.71)] == [0, 0, 1, 1, 2, 3]
+    assert [pick(u, k=2) for u in (0.0, 0.5, 0.6)] == [1, 1, 3]
+    assert [pick(u, p=0.75) for u in (0.0, 0.5, 0.7)] == [1, 2, 3]
+    assert [pick(u, p=0.7) for u in (0.0, 0.5, 0.7)] == [1, 1, 3]  # 0.7 lies before the third
+    assert [pick(u, m=0.6) for u in (0.0, 0.6)] == [1, 3]
+    assert pick(0.9, t=0.0) == 1 and pick(0.9, p=0.0) == 1 and pick(0.9, t=1e-3) == 1
+    assert ref.sample([0.0, math.nan], 0.5, 1.0, 0, 1.0, 0.0)[0] == -1
