@@ -8,17 +8,17 @@
 //   what is kept exceeds u times all of it
 //
 // Which token it is hangs on sums over a whole row, so they are exact: z is
-// formed in 64 bits, bins of 1/8 in z split the line, and a weight is a whole
+// formed in 64 bits, bins of 1/7 in z split the line, and a weight is a whole
 // number, round(2^36 exp(z - middle of its bin)).  Sums of them within a bin do
-// not depend on the order or on how a row is cut, and 513 bins (all that lies
-// within e^-64 of the maximum) times their powers of e^-1/8 are added in 64 bits.
+// not depend on the order or on how a row is cut, and 449 bins (all that lies
+// within e^-64 of the maximum) times their powers of e^-1/7 are added in 64 bits.
 //
 // Bound by reading the logits: once, by S workgroups a row (k_sample_bins, 8192
 // logits each), which leave per bin a count and a mass in one 64-bit word.  The
 // second kernel, a workgroup a row, finds from the joined bins the one in which
-// each filter cuts, reads the row again (from L2) only for that bin's tokens,
-// sorts them, and so knows the cut itself; then the chunk that the given number
-// falls into, and reads that.  Nothing is sorted but one bin.
+// each filter cuts, reads the row again (from L2) for that bin's tokens, and
+// narrows their range to the one logit at which it cuts; then the chunk that the
+// given number falls into, and reads that.  Nothing is sorted.
 #include "device_common.h"
 #include "serving_launch.h"
 
@@ -29,59 +29,105 @@ namespace {
 enum { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
 constexpr int kBinThreads = 512;
-constexpr int kPickThreads = 1024;
+constexpr int kPickThreads = 512;
 constexpr int kCopies = 8;       // of a workgroup's bins in LDS: lanes of equal bins collide less
-constexpr int kLastBin = 512;    // 64 below the maximum
+constexpr int kLastBin = 448;    // 64 below the maximum
 constexpr int kPitch = kSampleBins;
-constexpr int kList = 2048;      // tokens of one bin that are sorted
-constexpr int kDigits = 2048;
+constexpr int kList = 4096;      // tokens of one bin that LDS holds
+constexpr int kDigits = 512;     // that a range of keys is split into, a thread each
+constexpr int kDigitBits = 9;
 constexpr int kCountShift = 50;  // a word: a chunk's count (14 bits), its mass
 constexpr uint64_t kMass = ((uint64_t)1 << kCountShift) - 1;
-static_assert(kSampleChunk == kPickThreads * 8, "a thread takes 8 logits of a chunk");
+static_assert(kSampleChunk == kPickThreads * 16, "a thread takes 16 logits of a chunk");
+static_assert(kLastBin < kPickThreads, "a thread has a bin");
 static_assert(kSampleChunk < (1 << (64 - kCountShift)), "");
 static_assert(kPitch > kLastBin, "");
 
-// 8 logits from place v0 of the row, whose places mis .. mis + V - 1 exist and
-// whose place 0 is on 16 bytes; -inf elsewhere.
+// e^-a and e^(-b / 7), to the nearest.
+alignas(16) __constant__ double kWhole[65] = {
+    0x1.0000000000000p+0, 0x1.78b56362cef38p-2, 0x1.152aaa3bf81ccp-3, 0x1.97db0ccceb0afp-5,
+    0x1.2c155b8213cf4p-6, 0x1.b993fe00d5376p-8, 0x1.44e51f113d4d6p-9, 0x1.de16b9c24a98fp-11,
+    0x1.5fc21041027adp-12, 0x1.02cf22526545ap-13, 0x1.7cd79b5647c9bp-15, 0x1.18354238f6764p-16,
+    0x1.9c54c3b43bc8bp-18, 0x1.2f6053b981d98p-19, 0x1.be6c6fdb01612p-21, 0x1.4875ca227ec38p-22,
+    0x1.e355bbaee85cbp-24, 0x1.639e3175a689dp-25, 0x1.05a628c699fa1p-26, 0x1.81056ff2c5772p-28,
+    0x1.1b48655f37267p-29, 0x1.a0db0d0ddb3ecp-31, 0x1.32b48bf117da2p-32, 0x1.c3527e433fab1p-34,
+    0x1.4c1078fe9228ap-35, 0x1.e8a37a45fc32ep-37, 0x1.67852a7007e42p-38, 0x1.0885298767e9ap-39,
+    0x1.853f01d6d53bap-41, 0x1.1e642baeb84a0p-42, 0x1.a56e0c2ac7f75p-44, 0x1.36121e24d3bbap-45,
+    0x1.c8464f7616468p-47, 0x1.4fb547c775da8p-48, 0x1.ee001eed62aa0p-50, 0x1.6b7719a59f0e0p-51,
+    0x1.0b6c3afdde064p-52, 0x1.898471fca6055p-54, 0x1.2188ad6ae3303p-55, 0x1.aa0de4bf35b38p-57,
+    0x1.39792499b1a24p-58, 0x1.cd480a1b74820p-60, 0x1.536452ee2f75cp-61, 0x1.f36bd37f42f3ep-63,
+    0x1.6f741de1748ecp-64, 0x1.0e5b73d1ff53dp-65, 0x1.8dd5e1bb09d7ep-67, 0x1.24b6031b49bdap-68,
+    0x1.aebabae3a41b5p-70, 0x1.3ce9b9de78f85p-71, 0x1.d257d547e083fp-73, 0x1.571db733a9d61p-74,
+    0x1.f8e6c24b5592ep-76, 0x1.737c5645114b5p-77, 0x1.1152eaeb73c08p-78, 0x1.923372c67a074p-80,
+    0x1.27ec458c65e3cp-81, 0x1.b374b315f87c1p-83, 0x1.4063f8cc8bb98p-84, 0x1.d775d87da854dp-86,
+    0x1.5ae191a99585ap-87, 0x1.fe7116182e9ccp-89, 0x1.778fe2497184cp-90, 0x1.1452b7723aed2p-91,
+    0x1.969d47321e4ccp-93};
+__constant__ double kSeventh[7] = {
+    0x1.0000000000000p+0, 0x1.bbd76b8a1ab98p-1, 0x1.80c1a1bae3d1ep-1, 0x1.4d896b8eddab2p-1,
+    0x1.2122bbd2f6b6dp-1, 0x1.f54a68a74e851p-2, 0x1.b28ecb95f8c93p-2};
+// The power of e of a bin that many below the maximum's.
+__device__ __forceinline__ double bin_scale(int below) {
+  const int whole = below / 7;
+  return kWhole[whole] * kSeventh[below - whole * 7];
+}
+
+// The row's places mis .. mis + V - 1 exist, and its place 0 is on 16 bytes.
+// 8 logits as they lie in memory, -inf beside the row.
 template <int T>
-__device__ __forceinline__ void load8(const void* base, int v0, int mis, int end, float (&x)[8]) {
-  if (v0 >= mis && v0 + 8 <= end) {
+struct Piece {
+  uint4 w[T == kF32 ? 2 : 1];
+  __device__ __forceinline__ float value(int e) const {
+    const uint4& q = w[T == kF32 ? e / 4 : 0];
+    const int d = T == kF32 ? e % 4 : e / 2;
+    const uint32_t u = d == 0 ? q.x : d == 1 ? q.y : d == 2 ? q.z : q.w;
+    if constexpr (T == kF32)
+      return __uint_as_float(u);
+    else if constexpr (T == kBF16)
+      return __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
+    else
+      return h2f((uint16_t)(e & 1 ? u >> 16 : u));
+  }
+};
+// Pieces are requested without a condition, so that the loads of several do not
+// wait for one another (a row of 128000 logits: 10 us a reading with one, 4
+// so): one that is not wholly in the row reads a table instead, and then
+// (patch_piece) what there is of it.
+__device__ __forceinline__ bool whole_piece(int v0, int mis, int end) { return v0 >= mis && v0 + 8 <= end; }
+template <int T>
+__device__ __forceinline__ Piece<T> load_piece(const void* base, int v0, int mis, int end) {
+  constexpr int eb = T == kF32 ? 4 : 2;
+  const char* row = static_cast<const char*>(base) + (int64_t)v0 * eb;
+  const uint4* at = reinterpret_cast<const uint4*>(
+      whole_piece(v0, mis, end) ? row : reinterpret_cast<const char*>(kWhole));
+  Piece<T> p;
+  p.w[0] = at[0];
+  if constexpr (T == kF32) p.w[1] = at[1];
+  return p;
+}
+template <int T>
+__device__ __forceinline__ void patch_piece(Piece<T>& p, const void* base, int v0, int mis, int end) {
+  if (whole_piece(v0, mis, end)) return;
+  uint32_t u[4 * (T == kF32 ? 2 : 1)];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool there = v0 + e >= mis && v0 + e < end;
     if constexpr (T == kF32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + v0);
-      const float4 a = p[0], b = p[1];
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      u[e] = 0xff800000u;
+      if (there) u[e] = static_cast<const uint32_t*>(base)[v0 + e];
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + v0);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (T == kBF16)
-          x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-        else
-          x[i] = h2f((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]));
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = -INFINITY;
-      if (v0 + i >= mis && v0 + i < end) {
-        if constexpr (T == kF32)
-          x[i] = static_cast<const float*>(base)[v0 + i];
-        else if constexpr (T == kBF16)
-          x[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[v0 + i] << 16);
-        else
-          x[i] = h2f(static_cast<const uint16_t*>(base)[v0 + i]);
-      }
+      uint32_t h = T == kBF16 ? 0xff80u : 0xfc00u;
+      if (there) h = static_cast<const uint16_t*>(base)[v0 + e];
+      u[e / 2] = e & 1 ? u[e / 2] | h << 16 : h;
     }
   }
+  p.w[0] = uint4{u[0], u[1], u[2], u[3]};
+  if constexpr (T == kF32) p.w[1] = uint4{u[4], u[5], u[6], u[7]};
 }
 
 struct Row {
   const void* base;  // place 0, on 16 bytes
   int mis, end;      // places of the row
-  double per8;       // 8 / T
+  double per7;       // 7 / T
   bool greedy;
 };
 template <int T>
@@ -94,19 +140,19 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int b) {
   r.end = r.mis + a.V;
   const float t = a.temperature != nullptr ? a.temperature[b] : a.temperature_all;
   r.greedy = !(t > 0.0f);
-  r.per8 = r.greedy ? 8.0 : 8.0 / (double)t;
+  r.per7 = r.greedy ? 7.0 : 7.0 / (double)t;
   return r;
 }
 
-// z in eighths, and the weight of what it exceeds its bin's lower end by.
-__device__ __forceinline__ double eighths(float x, double per8) {
+// z in sevenths, and the weight of what it exceeds its bin's lower end by.
+__device__ __forceinline__ double sevenths(float x, double per7) {
 #pragma clang fp contract(off)
-  return (double)x * per8;
+  return (double)x * per7;
 }
-__device__ __forceinline__ uint64_t weight(double z8, double bin) {
+__device__ __forceinline__ uint64_t weight(double z7, double bin) {
 #pragma clang fp contract(off)
-  const double x = __builtin_fma(z8 - bin, 0.125, -0.0625);  // +- 1/16
-  // the series of exp; what follows is below 2^-47
+  const double x = (z7 - bin - 0.5) * (1.0 / 7.0);  // +- 1/14
+  // the series of exp; what follows is below 2^-45
   double p = 1.0 / 5040;
   p = __builtin_fma(p, x, 1.0 / 720);
   p = __builtin_fma(p, x, 1.0 / 120);
@@ -118,6 +164,21 @@ __device__ __forceinline__ uint64_t weight(double z8, double bin) {
   // rounded to a whole number by the addition; its bits are the mantissa's
   const double y = __builtin_fma(p, 0x1p36, 0x1p52);
   return (uint64_t)__double_as_longlong(y) & (((uint64_t)1 << 52) - 1);
+}
+
+// Whether a row's filters cut anywhere that bins are needed for.
+struct Filters {
+  int k;
+  float p, m;
+  bool any;
+};
+__device__ __forceinline__ Filters filters_of(const SampleArgs& a, int b) {
+  Filters f;
+  f.k = a.top_k != nullptr ? a.top_k[b] : a.top_k_all;
+  f.p = a.top_p != nullptr ? a.top_p[b] : a.top_p_all;
+  f.m = a.min_p != nullptr ? a.min_p[b] : a.min_p_all;
+  f.any = (f.k > 0 && f.k < a.V) || f.p < 1.0f || f.m > 0.0f;
+  return f;
 }
 
 // Ascending keys for descending logits (-0 and 0 are equal).
@@ -140,20 +201,35 @@ __device__ __forceinline__ float wave_max_f(float v) {
 template <int T>
 __global__ __launch_bounds__(kBinThreads) void k_sample_bins(SampleArgs a) {
   constexpr int kPieces = kSampleChunk / 8 / kBinThreads;
-  __shared__ uint64_t bins[kCopies][kPitch];
+  __shared__ union {
+    uint64_t bins[kCopies][kPitch];
+    double scale[kPitch];
+  } s;
   __shared__ float tops[kBinThreads / 64];
+  __shared__ double sums[kBinThreads / 64];
   __shared__ int first, last, bad;
   const int c = blockIdx.x, b = blockIdx.y;
   const Row r = row_of<T>(a, b);
+  const bool any = filters_of(a, b).any;
+  Piece<T> raw[kPieces];
   float x[kPieces][8];
   int at[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     at[i] = c * kSampleChunk + (i * kBinThreads + (int)threadIdx.x) * 8;
-    load8<T>(r.base, at[i], r.mis, r.end, x[i]);
+    raw[i] = load_piece<T>(r.base, at[i], r.mis, r.end);
   }
-  for (int i = threadIdx.x; i < kCopies * kPitch; i += kBinThreads) (&bins[0][0])[i] = 0;
+  if (any)
+    for (int i = threadIdx.x; i < kCopies * kPitch; i += kBinThreads) (&s.bins[0][0])[i] = 0;
+  else
+    for (int i = threadIdx.x; i <= kLastBin; i += kBinThreads) s.scale[i] = bin_scale(i);
   if (threadIdx.x == 0) first = 0x7fffffff, last = 0, bad = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    patch_piece<T>(raw[i], r.base, at[i], r.mis, r.end);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[i][e] = raw[i].value(e);
+  }
   float top = -INFINITY;
   bool wrong = false;
 #pragma unroll
@@ -170,6 +246,7 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(SampleArgs a) {
 #pragma unroll
   for (int w = 0; w < kBinThreads / 64; ++w) top = fmaxf(top, tops[w]);
 
+  double sum = 0.0;
   if (r.greedy) {
     int mine = 0x7fffffff;
 #pragma unroll
@@ -177,26 +254,44 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(SampleArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (x[i][e] == top) mine = min(mine, at[i] + e - r.mis);
-    if (mine != 0x7fffffff) atomicMin(&first, mine);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mine = min(mine, __shfl_xor(mine, o, 64));
+    if ((threadIdx.x & 63) == 0) atomicMin(&first, mine);
+  } else if (top > -INFINITY && !any) {
+    // only the chunk's mass, below its own maximum's bin
+    const double upper = floor(sevenths(top, r.per7));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double z7 = sevenths(x[i][e], r.per7);
+        const double bin = floor(z7);
+        const double below = upper - bin;
+        if (below <= (double)kLastBin) sum += (double)weight(z7, bin) * s.scale[(int)below];
+      }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
   } else if (top > -INFINITY) {
-    uint64_t* own = bins[threadIdx.x & (kCopies - 1)];
-    const double upper = floor(eighths(top, r.per8));
+    uint64_t* own = s.bins[threadIdx.x & (kCopies - 1)];
+    const double upper = floor(sevenths(top, r.per7));
     int low = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const double z8 = eighths(x[i][e], r.per8);
-        const double bin = floor(z8);
+        const double z7 = sevenths(x[i][e], r.per7);
+        const double bin = floor(z7);
         const double below = upper - bin;
         if (below <= (double)kLastBin) {  // (not where z is -inf or NaN)
           const int rel = (int)below;
           low = max(low, rel);
           atomicAdd(reinterpret_cast<unsigned long long*>(own + rel),
-                    (unsigned long long)(weight(z8, bin) + ((uint64_t)1 << kCountShift)));
+                    (unsigned long long)(weight(z7, bin) + ((uint64_t)1 << kCountShift)));
         }
       }
-    atomicMax(&last, low);
+    low = wave_max(low);
+    if ((threadIdx.x & 63) == 0) atomicMax(&last, low);
   }
   __syncthreads();
   const int64_t place = (int64_t)b * a.S + c;
@@ -206,457 +301,577 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(SampleArgs a) {
     h.first = first;
     h.last = r.greedy || !(top > -INFINITY) ? -1 : last;
     h.bad = bad;
+    h.mass = 0.0;
+    if (!r.greedy && !any && top > -INFINITY)
+      for (int w = 0; w < kBinThreads / 64; ++w) h.mass += sums[w];
     a.heads[place] = h;
   }
-  if (r.greedy) return;
+  if (r.greedy || !any) return;
   uint64_t* out = a.bins + place * kPitch;
   for (int i = threadIdx.x; i <= last; i += kBinThreads) {
     uint64_t n = 0;
 #pragma unroll
-    for (int k = 0; k < kCopies; ++k) n += bins[k][i];
+    for (int k = 0; k < kCopies; ++k) n += s.bins[k][i];
     out[i] = n;
   }
 }
 
 // ----------------------------------------------------------- the row's token
 
-__device__ __forceinline__ double shfl_up_d(double v, int o) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = __shfl_up((uint32_t)u, o, 64), hi = __shfl_up((uint32_t)(u >> 32), o, 64);
-  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
-__device__ __forceinline__ uint64_t shfl_up_u(uint64_t u, int o) {
-  const uint32_t lo = __shfl_up((uint32_t)u, o, 64), hi = __shfl_up((uint32_t)(u >> 32), o, 64);
-  return (uint64_t)hi << 32 | lo;
-}
+constexpr int kPickWaves = kPickThreads / 64;
+static_assert(kPickWaves == 8, "the waves' sums are joined by eights of lanes");
 
 // Inclusive sums over the workgroup's threads, in a fixed order.
-template <typename V, typename F>
-__device__ __forceinline__ V block_scan(V x, V* part, F up) {
+template <typename V>
+__device__ __forceinline__ V block_scan(V x, V* part) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const V y = up(x, o);
+    const V y = __shfl_up(x, o, 64);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 63) part[wave] = x;
   __syncthreads();
-  V before = 0;
-  for (int w = 0; w < wave; ++w) before += part[w];
-  return before + x;
+  V p = part[lane & 7];
+#pragma unroll
+  for (int o = 1; o < kPickWaves; o <<= 1) {
+    const V y = __shfl_up(p, o, 64);
+    if ((lane & 7) >= o) p += y;
+  }
+  const V before = __shfl(p, wave > 0 ? wave - 1 : 0, 64);
+  return wave > 0 ? before + x : x;
+}
+// The same of two numbers at once, behind the same barriers.
+template <typename V>
+__device__ __forceinline__ void scan_both(V& x, uint32_t& n, V* part, uint32_t* part_n) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const V y = __shfl_up(x, o, 64);
+    const uint32_t m = __shfl_up(n, o, 64);
+    if (lane >= o) x += y, n += m;
+  }
+  __syncthreads();
+  if (lane == 63) part[wave] = x, part_n[wave] = n;
+  __syncthreads();
+  V p = part[lane & 7];
+  uint32_t q = part_n[lane & 7];
+#pragma unroll
+  for (int o = 1; o < kPickWaves; o <<= 1) {
+    const V y = __shfl_up(p, o, 64);
+    const uint32_t m = __shfl_up(q, o, 64);
+    if ((lane & 7) >= o) p += y, q += m;
+  }
+  const V before = __shfl(p, wave > 0 ? wave - 1 : 0, 64);
+  const uint32_t n_before = __shfl(q, wave > 0 ? wave - 1 : 0, 64);
+  if (wave > 0) x += before, n += n_before;
+}
+
+// The first (or last) thread whose `yes` is set, -1: none.  Not by an atomic
+// that all of them would wait for one another at (27 us for 8192 on one word).
+template <bool FIRST>
+__device__ __forceinline__ int block_find(bool yes, int* part) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t set = __ballot(yes);
+  __syncthreads();
+  if (lane == 0) part[wave] = set == 0 ? -1 : wave * 64 + (FIRST ? __builtin_ctzll(set) : 63 - __builtin_clzll(set));
+  __syncthreads();
+  const int mine = part[lane & 7];
+  const uint64_t waves = __ballot(mine >= 0) & 0xff;
+  if (waves == 0) return -1;
+  return __shfl(mine, FIRST ? __builtin_ctzll(waves) : 63 - __builtin_clzll(waves), 64);
+}
+// Places behind *n for the lanes that are here, one atomic for all of them.
+__device__ __forceinline__ int append(int* n) {
+  const uint64_t here = __ballot(true);
+  const int lane = threadIdx.x & 63, leader = __builtin_ctzll(here);
+  int first = 0;
+  if (lane == leader) first = atomicAdd(n, __popcll(here));
+  first = __builtin_amdgcn_readlane(first, leader);
+  return first + __popcll(here & (((uint64_t)1 << lane) - 1));
 }
 
 struct Pick {
-  double scale[kPitch];   // e^(-bin / 8)
+  double scale[kPitch];   // e^(-bin / 7)
   double mass[kPitch];    // before a bin, in bin order (largest z first)
   uint64_t in[kPitch];    // in a bin
   uint32_t count[kPitch];   // before a bin
   uint32_t own[kPitch];     // in a bin
-  union {
-    uint64_t list[kList];
-    struct {
-      uint64_t mass[kDigits];
-      uint32_t count[kDigits];
-    } digit;
-  };
+  uint64_t list[kList];     // tokens of a bin, in any order
+  uint64_t digit_mass[kCopies / 2][kDigits];
+  uint32_t digit_count[kCopies / 2][kDigits];
   uint64_t extra[kSampleMaxChunks];  // of the bin that is kept in part
   double chunk[kSampleMaxChunks];    // kept mass of a chunk
   int off[kSampleMaxChunks], last[kSampleMaxChunks];
-  uint8_t has[kSampleMaxChunks];
-  uint64_t part_u[kPickThreads / 64];
-  double part_d[kPickThreads / 64];
-  float tops[kPickThreads / 64];
-  int found, n;
-  uint64_t answer_comp, answer_mass;
+  int has[kSampleMaxChunks];         // chunks with tokens of a bin
+  uint32_t ties[kSampleMaxChunks];   // tokens of a chunk with one logit
+  unsigned long long part_u[kPickWaves];
+  double part_d[kPickWaves];
+  uint32_t part_n[kPickWaves];
+  int part_i[kPickWaves];
+  float tops[kPickWaves];
+  int found, n, n_has;
+  uint64_t answer[4];
 };
 
+__device__ __forceinline__ void add_lds(uint64_t* p, uint64_t x) {
+  atomicAdd(reinterpret_cast<unsigned long long*>(p), (unsigned long long)x);
+}
+
+// A logit by its place.
 template <int T>
-struct Picker {
-  const SampleArgs& a;
-  Pick& s;
-  Row r;
-  int b;
-  double upper;     // the maximum's bin
-  int listed = -1;  // the bin that s.list holds, sorted
+__device__ __forceinline__ float load1(const void* base, int v) {
+  if constexpr (T == kF32)
+    return static_cast<const float*>(base)[v];
+  else if constexpr (T == kBF16)
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[v] << 16);
+  else
+    return h2f(static_cast<const uint16_t*>(base)[v]);
+}
 
-  __device__ Picker(const SampleArgs& a_, Pick& s_, int b_) : a(a_), s(s_), b(b_) { r = row_of<T>(a, b); }
+// The code is kept short on purpose (one copy of the scan, loops that are not
+// unrolled): a workgroup runs each part once or twice, and instructions that
+// are fetched once cost more than what they save.
+template <int T>
+__global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
+  __shared__ Pick s;
+  constexpr int kGrain = T == kF32 ? 0 : T == kBF16 ? 16 : 13;  // keys differ by 2^kGrain at least
+  const int tid = threadIdx.x, b = blockIdx.x;
+  const Row r = row_of<T>(a, b);
+  const Filters f = filters_of(a, b);
+  const float t = a.temperature != nullptr ? a.temperature[b] : a.temperature_all;
+  const float given = a.u[b];
 
-  __device__ __forceinline__ uint64_t word(int c, int bin) const {
+  // the chunks' heads
+  SampleHead h{-INFINITY, 0, -1, 0, 0.0};
+  if (tid < a.S) h = a.heads[(int64_t)b * a.S + tid];
+  if (tid == 0) s.n = 0, s.found = 0x7fffffff;
+  float top = wave_max_f(h.top);
+  if ((tid & 63) == 0) s.tops[tid >> 6] = top;
+  __syncthreads();
+  for (int w = 0; w < kSampleMaxChunks / 64 + 1; ++w) top = fmaxf(top, s.tops[w]);
+  if (h.bad) s.n = 1;
+  if (r.greedy && tid < a.S && h.top == top) atomicMin(&s.found, h.first);
+  __syncthreads();
+  const bool none = s.n != 0 || !(top > -INFINITY) || t != t;
+  if (none || r.greedy) {
+    if (tid == 0) a.tokens[b] = none ? -1 : s.found;
+    return;
+  }
+  const double top7 = sevenths(top, r.per7);
+  const double upper = floor(top7);  // the maximum's bin
+  if (tid < kSampleMaxChunks) {
+    int off = 1 << 20;
+    if (tid < a.S && h.last >= 0) {
+      const double d = upper - floor(sevenths(h.top, r.per7));
+      if (d <= (double)kLastBin) off = (int)d;
+    }
+    s.off[tid] = off;
+    s.last[tid] = h.last;
+    s.extra[tid] = 0;
+    s.chunk[tid] = off <= kLastBin ? h.mass * bin_scale(off) : 0.0;
+  }
+  if (tid <= kLastBin) s.scale[tid] = bin_scale(tid);
+  __syncthreads();
+
+  // A chunk's word of a bin.  It is read in any case, so that loads do not
+  // wait for one another; what is not there is 0.
+  const uint64_t* words = a.bins + (int64_t)b * a.S * kPitch;
+  auto word = [&](int c, int bin) __attribute__((always_inline)) {
     const int j = bin - s.off[c];
-    return j >= 0 && j <= s.last[c] ? a.bins[((int64_t)b * a.S + c) * kPitch + j] : 0;
-  }
-  __device__ __forceinline__ uint64_t comp(float x, int v) const {
+    const bool there = j >= 0 && j <= s.last[c];
+    const uint64_t x = words[c * kPitch + (there ? j : 0)];
+    return there ? x : 0;
+  };
+  auto comp = [&](float x, int v) __attribute__((always_inline)) {
     return (uint64_t)key_of(x) << 32 | (uint32_t)(v - r.mis);
-  }
+  };
 
-  // f(x, place, z8) for the tokens of a bin.
-  template <typename F>
-  __device__ __forceinline__ void each(int bin, F f) {
-    __syncthreads();
-    if ((int)threadIdx.x < a.S) s.has[threadIdx.x] = (word(threadIdx.x, bin) >> kCountShift) != 0;
-    __syncthreads();
-    const double at = upper - (double)bin;
-    // logits of the bin, generously, in 32 bits
-    const double lo = at / r.per8, hi = (at + 1.0) / r.per8;
-    float flo = (float)(lo - (fabs(lo) * 1e-6 + 1e-40)), fhi = (float)(hi + (fabs(hi) * 1e-6 + 1e-40));
-    if (!(r.per8 > 0.0)) flo = -INFINITY, fhi = INFINITY;  // an infinite temperature
-    for (int c = 0; c < a.S; ++c) {
-      if (!s.has[c]) continue;
-      const int v0 = c * kSampleChunk + (int)threadIdx.x * 8;
-      float x[8];
-      load8<T>(r.base, v0, r.mis, r.end, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (x[e] >= flo && x[e] <= fhi) {
-          const double z8 = eighths(x[e], r.per8);
-          if (floor(z8) == at) f(x[e], v0 + e, z8);
-        }
-    }
-  }
-
-  // Where the tokens of `bin` stop being kept: those whose rank in the bin is
-  // below `most` and that have less than `limit` before them, `before` of it
-  // ahead of the bin.  Returns the last one that is kept, and the kept mass.
-  __device__ void resolve(int bin, double before, uint32_t most, double limit, uint64_t* last,
-                          uint64_t* mass) {
-    const double scale = s.scale[bin];
-    auto keeps = [&](uint32_t rank, uint64_t m) {
-      return rank < most && (before + (double)m * scale < limit || (before == 0.0 && m == 0));
-    };
-    uint32_t n = s.own[bin], rank0 = 0;
-    uint64_t mass0 = 0, want = 0, mask = 0;  // keys (key & mask) == want are left
-    if (n > kList) {
-      const int shifts[3] = {21, 10, 0};
-      for (int d = 0; d < 3 && n > kList; ++d) {
-        listed = -1;
-        __syncthreads();
-        for (int i = threadIdx.x; i < kDigits; i += kPickThreads) s.digit.mass[i] = 0, s.digit.count[i] = 0;
-        const int shift = shifts[d];
-        each(bin, [&](float x, int, double z8) {
-          const uint32_t k = key_of(x);
-          if ((k & mask) != want) return;
-          const uint32_t i = (k >> shift) & (d == 2 ? 1023u : 2047u);
-          atomicAdd(s.digit.count + i, 1u);
-          atomicAdd(reinterpret_cast<unsigned long long*>(s.digit.mass + i),
-                    (unsigned long long)weight(z8, upper - (double)bin));
-        });
-        if (threadIdx.x == 0) s.found = kDigits;
-        __syncthreads();
-        // two digits a thread
-        const int i0 = threadIdx.x * 2;
-        const uint64_t m0 = s.digit.mass[i0], m1 = s.digit.mass[i0 + 1];
-        const uint32_t c0 = s.digit.count[i0], c1 = s.digit.count[i0 + 1];
-        const uint64_t mi = block_scan<uint64_t>(m0 + m1, s.part_u, shfl_up_u) + mass0;
-        const uint64_t ci = block_scan<uint64_t>((uint64_t)c0 + c1, s.part_u, shfl_up_u) + rank0;
-        // the last digit whose first token is kept
-        const uint64_t ma = mi - m0 - m1, mb = mi - m1;
-        const uint32_t ca = (uint32_t)ci - c0 - c1, cb = (uint32_t)ci - c1;
-        int mine = -1;
-        if (c0 > 0 && keeps(ca, ma)) mine = i0;
-        if (c1 > 0 && keeps(cb, mb)) mine = i0 + 1;
-        __syncthreads();
-        if (threadIdx.x == 0) s.found = -1;
-        __syncthreads();
-        if (mine >= 0) atomicMax(&s.found, mine);
-        __syncthreads();
-        const int digit = s.found;
-        if (mine == digit) {
-          s.answer_comp = digit & 1 ? cb : ca;
-          s.answer_mass = digit & 1 ? mb : ma;
-          s.n = (int)(digit & 1 ? c1 : c0);
-        }
-        __syncthreads();
-        rank0 = (uint32_t)s.answer_comp;
-        mass0 = s.answer_mass;
-        n = (uint32_t)s.n;
-        want |= (uint64_t)digit << shift;
-        mask |= (uint64_t)(d == 2 ? 1023u : 2047u) << shift;
-        __syncthreads();
-      }
-      if (n > kList) {
-        // one key, many tokens: a number of them, in index order
-        const uint32_t key = (uint32_t)want;
-        const double z8 = eighths(of_key(key), r.per8);
-        const uint64_t w = weight(z8, upper - (double)bin);
-        uint32_t lo = 1, hi = n;
-        while (lo < hi) {
-          const uint32_t mid = lo + (hi - lo + 1) / 2;
-          if (keeps(rank0 + mid - 1, mass0 + (uint64_t)(mid - 1) * w)) lo = mid; else hi = mid - 1;
-        }
-        *mass = mass0 + (uint64_t)lo * w;
-        // the lo-th of them: threads take runs that follow one another
-        const int per = (r.end + 8 * kPickThreads - 1) / (8 * kPickThreads) * 8;
-        uint32_t mine = 0;
-        for (int v = (int)threadIdx.x * per; v < (int)threadIdx.x * per + per; v += 8) {
-          float x[8];
-          load8<T>(r.base, v, r.mis, r.end, x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mine += v + e >= r.mis && v + e < r.end && key_of(x[e]) == key;
-        }
-        const uint64_t upto = block_scan<uint64_t>(mine, s.part_u, shfl_up_u);
-        if (upto >= lo && upto - mine < lo) {
-          uint32_t left = lo - (uint32_t)(upto - mine);
-          for (int v = (int)threadIdx.x * per; left > 0; v += 8) {
-            float x[8];
-            load8<T>(r.base, v, r.mis, r.end, x);
-            for (int e = 0; e < 8 && left > 0; ++e)
-              if (v + e >= r.mis && v + e < r.end && key_of(x[e]) == key && --left == 0) s.found = v + e - r.mis;
-          }
-        }
-        __syncthreads();
-        *last = (uint64_t)key << 32 | (uint32_t)s.found;
-        __syncthreads();
-        return;
-      }
-    }
-    if (listed != bin || mask != 0) {
-      __syncthreads();
-      if (threadIdx.x == 0) s.n = 0;
-      for (int i = threadIdx.x; i < kList; i += kPickThreads) s.list[i] = ~(uint64_t)0;
-      each(bin, [&](float x, int v, double) {
-        if ((key_of(x) & mask) != want) return;
-        const int i = atomicAdd(&s.n, 1);
-        if (i < kList) s.list[i] = comp(x, v);
-      });
-      int size = 2;
-      while (size < (int)n) size *= 2;
-      // bitonic
-      for (int k = 2; k <= size; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) {
-          __syncthreads();
-          for (int t = threadIdx.x; t < size / 2; t += kPickThreads) {
-            const int i = 2 * t - (t & (j - 1));
-            const uint64_t x = s.list[i], y = s.list[i + j];
-            if ((x > y) == ((i & k) == 0)) s.list[i] = y, s.list[i + j] = x;
-          }
-        }
-      listed = mask == 0 ? bin : -1;
-    }
-    __syncthreads();
-    const uint32_t i0 = threadIdx.x * 2;
-    uint64_t c[2], w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c[i] = s.list[i0 + i];
-      w[i] = i0 + i < n ? weight(eighths(of_key((uint32_t)(c[i] >> 32)), r.per8), upper - (double)bin) : 0;
-    }
-    const uint64_t upto = block_scan<uint64_t>(w[0] + w[1], s.part_u, shfl_up_u) + mass0;
-    __syncthreads();
-    if (threadIdx.x == 0) s.found = -1;
-    __syncthreads();
-    int mine = -1;
-    if (i0 < n && keeps(rank0 + i0, upto - w[0] - w[1])) mine = (int)i0;
-    if (i0 + 1 < n && keeps(rank0 + i0 + 1, upto - w[1])) mine = (int)i0 + 1;
-    if (mine >= 0) atomicMax(&s.found, mine);
-    __syncthreads();
-    if (mine == s.found) {
-      s.answer_comp = c[mine & 1];
-      s.answer_mass = mine & 1 ? upto : upto - w[1];
-    }
-    __syncthreads();
-    *last = s.answer_comp;
-    *mass = s.answer_mass;
-    __syncthreads();
-  }
-
-  __device__ void run() {
-    const int tid = threadIdx.x;
-    // the chunks' heads
-    float top = -INFINITY;
-    int first = 0x7fffffff, bad = 0;
-    SampleHead h{-INFINITY, 0, -1, 0};
-    if (tid < a.S) h = a.heads[(int64_t)b * a.S + tid];
-    if (tid == 0) s.n = 0, s.found = 0x7fffffff;
-    top = wave_max_f(h.top);
-    if ((tid & 63) == 0) s.tops[tid >> 6] = top;
-    __syncthreads();
-    for (int w = 0; w < kPickThreads / 64; ++w) top = fmaxf(top, s.tops[w]);
-    if (h.bad) s.n = 1;
-    if (r.greedy && tid < a.S && h.top == top) atomicMin(&s.found, h.first);
-    __syncthreads();
-    bad = s.n;
-    first = s.found;
-    const float t = a.temperature != nullptr ? a.temperature[b] : a.temperature_all;
-    if (bad || !(top > -INFINITY) || t != t || r.greedy) {
-      if (tid == 0) a.tokens[b] = bad || !(top > -INFINITY) || t != t ? -1 : first;
-      return;
-    }
-    const double top8 = eighths(top, r.per8);
-    upper = floor(top8);
-    if (tid < kSampleMaxChunks) {
-      int off = 1 << 20;
-      if (tid < a.S && h.last >= 0) {
-        const double d = upper - floor(eighths(h.top, r.per8));
-        if (d <= (double)kLastBin) off = (int)d;
-      }
-      s.off[tid] = off;
-      s.last[tid] = h.last;
-      s.extra[tid] = 0;
-    }
-    __syncthreads();
-
+  // The cut: bins before `bin` are kept, of it the tokens up to `cut` in order
+  // and from `least` on in z7.
+  int bin = kLastBin + 1;
+  uint64_t cut = ~(uint64_t)0;
+  double least = -INFINITY;
+  if (f.any) {
     // all chunks' bins, and what lies before each
     uint64_t m = 0;
     uint32_t n = 0;
-    double scale = 0.0;
     if (tid <= kLastBin) {
+#pragma unroll 16
       for (int c = 0; c < a.S; ++c) {
         const uint64_t x = word(c, tid);
         m += x & kMass;
         n += (uint32_t)(x >> kCountShift);
       }
-      scale = exp(-0.125 * tid);
-      s.scale[tid] = scale;
       s.in[tid] = m;
       s.own[tid] = n;
     }
-    const double own = (double)m * scale;
-    const double upto = block_scan<double>(own, s.part_d, shfl_up_d);
-    const uint64_t nupto = block_scan<uint64_t>(n, s.part_u, shfl_up_u);
+    const double own = tid <= kLastBin ? (double)m * s.scale[tid] : 0.0;
+    double upto = own;
+    uint32_t nupto = n;
+    scan_both(upto, nupto, s.part_d, s.part_n);
     if (tid <= kLastBin) {
-      s.mass[tid] = upto - own;
-      s.count[tid] = (uint32_t)nupto - n;
+      s.mass[tid] = tid == 0 ? 0.0 : upto - own;
+      s.count[tid] = nupto - n;
     }
+    if (tid == kLastBin) s.answer[0] = nupto, s.answer[1] = (uint64_t)__double_as_longlong(upto);
     __syncthreads();
-    if (tid == kLastBin) s.answer_mass = (uint64_t)__double_as_longlong(upto), s.answer_comp = nupto;
-    if (tid == 0) s.mass[0] = 0.0;
-    __syncthreads();
-    double total = __longlong_as_double((long long)s.answer_mass);
-    const uint32_t all = (uint32_t)s.answer_comp;
+    const uint32_t all = (uint32_t)s.answer[0];
+    double total = __longlong_as_double((long long)s.answer[1]);
+    uint32_t most = 0xffffffffu;  // tokens of `bin` that top-k leaves
+    int listed = -1, n_list = 0;  // the bin that s.list holds
 
-    // the cut: bins before `bin` are kept, of it the tokens up to `comp`
-    int bin = kLastBin + 1;
-    uint64_t cut = ~(uint64_t)0;
-    uint32_t most = 0xffffffffu;
-    const int k = a.top_k != nullptr ? a.top_k[b] : a.top_k_all;
-    if (k > 0 && (uint32_t)k < all) {
-      __syncthreads();
-      if (tid <= kLastBin && s.own[tid] > 0 && s.count[tid] < (uint32_t)k && s.count[tid] + s.own[tid] >= (uint32_t)k)
-        s.found = tid;
-      __syncthreads();
-      bin = s.found;
-      most = (uint32_t)k - s.count[bin];
-      uint64_t kept = s.in[bin];
-      if (most < s.own[bin])
-        resolve(bin, s.mass[bin], most, INFINITY, &cut, &kept);
-      else
-        most = 0xffffffffu;
-      total = s.mass[bin] + (double)kept * s.scale[bin];
-    }
-    const float p = a.top_p != nullptr ? a.top_p[b] : a.top_p_all;
-    if (p < 1.0f) {
-      const double limit = (double)p * total;
-      __syncthreads();
-      if (tid == 0) s.found = 0;
-      __syncthreads();
-      // the last bin whose first token is kept
-      const bool starts = tid <= kLastBin && tid <= bin && s.own[tid] > 0 && s.mass[tid] < limit;
-      if (starts) atomicMax(&s.found, tid);
-      __syncthreads();
-      const int at = s.found;
-      uint64_t kept = 0;
-      resolve(at, s.mass[at], at == bin ? most : 0xffffffffu, limit, &cut, &kept);
+    // top-k, top-p, and with min-p the kept mass of the bin that is cut
+#pragma unroll 1
+    for (int phase = 0; phase < 3; ++phase) {
+      // Tokens of bin `at` are kept whose rank in it is below `ranks` and that
+      // have less than `limit` before them (the first of all always).
+      int at = 0;
+      uint32_t ranks = 0xffffffffu;
+      double limit = INFINITY;
+      if (phase == 0) {
+        if (f.k <= 0 || (uint32_t)f.k >= all) continue;
+        at = bin = block_find<true>(
+            tid <= kLastBin && s.own[tid] > 0 && s.count[tid] + s.own[tid] >= (uint32_t)f.k, s.part_i);
+        ranks = most = (uint32_t)f.k - s.count[bin];
+        total = s.mass[bin] + (double)s.in[bin] * s.scale[bin];
+        if (most == s.own[bin]) continue;  // between two bins
+      } else if (phase == 1) {
+        if (!(f.p < 1.0f)) continue;
+        limit = (double)f.p * total;
+        // the last bin whose first token is kept
+        at = block_find<false>(
+            tid == 0 || (tid <= kLastBin && tid <= bin && s.own[tid] > 0 && s.mass[tid] < limit), s.part_i);
+        if (at == bin) ranks = most;
+      } else {
+        if (f.m > 0.0f) {
+          const double z7 = top7 + 7.0 * log((double)fminf(f.m, 1.0f));
+          const double below = upper - floor(z7);
+          if (below <= (double)bin) {
+            if (below < (double)bin) bin = (int)below, cut = ~(uint64_t)0;
+            least = z7;
+          }
+        }
+        if (bin > kLastBin || listed == bin) continue;
+        at = bin;
+      }
+      const double before = s.mass[at], scale = s.scale[at], lower = upper - (double)at;
+      auto keeps = [&](uint32_t rank, uint64_t m) __attribute__((always_inline)) {
+        return rank < ranks && (before + (double)m * scale < limit || (before == 0.0 && m == 0));
+      };
+      // the bin's logits, generously, in 32 bits, and their keys
+      const double lo = lower / r.per7, hi = (lower + 1.0) / r.per7;
+      float flo = (float)(lo - (fabs(lo) * 1e-6 + 1e-40)), fhi = (float)(hi + (fabs(hi) * 1e-6 + 1e-40));
+      if (!(r.per7 > 0.0)) flo = -INFINITY, fhi = INFINITY;  // an infinite temperature
+      uint32_t k0 = key_of(fhi), k1 = key_of(flo), left = s.own[at], rank0 = 0;
+      uint64_t mass0 = 0;
+
+      // The bin's tokens are read from the row into the list, if that holds
+      // them (kFill), then taken from there, else from the row each time: to split
+      // what is left of the keys until it is one (kSplit), at last to count by
+      // chunk the tokens that have it (kTies); with min-p to add up what is kept
+      // (kSum; from a list this is done below).
+      enum { kFill, kSplit, kTies, kSum };
+      int step = left <= kList && listed != at ? kFill : phase == 2 ? kSum : kSplit;
+      uint32_t ties = 0;  // tokens of the last key that are kept
+#pragma unroll 1
+      for (;;) {
+        int shift = 32 - __builtin_clz(k1 - k0 | 1) - kDigitBits;
+        if (shift < 0) shift = 0;
+        __syncthreads();
+        if (tid == 0) s.n = 0, s.n_has = 0;
+        if (step == kSplit)
+#pragma unroll
+          for (int i = 0; i < kCopies / 2; ++i) s.digit_mass[i][tid] = 0, s.digit_count[i][tid] = 0;
+        if (step == kTies && tid < kSampleMaxChunks) s.ties[tid] = 0;
+        __syncthreads();
+        auto take = [&](uint32_t key, uint32_t index, int c) __attribute__((always_inline)) {
+          if (key < k0 || key > k1) return;
+          if (step == kTies) {
+            atomicAdd(s.ties + c, 1u);
+            return;
+          }
+          const double z7 = sevenths(of_key(key), r.per7);
+          if (floor(z7) != lower) return;
+          uint64_t* sum = s.extra + c;
+          if (step == kSplit) {
+            const uint32_t i = (tid & (kCopies / 2 - 1)) * kDigits + ((key - k0) >> shift);
+            sum = &s.digit_mass[0][0] + i;
+            atomicAdd(&s.digit_count[0][0] + i, 1u);
+          } else if (((uint64_t)key << 32 | index) > cut || z7 < least) {
+            return;
+          }
+          add_lds(sum, weight(z7, lower));
+        };
+        if (listed == at) {
+#pragma unroll 1
+          for (int i = tid; i < n_list; i += kPickThreads) {
+            const uint64_t x = s.list[i];
+            take((uint32_t)(x >> 32), (uint32_t)x, ((int)(uint32_t)x + r.mis) / kSampleChunk);
+          }
+        } else {
+          if (tid < a.S && (word(tid, at) >> kCountShift) != 0) s.has[append(&s.n_has)] = tid;  // (any order)
+          __syncthreads();
+          // pieces of 8 logits, two of a chunk for each thread
+          constexpr int kU = T == kF32 ? 4 : 8;  // in flight
+          const int pieces = s.n_has * 2;
+#pragma unroll 1
+          for (int i = 0; i < pieces; i += kU) {
+            Piece<T> x[kU];
+            int v0[kU];
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+              const int j = min(i + k, pieces - 1);
+              v0[k] = s.has[j >> 1] * kSampleChunk + ((j & 1) * kPickThreads + tid) * 8;
+              x[k] = load_piece<T>(r.base, v0[k], r.mis, r.end);
+            }
+            uint64_t hits = 0;
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+              patch_piece<T>(x[k], r.base, v0[k], r.mis, r.end);
+              uint32_t h = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float y = x[k].value(e);
+                h |= (y >= flo && y <= fhi ? 1u : 0u) << e;
+              }
+              if (i + k < pieces) hits |= (uint64_t)h << 8 * k;
+            }
+            if (step == kFill) {
+              // places in the list for all of a wave's at once; a token goes there
+              // as its piece, thread and bit, and is looked up afterwards, so that
+              // no load is waited for here
+              const int mine = __popcll(hits);
+              int j = mine;
+#pragma unroll
+              for (int o = 1; o < 64; o <<= 1) {
+                const int y = __shfl_up(j, o, 64);
+                if ((tid & 63) >= o) j += y;
+              }
+              int first = 0;
+              if ((tid & 63) == 63 && j > 0) first = atomicAdd(&s.n, j);
+              j += __builtin_amdgcn_readlane(first, 63) - mine;
+#pragma unroll 1
+              for (; hits != 0; hits &= hits - 1, ++j) {
+                const int k = __builtin_ctzll(hits);
+                if (j < kList) s.list[j] = (uint64_t)((i + (k >> 3)) * (8 * kPickThreads) + tid * 8 + (k & 7));
+              }
+            }
+#pragma unroll 1
+            while (hits != 0) {
+              const int k = __builtin_ctzll(hits);
+              hits &= hits - 1;
+              const int p = i + (k >> 3), c = s.has[p >> 1];
+              const int v = c * kSampleChunk + ((p & 1) * kPickThreads + tid) * 8 + (k & 7);
+              // (what lies beside the row is no logit)
+              if (v >= r.mis && v < r.end) take(key_of(load1<T>(r.base, v)), (uint32_t)(v - r.mis), c);
+            }
+          }
+        }
+        if (step == kSum) break;
+        __syncthreads();
+        if (step == kFill) {
+          n_list = s.n;
+          listed = n_list <= kList ? at : -1;  // (bordering logits come along)
+          if (listed == at) {
+#pragma unroll 4
+            for (int i = tid; i < n_list; i += kPickThreads) {
+              const int p = (int)s.list[i] / (8 * kPickThreads), in = (int)s.list[i] % (8 * kPickThreads);
+              const int v = s.has[p >> 1] * kSampleChunk + (p & 1) * (8 * kPickThreads) + in;
+              const bool there = v >= r.mis && v < r.end;
+              const uint32_t key = key_of(load1<T>(r.base, there ? v : r.mis));
+              s.list[i] = there ? (uint64_t)key << 32 | (uint32_t)(v - r.mis) : ~(uint64_t)0;
+            }
+          }
+          if (phase == 2 && listed == at) break;
+          step = phase == 2 ? kSum : kSplit;
+          continue;
+        }
+        if (step == kTies) break;
+        // the last digit whose first token is kept
+        uint64_t m0 = 0;
+        uint32_t c0 = 0;
+#pragma unroll
+        for (int i = 0; i < kCopies / 2; ++i) m0 += s.digit_mass[i][tid], c0 += s.digit_count[i][tid];
+        unsigned long long ma = m0;
+        uint32_t ca = c0;
+        scan_both(ma, ca, s.part_u, s.part_n);
+        ma += mass0 - m0;
+        ca += rank0 - c0;
+        if (block_find<false>(c0 > 0 && keeps(ca, ma), s.part_i) == tid) {
+          s.answer[0] = ma;
+          s.answer[1] = ca;
+          s.answer[2] = c0;
+          s.answer[3] = tid;
+        }
+        __syncthreads();
+        mass0 = s.answer[0];
+        rank0 = (uint32_t)s.answer[1];
+        left = (uint32_t)s.answer[2];
+        k0 += (uint32_t)s.answer[3] << shift;
+        k1 = k0 + (1u << shift) - 1;
+        if (shift > kGrain) continue;
+        // One key is left: of logits in 16 bits the one in the range that ends
+        // in ones (positive) or zeros.
+        if (kGrain > 0) {
+          constexpr uint32_t ends = (1u << kGrain) - 1;
+          k0 = (k0 | ends) <= min(k1, 0x7fffffffu) ? k0 | ends : (k0 + ends) & ~ends;
+          k1 = k0;
+        }
+          // How many of its tokens are kept:
+        const uint64_t w = weight(sevenths(of_key(k0), r.per7), lower);
+        uint32_t least_n = 1, most_n = left;
+        while (least_n < most_n) {
+          const uint32_t mid = least_n + (most_n - least_n + 1) / 2;
+          if (keeps(rank0 + mid - 1, mass0 + (uint64_t)(mid - 1) * w)) least_n = mid; else most_n = mid - 1;
+        }
+        ties = least_n;
+        total = before + (double)(mass0 + (uint64_t)ties * w) * scale;
+        if (ties == left) break;
+        step = kTies;
+      }
+      if (phase == 2) continue;
       bin = at;
-    }
-    const float mp = a.min_p != nullptr ? a.min_p[b] : a.min_p_all;
-    double least = -INFINITY;  // z8 of min-p, where it cuts in `bin`
-    if (mp > 0.0f) {
-      const double z8 = top8 + 8.0 * log((double)fminf(mp, 1.0f));
-      const double below = upper - floor(z8);
-      if (below < (double)bin) bin = (int)below, cut = ~(uint64_t)0, least = z8;
-      else if (below == (double)bin) least = z8;
+      cut = (uint64_t)k0 << 32 | 0xffffffffu;
+      if (step != kTies) continue;
+      // the last of them in index order: its chunk, then its place there
+      uint32_t n = tid < a.S ? s.ties[tid] : 0;
+      uint32_t upto = block_scan(n, s.part_n);
+      const int c = block_find<true>(upto >= ties, s.part_i);
+      if (tid == c) s.answer[0] = upto - n;
+      __syncthreads();
+      const uint32_t rank = ties - (uint32_t)s.answer[0];
+      const int v0 = c * kSampleChunk + tid * 16;
+      uint32_t same = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        Piece<T> x = load_piece<T>(r.base, v0 + 8 * i, r.mis, r.end);
+        patch_piece<T>(x, r.base, v0 + 8 * i, r.mis, r.end);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int v = v0 + 8 * i + e;
+          same |= (key_of(x.value(e)) == k0 && v >= r.mis && v < r.end ? 1u : 0u) << (8 * i + e);
+        }
+      }
+      n = __popc(same);
+      upto = block_scan(n, s.part_n);
+      if (upto >= rank && upto - n < rank) {
+        for (uint32_t i = upto - n + 1; i < rank; ++i) same &= same - 1;
+        s.found = v0 + __builtin_ctz(same) - r.mis;
+      }
+      __syncthreads();
+      cut = (uint64_t)k0 << 32 | (uint32_t)s.found;
     }
 
     // the kept mass of each chunk
-    auto kept_in = [&](float x, int v, double z8) { return comp(x, v) <= cut && z8 >= least; };
-    if (bin <= kLastBin) {
-      const double at = upper - (double)bin;
-      each(bin, [&](float x, int v, double z8) {
-        if (kept_in(x, v, z8))
-          atomicAdd(reinterpret_cast<unsigned long long*>(s.extra + v / kSampleChunk),
-                    (unsigned long long)weight(z8, at));
-      });
+    if (listed == bin) {
+      const double lower = upper - (double)bin;
+      for (int i = tid; i < n_list; i += kPickThreads) {
+        const uint64_t x = s.list[i];
+        const double z7 = sevenths(of_key((uint32_t)(x >> 32)), r.per7);
+        if (floor(z7) == lower && x <= cut && z7 >= least) add_lds(s.extra + ((int)(uint32_t)x + r.mis) / kSampleChunk, weight(z7, lower));
+      }
     }
     __syncthreads();
+#pragma unroll 1
     for (int c = tid >> 6; c < a.S; c += kPickThreads / 64) {
       double x = 0.0;
       if (s.off[c] <= kLastBin) {
-        const uint64_t* w = a.bins + ((int64_t)b * a.S + c) * kPitch;
-        const int end = min(s.last[c], min(bin - 1, kLastBin) - s.off[c]);
-        for (int j = tid & 63; j <= end; j += 64) x += (double)(w[j] & kMass) * s.scale[j + s.off[c]];
-      }
+        const uint64_t* w = words + c * kPitch;
+        const int last = s.last[c], end = min(last, min(bin - 1, kLastBin) - s.off[c]);
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = shfl_up_d(x, o);
-        if ((tid & 63) >= o) x += y;
-      }
-      if ((tid & 63) == 63) s.chunk[c] = x + (bin <= kLastBin ? (double)s.extra[c] * s.scale[bin] : 0.0);
-    }
-    __syncthreads();
-    double sum = 0.0;
-    for (int c = 0; c < a.S; ++c) sum += s.chunk[c];
-    float u = a.u[b];
-    u = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-    const double target = (double)u * sum;
-    double begin = 0.0;
-    int c = 0;
-    while (c < a.S && !(begin + s.chunk[c] > target)) begin += s.chunk[c++];
-    // (rounding may leave nothing in the chunk: then the next one's first, or
-    // the last that is kept)
-    for (bool over = false;;) {
-      if (c >= a.S) {
-        over = true;
-        c = a.S - 1;
-        while (c > 0 && !(s.chunk[c] > 0.0)) --c;
-      }
-      const int v0 = c * kSampleChunk + tid * 8;
-      float x[8];
-      double w[8], mine = 0.0;
-      load8<T>(r.base, v0, r.mis, r.end, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double z8 = eighths(x[e], r.per8);
-        const double f = floor(z8);
-        const double below = upper - f;
-        w[e] = 0.0;
-        if (top8 - z8 < 512.0 && below <= (double)bin && (below < (double)bin || kept_in(x[e], v0 + e, z8)))
-          w[e] = (double)weight(z8, f) * s.scale[(int)below];
-        mine += w[e];
-      }
-      const double last = block_scan<double>(mine, s.part_d, shfl_up_d);
-      __syncthreads();
-      if (tid == 0) s.found = over ? -1 : 0x7fffffff;
-      __syncthreads();
-      double at = begin + (last - mine);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        at += w[e];
-        if (w[e] > 0.0) {
-          if (over)
-            atomicMax(&s.found, v0 + e);
-          else if (at > target)
-            atomicMin(&s.found, v0 + e);
+        for (int i = 0; i <= kLastBin / 64; ++i) {
+          const int j = i * 64 + (tid & 63);
+          const uint64_t m = w[min(j, last)] & kMass;  // (loads in flight together)
+          if (j <= end) x += (double)m * s.scale[j + s.off[c]];
         }
       }
-      __syncthreads();
-      const int found = s.found;
-      if (found != 0x7fffffff) {
-        if (tid == 0) a.tokens[b] = found < 0 ? -1 : found - r.mis;
-        return;
-      }
-      begin += s.chunk[c];
-      ++c;
-      __syncthreads();
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+      if ((tid & 63) == 0) s.chunk[c] = x + (bin <= kLastBin ? (double)s.extra[c] * s.scale[bin] : 0.0);
     }
+    __syncthreads();
   }
-};
 
-template <int T>
-__global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
-  __shared__ Pick s;
-  Picker<T> p(a, s, blockIdx.x);
-  p.run();
+  // three chunks a lane, every wave by itself
+  double before[3], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    before[i] = sum;
+    sum += s.chunk[(tid & 63) * 3 + i];
+  }
+  const double mine = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double y = __shfl_up(sum, o, 64);
+    if ((tid & 63) >= o) sum += y;
+  }
+  const double target = (double)(given > 0.0f ? fminf(given, 0x1.fffffep-1f) : 0.0f) * __shfl(sum, 63, 64);
+  const uint64_t past = __ballot(sum > target);
+  int c = a.S;
+  double begin = 0.0;
+  if (past != 0) {
+    // the chunk of the first lane that passes the target
+    const int lane = __builtin_ctzll(past);
+    const double base = __shfl(sum - mine, lane, 64);
+    int i = 0;
+#pragma unroll
+    for (int k = 1; k < 3; ++k) {
+      const double at = base + __shfl(before[k], lane, 64);
+      if (at <= target) i = k, begin = at;
+    }
+    if (i == 0) begin = base;
+    c = lane * 3 + i;
+  }
+  // (rounding may leave nothing in the chunk: then the next one's first, or the
+  // last that is kept)
+#pragma unroll 1
+  for (;;) {
+    const bool over = c >= a.S;
+    if (over) {
+      c = a.S - 1;
+      while (c > 0 && !(s.chunk[c] > 0.0)) --c;
+    }
+    const int v0 = c * kSampleChunk + tid * 16;
+    Piece<T> x0 = load_piece<T>(r.base, v0, r.mis, r.end), x1 = load_piece<T>(r.base, v0 + 8, r.mis, r.end);
+    patch_piece<T>(x0, r.base, v0, r.mis, r.end);
+    patch_piece<T>(x1, r.base, v0 + 8, r.mis, r.end);
+    auto mass = [&](float x, int v) __attribute__((always_inline)) {
+      const double z7 = sevenths(x, r.per7);
+      const double f = floor(z7);
+      const double below = upper - f;
+      return top7 - z7 < (double)kLastBin && below <= (double)bin &&
+                     (below < (double)bin || (comp(x, v) <= cut && z7 >= least))
+                 ? (double)weight(z7, f) * s.scale[(int)below]
+                 : 0.0;
+    };
+    double w[16], mine = 0.0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      w[e] = mass(e < 8 ? x0.value(e) : x1.value(e - 8), v0 + e);
+      mine += w[e];
+    }
+    double at = begin + (block_scan(mine, s.part_d) - mine);
+    int hit = -1;  // the thread's first place past the target (its last one, if nothing is)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      at += w[e];
+      if (w[e] > 0.0 && (over || (at > target && hit < 0))) hit = v0 + e;
+    }
+    const int first = over ? block_find<false>(hit >= 0, s.part_i) : block_find<true>(hit >= 0, s.part_i);
+    if (first >= 0) {
+      if (tid == first) a.tokens[b] = hit - r.mis;
+      return;
+    }
+    if (over) {  // (the maximum's weight is never 0)
+      if (tid == 0) a.tokens[b] = -1;
+      return;
+    }
+    begin += s.chunk[c];
+    ++c;
+    __syncthreads();
+  }
 }
 
 template <int T>

@@ -97,13 +97,14 @@ hipError_t launch_qk_rope(const QkRopeArgs& a, bool bf16, hipStream_t s);
 
 // ---- the next tokens
 constexpr int kSampleChunk = 8192;    // logits of a workgroup
-constexpr int kSampleBins = 520;      // 64-bit words that it leaves
-constexpr int kSampleMaxChunks = 136;  // of a row
+constexpr int kSampleBins = 456;      // 64-bit words that it leaves
+constexpr int kSampleMaxChunks = 192;  // of a row, three a lane of a wave
 struct SampleHead {
   float top;  // the chunk's maximum
   int first;  // greedy: the first index that has it
   int last;   // the last bin with a token, -1: none
   int bad;    // an infinity or NaN
+  double mass;  // of a row without filters, below the chunk's maximum's bin
 };
 struct SampleArgs {
   const void* logits;
