@@ -134,7 +134,7 @@ def test_reference_extend():
 
 def test_sample_refusals(lib):
     need = lib.sample_tokens_workspace_size(3, 10000)
-    assert need >= 3 * 2 * 513 * 8
+    assert need >= 3 * 2 * 449 * 8
     for bad in ((-1, 5), (5, -1), (65536, 5), (1, (1 << 20) + 1), (65535, 1 << 20)):
         assert lib.sample_tokens_workspace_size(*bad) == 0, bad
 
