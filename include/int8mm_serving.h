@@ -219,6 +219,39 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
                             float scale, int64_t window, float softcap, void* out, float* lse,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Bytes of workspace kv_attention_shared needs for these sizes (256-byte
+ * aligned); 0 for sizes that it refuses. */
+INT8MM_API size_t kv_attention_shared_workspace_size(int64_t B, int64_t q_heads, int64_t kv_heads,
+                                                     int64_t head_dim, int64_t prefix_len,
+                                                     int64_t max_len);
+
+/*
+ * kv_attention_shared -- kv_attention of a batch whose sequences all begin with
+ * the same prefix_len tokens (forks of one prompt): these are read once for the
+ * batch, from the pages
+ *   prefix_pages [ceil(prefix_len / page_size)] int32, a row of a table.
+ * Token t of every sequence is in page prefix_pages[t / page_size] if t <
+ * prefix_len, and as for kv_attention otherwise; table entries of whole prefix
+ * pages are not read.  A sequence may be shorter than the prefix: it sees its
+ * first lengths[row] tokens.  All else as kv_attention, but that
+ *   - an infinity or NaN makes what depends on it infinite or NaN, which of the
+ *     two is unspecified;
+ *   - probabilities enter the matrix cores with 16 bits (float16: 22 bits of
+ *     those of at least 2^-14 of the maximum, ending at 2^-38 of it) where the
+ *     query heads of a kv head, of all sequences, are more than 16;
+ *   - how sums are rounded may depend on the sizes of the batch and on all
+ *     sequences' lengths; the same call gives the same bits again.
+ * prefix_len 0 .. 2^30.  Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.
+ */
+INT8MM_API int kv_attention_shared(const void* q, int dtype, int64_t B, int64_t q_heads,
+                                   int64_t q_batch_stride, int64_t q_head_stride,
+                                   const int8mm_kv* kv, const int32_t* table, int64_t table_rows,
+                                   int64_t table_width, const int32_t* lengths,
+                                   const int32_t* rows, const int32_t* prefix_pages,
+                                   int64_t prefix_len, int64_t max_len, float scale,
+                                   int64_t window, float softcap, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Workspace of kv_pages_reserve, _extend, _fork and _compact for a pool of num_pages and n rows or pairs (256-byte aligned). */
 INT8MM_API size_t kv_pages_workspace_size(int64_t num_pages, int64_t n);
 

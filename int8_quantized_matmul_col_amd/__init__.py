@@ -69,6 +69,8 @@ from .serving import (  # noqa: F401
     int4_unpack_weight,
     kv_append,
     kv_attention,
+    kv_attention_shared,
+    kv_attention_shared_workspace_size,
     kv_attention_workspace_size,
     kv_gather,
     kv_pages_compact,

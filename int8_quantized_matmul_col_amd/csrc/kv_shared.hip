@@ -1,0 +1,644 @@
+// The attention of one new token per sequence where all sequences begin with
+// the same tokens: those are read once for the whole batch.
+//
+// Per kv head, the queries of all sequences on it (B times the query heads that
+// share it) are rows of one product with the prefix's keys, and their
+// probabilities of one with its values; each sequence's own tokens behind the
+// prefix are kv_attention's kernel's, and a third kernel joins the parts.
+//
+// The prefix's kernel.  A workgroup takes a tile of up to 16 R rows, one kv head
+// and a piece of the prefix, its 4 waves the piece's chunks of 32 tokens (64 of
+// an int8 cache) in turn.  As in kv_attention a score tile's rows are tokens,
+// permuted so that the probabilities that a lane forms are the operand of the
+// second product as they are; here one load of keys and values serves R tiles
+// of 16 rows, whose queries and outputs stay in registers (64 rows at 128 dims:
+// 64 + 128 registers, one wave a SIMD).  R = 1 is for batches of up to 16 rows,
+// two waves a SIMD.  Pieces are as long as leave one workgroup for every CU (two
+// at R = 1): each costs a partial output to write and to join.
+//
+// What bounds it: at 64 rows a tile's softmax, about 130 vector instructions for
+// 24 matrix instructions of 16 cycles; at 16 rows HBM.
+//
+// Precision as kv_attention's, but for probabilities: two bfloat16 numbers (three
+// at R = 1), which hold 16 bits, or two of float16 in one sum, which hold 22 of
+// those of at least 2^-14 of the maximum and end at 2^-38 of it.
+#include "kv_device.h"
+
+namespace i8mm {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kAlign = 64;       // of a piece's first token, a multiple of both chunk sizes
+constexpr int kMaxPieces = 512;  // of the prefix, and of a sequence's own tokens
+
+// float16: probabilities are held times 2^13, at most 2^15.
+constexpr float kSlackF16 = 2.0f, kBiasF16 = 13.0f;
+constexpr float kSlack = 8.0f;
+
+// As split() of float16, the remainder unscaled: it is at least 2^-12 of the
+// number (positive down to 2^-26 of the maximum).
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t (&part)[2]) {
+  const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), 4096u);
+  const uint32_t ub = __builtin_elementwise_sub_sat(__float_as_uint(b), 4096u);
+  const v2h h = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(ua), __uint_as_float(ub)));
+  part[0] = __builtin_bit_cast(uint32_t, h);
+  part[1] = f2h2(a - (float)h[0], b - (float)h[1]);
+}
+
+// The prefix tokens [lo, hi) that batch entry b sees.
+struct Seen {
+  int lo, hi;
+};
+__device__ __forceinline__ Seen seen_of(const KvSharedArgs& a, int b, int num_pages, int ps) {
+  const int row = a.own.rows != nullptr ? a.own.rows[b] : b;
+  Seen v{0, 0};
+  if ((unsigned)row >= (unsigned)a.own.table_rows || num_pages == 0) return v;
+  int64_t top = (int64_t)a.own.table_width * ps;
+  if (top > a.own.max_len) top = a.own.max_len;
+  int n = a.own.lengths[row];
+  n = n < 0 ? 0 : n > top ? (int)top : n;
+  v.lo = a.own.window > 0 && a.own.window < n ? n - (int)a.own.window : 0;
+  v.hi = min(n, a.prefix_len);
+  return v;
+}
+
+__device__ __forceinline__ int wave_min_i(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
+  return v;
+}
+__device__ __forceinline__ int wave_max_i(int v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = max(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// The halves of a dword that hold an infinity or NaN of the cache's type, as ones.
+template <int CT>
+__device__ __forceinline__ uint32_t endless(uint32_t u) {
+  constexpr uint32_t e = CT == kBF16 ? 0x7f80u : 0x7c00u;
+  return ((u & e) == e ? 0xffffu : 0u) | ((u >> 16 & e) == e ? 0xffff0000u : 0u);
+}
+// 1 in the operands' type.
+template <bool BF16>
+constexpr uint32_t kOne = BF16 ? 0x3f80u : 0x3c00u;
+
+// tanh from one exponential, off by at most 6 units of 2^-24.
+__device__ __forceinline__ float tanh_of(float x) {
+  const float t = __builtin_amdgcn_exp2f(fabsf(x) * (-2.0f * kLog2e));
+  return copysignf((1.0f - t) * __builtin_amdgcn_rcpf(1.0f + t), x);
+}
+
+// CT: the cache's type; QBF: bfloat16 queries; NK: 32-dim steps (EXACT: head_dim
+// is NK * 32, otherwise at most that); R: tiles of 16 rows.
+template <int CT, bool QBF, int NK, bool EXACT, int R>
+__global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_prefix(KvSharedArgs a, Pages pg) {
+  constexpr bool I8 = CT == kI8;
+  constexpr bool PBF = CT != kF16;                    // type of the P x V operands
+  constexpr int kParts = PBF ? (R == 1 ? 3 : 2) : 2;  // that hold a probability
+  constexpr int CH = I8 ? 64 : 32;       // tokens per chunk
+  constexpr int SUB = CH / 4;            // consecutive tokens a lane feeds to P x V
+  constexpr int NT = CH / 16;            // score tiles
+  constexpr int NKL = I8 ? NK / 2 : NK;  // 16-byte key loads per token row and lane
+  constexpr int DT = NK * 2;             // output tiles of 16 dims
+  constexpr int EB = I8 ? 1 : 2;
+  constexpr float kB = PBF ? 0.0f : kBiasF16, kS = PBF ? kSlack : kSlackF16;
+  const int D = EXACT ? NK * 32 : pg.D;
+
+  __shared__ float so[kWaves * DT * 256];  // outputs, [wave][tile][4][lane]
+  __shared__ float sm[kWaves * 16], sl[kWaves * 16];
+  __shared__ v4u sq[R * NK * 64];  // Q^T operands, [tile][32 dims][lane]
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, qd = lane >> 4;
+  // The tiles of one head and piece are a multiple of 8 workgroups apart, so on
+  // one XCD, whose L2 has the keys and values for all of them.
+  const int each = (a.pieces * pg.kv_heads + 7) & ~7;
+  const int tile = blockIdx.x / each, at_tile = blockIdx.x - tile * each;
+  if (at_tile >= a.pieces * pg.kv_heads) return;
+  const int kvh = at_tile % pg.kv_heads, piece = at_tile / pg.kv_heads;
+  const int group = a.own.group;
+  const int M = a.own.B * group;
+
+  // this lane's rows: queries, what they see
+  int lo[R], hi[R];
+  bool none[R];  // sees nothing: its row is computed as the others are, and dropped
+  int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, hi_max = 0;
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    const int m = min((tile * R + t) * 16 + r, M - 1), b = m / group;
+    const Seen v = seen_of(a, b, pg.num_pages, pg.ps);
+    lo[t] = v.lo;
+    hi[t] = v.hi;
+    none[t] = v.lo >= v.hi;
+    if (none[t]) {
+      lo[t] = 0;
+      hi[t] = 0x7fffffff;
+    } else {
+      lo_min = min(lo_min, v.lo);
+      lo_max = max(lo_max, v.lo);
+      hi_min = min(hi_min, v.hi);
+      hi_max = max(hi_max, v.hi);
+    }
+    const uint16_t* qp = a.own.q + (int64_t)b * a.own.q_batch_stride + (int64_t)(kvh * group + m % group) * a.own.q_head_stride;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      if ((t * NK + j) % kWaves != wave) continue;
+      const int d = I8 ? (j / 2) * 64 + qd * 16 + (j & 1) * 8 : j * 32 + qd * 8;
+      v4u x = v4u{0, 0, 0, 0};
+      if (EXACT || d < D) x = *reinterpret_cast<const v4u*>(qp + d);
+      sq[(t * NK + j) * 64 + lane] = x;
+    }
+  }
+  __syncthreads();
+  lo_min = __builtin_amdgcn_readfirstlane(wave_min_i(lo_min));
+  lo_max = __builtin_amdgcn_readfirstlane(wave_max_i(lo_max));
+  hi_min = __builtin_amdgcn_readfirstlane(wave_min_i(hi_min));
+  hi_max = __builtin_amdgcn_readfirstlane(wave_max_i(hi_max));
+
+  // the piece's tokens that any row sees
+  const int s0 = max(piece * a.piece_len, min(lo_min, a.prefix_len) & ~(kAlign - 1));
+  const int s1 = min(min((piece + 1) * a.piece_len, a.prefix_len), hi_max);
+  const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+
+  v4f o[R][DT];
+  float m[R], l[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[t][i] = v4f{0, 0, 0, 0};
+    m[t] = -INFINITY;
+    l[t] = 0.0f;
+  }
+
+  if (wave < chunks) {
+    const int n_pages = (a.prefix_len + pg.ps - 1) >> pg.lps;
+    int pbase = s0 >> pg.lps;
+    auto entries = [&](int at) __attribute__((always_inline)) {
+      return at + lane < n_pages ? a.prefix_pages[at + lane] : -1;
+    };
+    int tab = entries(pbase);  // lane's page id: entry pbase + lane
+    // values are requested a chunk ahead where registers hold two
+    constexpr bool kAhead = NK <= 4;
+    v4u kr[NT][NKL], vr[DT], vn[kAhead ? DT : 1];
+    float ksc = 0.0f, vsc = 0.0f;
+    bool vvalid = false;  // of the chunk last addressed: this lane's page exists
+    const uint8_t* vptr = nullptr;
+
+    // pages of chunk c; loads its keys (and scales)
+    auto load_k = [&](int c) __attribute__((always_inline)) {
+      const int t0 = s0 + c * CH;
+      if (((t0 + CH - 1) >> pg.lps) >= pbase + 64) {
+        pbase = t0 >> pg.lps;
+        tab = entries(pbase);
+      }
+      const int kt = t0 + SUB * (r >> 2) + (r & 3);
+      const int vt = t0 + SUB * qd;
+      int pk = __shfl(tab, (kt >> pg.lps) - pbase);
+      int pv = __shfl(tab, (vt >> pg.lps) - pbase);
+      vvalid = (unsigned)pv < (unsigned)pg.num_pages;
+      pk = (unsigned)pk < (unsigned)pg.num_pages ? pk : 0;
+      pv = vvalid ? pv : 0;
+      const int kslot = kt & (pg.ps - 1), vslot = vt & (pg.ps - 1);
+      const uint8_t* kp = pg.k + pk * pg.k_page + ((int64_t)kvh * pg.ps + kslot) * (D * EB) + qd * 16;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NKL; ++j) {
+          const int at = j * 64 + qd * 16;  // byte in the row
+          if (EXACT || at < D * EB)
+            kr[t][j] = *reinterpret_cast<const v4u*>(kp + t * 4 * D * EB + j * 64);
+          else
+            kr[t][j] = v4u{0, 0, 0, 0};
+        }
+      vptr = pg.v + pv * pg.v_page + ((int64_t)kvh * D * pg.ps + vslot) * EB;
+      if constexpr (I8) {
+        ksc = pg.ks[pv * pg.ks_page + kvh * pg.ps + vslot + r];
+        vsc = pg.vs[pv * pg.vs_page + kvh * pg.ps + vslot + r];
+      }
+    };
+    const uint32_t vrow = r * pg.ps * EB;
+    auto load_v = [&](v4u* v) __attribute__((always_inline)) {
+      uint32_t step = 16 * pg.ps * EB;
+      asm volatile("" : "+s"(step));  // (offsets formed anew, not kept in registers)
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        // (tiles past head_dim, which are not stored, read its last one)
+        const uint32_t at = (EXACT ? i : min(i, D / 16 - 1)) * step;
+        v[i] = *reinterpret_cast<const v4u*>(vptr + at + vrow);
+      }
+    };
+
+    const float scale2 = a.own.softcap > 0.0f ? a.own.scale / a.own.softcap : a.own.scale * kLog2e;
+    load_k(wave);
+    load_v(vr);
+    for (int c = wave; c < chunks; c += kWaves) {
+      const int t0 = s0 + c * CH;
+      const bool page_ok = vvalid;
+      // all rows see all of it
+      const bool whole = t0 >= lo_max && t0 + CH <= min(hi_min, s1) && __all(page_ok);
+
+      // scores
+      v4f s[R][NT];
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) s[t][u] = v4f{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < NKL; ++j) {
+        constexpr int kQ = I8 ? 2 : 1;
+        v4u q[R][kQ];
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+#pragma unroll
+          for (int e = 0; e < kQ; ++e) q[t][e] = sq[(t * NK + kQ * j + e) * 64 + lane];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          v4u x[kQ];
+          if constexpr (I8) {
+            x[0] = codes8<QBF>(kr[u][j][0], kr[u][j][1]);
+            x[1] = codes8<QBF>(kr[u][j][2], kr[u][j][3]);
+          } else {
+            x[0] = kr[u][j];
+          }
+#pragma unroll
+          for (int e = 0; e < kQ; ++e)
+#pragma unroll
+            for (int t = 0; t < R; ++t) s[t][u] = mfma32<QBF>(x[e], q[t][e], s[t][u]);
+        }
+      }
+      float ks16 = 0.0f, vs16 = 0.0f;
+      if constexpr (I8) {
+        ks16 = ksc * (1.0f / 127.0f);
+        vs16 = vsc * (1.0f / 127.0f);
+        const int tok = t0 + SUB * qd + r;  // whose scales this lane holds
+        if (!(page_ok && tok < s1)) vs16 = 0.0f;
+      }
+      const bool more = c + kWaves < chunks;
+      if (more) {
+        load_k(c + kWaves);
+        if constexpr (kAhead) load_v(vn);
+      }
+      // Values that not every row sees: what lies behind the prefix may be
+      // anything, and an infinity or NaN may reach only the rows that see it.
+      if constexpr (!I8) {
+        if (!whole) {
+          bool odd = false;
+          v4u keep;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = t0 + SUB * qd + 2 * e;
+            keep[e] = (page_ok && tok < s1 ? 0x0000ffffu : 0u) | (page_ok && tok + 1 < s1 ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+            vr[i] &= keep;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= endless<CT>(vr[i][e]) != 0;
+          }
+          if (__any(odd)) {
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+              // how many such values a row sees, by ones in their places
+              v4u sees;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = t0 + SUB * qd + 2 * e, end = min(hi[t], s1);
+                sees[e] = (page_ok && tok >= lo[t] && tok < end ? kOne<PBF> : 0u) |
+                          (page_ok && tok + 1 >= lo[t] && tok + 1 < end ? kOne<PBF> << 16 : 0u);
+              }
+#pragma unroll
+              for (int i = 0; i < DT; ++i) {
+                v4u there;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) there[e] = endless<CT>(vr[i][e]) & (kOne<PBF> | kOne<PBF> << 16);
+                const v4f n = mfma32<PBF>(there, sees, v4f{0, 0, 0, 0});
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][i][e] = n[e] > 0.0f ? NAN : o[t][i][e];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) vr[i][e] &= ~endless<CT>(vr[i][e]);
+          }
+        }
+      }
+      // probabilities, as the P^T operand in parts
+      constexpr int kV = I8 ? 2 : 1;  // operands of 32 tokens
+      v4u p[R][kV][kParts];
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        if constexpr (I8) scale_tokens<0>(s[t], ks16);
+        auto visible = [&](int u, int i) __attribute__((always_inline)) {
+          const int tok = t0 + SUB * qd + 4 * u + i;
+          return page_ok && tok >= lo[t] && tok < min(hi[t], s1);
+        };
+#pragma unroll
+        for (int u = 0; u < NT; ++u) s[t][u] *= scale2;
+        if (a.own.softcap > 0.0f) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][u][i] = a.own.softcap * kLog2e * tanh_of(s[t][u][i]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][u][i] = visible(u, i) ? s[t][u][i] : -INFINITY;
+        }
+        // running maximum, per row (lane r), equal in the four lanes qd
+        float top = s[t][0][0];
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][u][i]);
+        if (__any(top > m[t] + kS)) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float mn = fmaxf(m[t], top);
+          const float f = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
+          m[t] = mn;
+          l[t] *= f;
+#pragma unroll
+          for (int i = 0; i < DT; ++i) o[t][i] *= f;
+        }
+        const float base = m[t] == -INFINITY ? 0.0f : m[t] - kB;
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[t][u][i] = __builtin_amdgcn_exp2f(s[t][u][i] - base);
+            l[t] += s[t][u][i];
+          }
+        if constexpr (I8) {
+          scale_tokens<0>(s[t], vs16);
+          if (!whole) {
+            // (a scale that is not finite, of a token that this row does not see)
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[t][u][i] = visible(u, i) ? s[t][u][i] : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kV; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x[kParts];
+            const float y = s[t][2 * u + e / 2][2 * (e & 1)], z = s[t][2 * u + e / 2][2 * (e & 1) + 1];
+            if constexpr (PBF)
+              split<true>(y, z, x);
+            else
+              split_f16(y, z, x);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) p[t][u][i][e] = x[i];
+          }
+        // (int8: all tiles later, with one conversion of the values)
+        if constexpr (!I8) {
+#pragma unroll
+          for (int e = 0; e < kParts; ++e)
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[t][i] = mfma32<PBF>(vr[i], p[t][0][e], o[t][i]);
+        }
+      }
+
+      if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int u = 0; u < kV; ++u) {
+            const v4u x = codes8<true>(vr[i][2 * u], vr[i][2 * u + 1]);
+#pragma unroll
+            for (int e = 0; e < kParts; ++e)
+#pragma unroll
+              for (int t = 0; t < R; ++t) o[t][i] = mfma32<true>(x, p[t][u][e], o[t][i]);
+          }
+      }
+      if (more) {
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int i = 0; i < DT; ++i) vr[i] = vn[i];
+        } else {
+          load_v(vr);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      l[t] += __shfl_xor(l[t], 16);
+      l[t] += __shfl_xor(l[t], 32);
+    }
+  }
+
+  // join the waves, a tile of rows at a time
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    if ((tile * R + t) * 16 >= M) break;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) so[((wave * DT + i) * 4 + e) * 64 + lane] = none[t] ? 0.0f : o[t][i][e];
+    if (qd == 0) {
+      sm[wave * 16 + r] = none[t] ? -INFINITY : m[t];
+      sl[wave * 16 + r] = none[t] ? 0.0f : l[t];
+    }
+    __syncthreads();
+    const int64_t at_t = ((int64_t)kvh * a.pieces + piece) * a.rows_padded + (tile * R + t) * 16;
+    for (int at = threadIdx.x; at < 16 * D; at += kThreads) {
+      const int h = at / D, d = at % D;
+      float mx = sm[h];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, sm[w * 16 + h]);
+      float sum = 0.0f, den = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float mw = sm[w * 16 + h];
+        // a wave without a visible token has l = 0 and o = 0
+        const float f = mw == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mw - mx);
+        den += f * sl[w * 16 + h];
+        sum += f * so[((w * DT + (d >> 4)) * 4 + (d & 3)) * 64 + ((d & 15) >> 2) * 16 + h];
+      }
+      a.part_o[(at_t + h) * D + d] = sum;
+      if (d == 0) {
+        a.part_ml[2 * (at_t + h)] = mx - kB;
+        a.part_ml[2 * (at_t + h) + 1] = den;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the prefix's pieces and the own tokens' of one (sequence, query head).
+template <bool QBF>
+__global__ __launch_bounds__(kThreads) void k_shared_join(KvSharedArgs a, int D) {
+  __shared__ float f[2 * kMaxPieces];
+  __shared__ float dens[kWaves], tops[kWaves];
+  __shared__ v4f part[kThreads];
+  const KvAttentionArgs& own = a.own;
+  const int64_t bh = blockIdx.x;
+  const int b = (int)(bh / own.q_heads), hq = (int)(bh % own.q_heads);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // of its own tokens: none, all in one place, or pieces as kv_attention cuts
+  const int2 cut = own.parts > 0 ? own.cuts[b] : int2{0, 1};
+  const int n = a.pieces + cut.y;
+  if (n == 0) {  // nothing anywhere
+    for (int d = threadIdx.x; d < D; d += kThreads) own.out[bh * D + d] = 0;
+    if (threadIdx.x == 0 && own.lse != nullptr) own.lse[bh] = -INFINITY;
+    return;
+  }
+  const int kvh = hq / own.group, in = hq % own.group;
+  const int tiles_h = (own.group + kKvHeadTile - 1) / kKvHeadTile;
+  const int gy = kvh * tiles_h + in / kKvHeadTile, h = in % kKvHeadTile;
+  // where piece i's sum and maximum are
+  auto place = [&](int i, const float*& o, const float*& ml) __attribute__((always_inline)) {
+    int64_t at;
+    if (i < a.pieces) {
+      at = ((int64_t)kvh * a.pieces + i) * a.rows_padded + (int64_t)b * own.group + in;
+      o = a.part_o, ml = a.part_ml;
+    } else if (cut.y == 1) {
+      at = bh;
+      o = own.whole_o, ml = own.whole_ml;
+    } else {
+      i -= a.pieces;
+      at = ((int64_t)gy * own.parts + (cut.x >> 1) + i) * 2 + (i == 0 ? cut.x & 1 : 0);
+      at = at * own.tile_heads + h;
+      o = own.part_o, ml = own.part_ml;
+    }
+    o += at * D;
+    ml += 2 * at;
+  };
+  const int quads = D / 4, groups = kThreads / quads;
+  const int g = threadIdx.x / quads, d = threadIdx.x % quads * 4;
+  constexpr int kU = 4;  // loads in flight
+  v4f v[kU];
+  auto load = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const float *o, *ml;
+      place(min(i + u * groups, n - 1), o, ml);
+      v[u] = *reinterpret_cast<const v4f*>(o + d);
+    }
+  };
+  load(g);
+  float mx = -INFINITY, den = 0.0f;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const float *o, *ml;
+    place(i, o, ml);
+    mx = fmaxf(mx, ml[0]);
+  }
+  mx = wave_max(mx);
+  if (lane == 0) tops[wave] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, tops[w]);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const float *o, *ml;
+    place(i, o, ml);
+    // no visible score: the sums are 0 (or NaN, which stays)
+    f[i] = ml[0] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - mx);
+    den += f[i] * ml[1];
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) den += __shfl_xor(den, o, 64);
+  if (lane == 0) dens[wave] = den;
+  __syncthreads();
+  v4f sum = {0, 0, 0, 0};
+  if (g < groups) {
+    for (int i = g; i < n; i += groups * kU) {
+      if (i != g) load(i);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i + u * groups < n) sum += f[i + u * groups] * v[u];
+    }
+  }
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  if (g == 0) {
+    den = 0.0f;
+    for (int w = 0; w < kWaves; ++w) den += dens[w];
+    for (int w = 1; w < groups && w < n; ++w) sum += part[w * quads + threadIdx.x];
+    const float inv = 1.0f / den;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float y = den == 0.0f ? 0.0f : sum[e] * inv;
+      own.out[bh * D + d + e] = QBF ? __builtin_bit_cast(uint16_t, (__bf16)y) : f2h(y);
+    }
+    if (threadIdx.x == 0 && own.lse != nullptr)
+      own.lse[bh] = den == 0.0f ? -INFINITY : (mx + __builtin_log2f(den)) * kLn2;
+  }
+}
+
+// Tiles of 16 rows that a workgroup of the prefix's kernel takes where there are
+// more than 16 rows: what the registers hold.
+constexpr int full_rows(int nk) { return nk <= 4 ? 4 : 2; }
+
+template <int CT, bool QBF, int NK, bool EXACT>
+hipError_t run(const KvSharedArgs& a, const Pages& pg, hipStream_t s) {
+  const int each = (a.pieces * pg.kv_heads + 7) & ~7, tiles = a.rows_padded / 16;
+  constexpr int R = full_rows(NK);
+  if (tiles == 1)
+    hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, 1>), dim3(each), dim3(kThreads), 0, s, a, pg);
+  else
+    hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, R>), dim3((unsigned)((tiles + R - 1) / R * each)),
+                       dim3(kThreads), 0, s, a, pg);
+  return hipGetLastError();
+}
+
+template <int CT, bool QBF>
+hipError_t pick(const KvSharedArgs& a, const Pages& pg, hipStream_t s) {
+  switch (pg.D) {
+    case 64: return run<CT, QBF, 2, true>(a, pg, s);
+    case 128: return run<CT, QBF, 4, true>(a, pg, s);
+    case 256: return run<CT, QBF, 8, true>(a, pg, s);
+  }
+  return pg.D < 128 ? run<CT, QBF, 4, false>(a, pg, s) : run<CT, QBF, 8, false>(a, pg, s);
+}
+
+}  // namespace
+
+KvSharedPlan kv_shared_plan(int64_t B, int64_t group, int64_t kv_heads, int64_t head_dim,
+                            int64_t prefix_len) {
+  KvSharedPlan p;
+  const int64_t tiles = (B * group + 15) / 16;
+  p.rows_padded = tiles * 16;
+  const int R = tiles == 1 ? 1 : full_rows(head_dim <= 128 ? 4 : 8);
+  // one workgroup for every CU, two of the small ones; a wave has a chunk
+  const int64_t want = (tiles == 1 ? 512 : 256) / (kv_heads * ((tiles + R - 1) / R));
+  const int64_t most = (prefix_len + 255) / 256;
+  int64_t n = want < 1 ? 1 : want;
+  if (n > most) n = most;
+  if (n > kMaxPieces) n = kMaxPieces;
+  p.most_pieces = n;
+  if (n < 1) n = 1;
+  p.piece_len = ((prefix_len + n - 1) / n + kAlign - 1) / kAlign * kAlign;
+  p.pieces = p.piece_len == 0 ? 0 : (prefix_len + p.piece_len - 1) / p.piece_len;
+  return p;
+}
+
+hipError_t launch_kv_shared(const KvSharedArgs& a, bool bf16, const int8mm_kv& kv, hipStream_t s) {
+  const Pages pg = pages_of(kv);
+  hipError_t e = hipSuccess;
+  if (a.pieces > 0) {
+    if (kv.dtype == INT8MM_F16)
+      e = pick<kF16, false>(a, pg, s);
+    else if (kv.dtype == INT8MM_BF16)
+      e = pick<kBF16, true>(a, pg, s);
+    else
+      e = bf16 ? pick<kI8, true>(a, pg, s) : pick<kI8, false>(a, pg, s);
+    if (e != hipSuccess) return e;
+  }
+  e = launch_kv_attention(a.own, bf16, kv, s);
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((int64_t)a.own.B * a.own.q_heads));
+  if (bf16)
+    hipLaunchKernelGGL(k_shared_join<true>, grid, dim3(kThreads), 0, s, a, pg.D);
+  else
+    hipLaunchKernelGGL(k_shared_join<false>, grid, dim3(kThreads), 0, s, a, pg.D);
+  return hipGetLastError();
+}
+
+}  // namespace i8mm

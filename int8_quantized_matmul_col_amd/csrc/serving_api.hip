@@ -90,6 +90,12 @@ AttentionSizes attention_sizes(int64_t B, int64_t groups, int64_t tile_heads, in
   }
   return z;
 }
+struct SharedSizes {
+  i8mm::KvSharedPlan plan;
+  int parts = 0;
+  AttentionSizes own;  // at 0
+  size_t whole_o = 0, whole_ml = 0, part_o = 0, part_ml = 0, total = 0;
+};
 int64_t tile_heads(int64_t q_heads, int64_t kv_heads) {
   const int64_t group = q_heads / kv_heads;
   return group < i8mm::kKvHeadTile ? group : i8mm::kKvHeadTile;
@@ -97,6 +103,24 @@ int64_t tile_heads(int64_t q_heads, int64_t kv_heads) {
 int64_t head_groups(int64_t q_heads, int64_t kv_heads) {
   const int64_t group = q_heads / kv_heads;
   return kv_heads * ((group + i8mm::kKvHeadTile - 1) / i8mm::kKvHeadTile);
+}
+
+// most: tokens that a sequence can show.  Sizes grow with it, so that what is
+// told for a larger one is enough.
+SharedSizes shared_sizes(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t prefix_len,
+                         int64_t most, int64_t window) {
+  SharedSizes z;
+  const int64_t groups = head_groups(q_heads, kv_heads), shared = prefix_len < most ? prefix_len : most;
+  z.plan = i8mm::kv_shared_plan(B, q_heads / kv_heads, kv_heads, D, shared);
+  z.parts = i8mm::kv_attention_parts(B, groups, most - shared, window);
+  z.own = attention_sizes(B, groups, tile_heads(q_heads, kv_heads), D, z.parts);
+  z.whole_o = z.own.total;
+  z.whole_ml = z.whole_o + align_up((size_t)(B * q_heads) * D * 4);
+  z.part_o = z.whole_ml + align_up((size_t)(B * q_heads) * 8);
+  const size_t rows = (size_t)kv_heads * z.plan.most_pieces * z.plan.rows_padded;
+  z.part_ml = z.part_o + align_up(rows * D * 4);
+  z.total = z.part_ml + align_up(rows * 8);
+  return z;
 }
 
 // ------------------------------------------- queries and keys by position
@@ -295,6 +319,87 @@ INT8MM_API int kv_attention(const void* q, int dtype, int64_t B, int64_t q_heads
   a.softcap = softcap;
   a.window = window;
   return status_of(i8mm::launch_kv_attention(a, dtype == INT8MM_BF16, *kv, stream));
+}
+
+INT8MM_API size_t kv_attention_shared_workspace_size(int64_t B, int64_t q_heads, int64_t kv_heads,
+                                                     int64_t head_dim, int64_t prefix_len,
+                                                     int64_t max_len) {
+  if (B < 0 || B > kMaxCount || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 ||
+      q_heads > 65536 || B * q_heads >= ((int64_t)1 << 24) || head_dim < 16 ||
+      head_dim > INT8MM_KV_MAX_HEAD_DIM || prefix_len < 0 || prefix_len > kMaxCount || max_len < 0 ||
+      max_len >= ((int64_t)1 << 31))
+    return 0;
+  if (B == 0) return 0;  // nothing to do
+  return shared_sizes(B, q_heads, kv_heads, head_dim, prefix_len, max_len, 0).total;
+}
+
+INT8MM_API int kv_attention_shared(const void* q, int dtype, int64_t B, int64_t q_heads,
+                                   int64_t q_batch_stride, int64_t q_head_stride,
+                                   const int8mm_kv* kv, const int32_t* table, int64_t table_rows,
+                                   int64_t table_width, const int32_t* lengths,
+                                   const int32_t* rows, const int32_t* prefix_pages,
+                                   int64_t prefix_len, int64_t max_len, float scale,
+                                   int64_t window, float softcap, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int st = check_kv(kv, false);
+  if (st != INT8MM_OK) return st;
+  if (!row_type(dtype, kv)) return INT8MM_EINVAL;
+  if (B < 0 || q_heads < 1 || q_heads > 65536 || q_heads % kv->kv_heads != 0 ||
+      B > kMaxCount || B * q_heads >= ((int64_t)1 << 24) || max_len < 0 || max_len >= ((int64_t)1 << 31) || window < 0 ||
+      prefix_len < 0 || prefix_len > kMaxCount || !table_shape(table_rows, table_width, kv->page_size))
+    return INT8MM_ESHAPE;
+  if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return INT8MM_EINVAL;
+  if (B == 0) return INT8MM_OK;
+  if (q == nullptr || out == nullptr || lengths == nullptr || (prefix_pages == nullptr && prefix_len > 0))
+    return INT8MM_EINVAL;
+  if (table == nullptr && table_rows > 0 && table_width > 0) return INT8MM_EINVAL;
+  if (!aligned(q, 16) || q_batch_stride % 8 != 0 || q_head_stride % 8 != 0 || !aligned(out, 2) ||
+      !aligned(lse, 4) || !aligned(table, 4) || !aligned(lengths, 4) || !aligned(rows, 4) ||
+      !aligned(prefix_pages, 4))
+    return INT8MM_EINVAL;
+  int64_t most = table_width * kv->page_size;
+  if (most > max_len) most = max_len;
+  // units of 128 tokens are counted in 32 bits
+  if (B * (most / 128 + 2) > kMaxCount) return INT8MM_ESHAPE;
+  const int64_t groups = head_groups(q_heads, kv->kv_heads);
+  if (groups > 65535) return INT8MM_ESHAPE;
+  const SharedSizes z = shared_sizes(B, q_heads, kv->kv_heads, kv->head_dim, prefix_len, most, window);
+  if (!workspace_ok(workspace, workspace_bytes, z.total)) return INT8MM_EWORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  i8mm::KvSharedArgs a{};
+  a.own.q = static_cast<const uint16_t*>(q);
+  a.own.q_batch_stride = q_batch_stride;
+  a.own.q_head_stride = q_head_stride;
+  a.own.table = table;
+  a.own.lengths = lengths;
+  a.own.rows = rows;
+  a.own.out = static_cast<uint16_t*>(out);
+  a.own.lse = lse;
+  a.own.part_o = reinterpret_cast<float*>(ws);
+  a.own.part_ml = reinterpret_cast<float*>(ws + z.own.part_ml);
+  a.own.cuts = reinterpret_cast<int2*>(ws + z.own.cuts);
+  a.own.B = (int)B;
+  a.own.q_heads = (int)q_heads;
+  a.own.group = (int)(q_heads / kv->kv_heads);
+  a.own.table_rows = (int)table_rows;
+  a.own.table_width = (int)table_width;
+  a.own.max_len = (int)max_len;
+  a.own.scale = scale;
+  a.own.softcap = softcap;
+  a.own.window = window;
+  a.own.parts = z.parts;
+  a.own.tile_heads = (int)tile_heads(q_heads, kv->kv_heads);
+  a.own.first = (int)(prefix_len < most ? prefix_len : most);
+  a.own.whole_o = reinterpret_cast<float*>(ws + z.whole_o);
+  a.own.whole_ml = reinterpret_cast<float*>(ws + z.whole_ml);
+  a.prefix_pages = prefix_pages;
+  a.part_o = reinterpret_cast<float*>(ws + z.part_o);
+  a.part_ml = reinterpret_cast<float*>(ws + z.part_ml);
+  a.prefix_len = a.own.first;
+  a.pieces = (int)z.plan.pieces;
+  a.piece_len = (int)z.plan.piece_len;
+  a.rows_padded = (int)z.plan.rows_padded;
+  return status_of(i8mm::launch_kv_shared(a, dtype == INT8MM_BF16, *kv, stream));
 }
 
 INT8MM_API size_t kv_pages_workspace_size(int64_t num_pages, int64_t n) {

@@ -73,6 +73,12 @@ struct KvAttentionArgs {
   int64_t window;
   int parts;       // kv_attention_parts
   int tile_heads;  // min(group, kKvHeadTile)
+  // A part of a larger sum: tokens before `first` are not taken, and sequences
+  // that were not cut go to whole_o [B][q_heads][head_dim] and whole_ml
+  // [B][q_heads][2] as the cut ones' parts do, not to out.
+  int first;
+  float* whole_o;
+  float* whole_ml;
 };
 hipError_t launch_kv_attention(const KvAttentionArgs& a, bool bf16, const int8mm_kv& kv,
                                hipStream_t s);
@@ -124,6 +130,23 @@ struct SampleArgs {
 // Chunks of a row of V logits that begins anywhere within 16 bytes.
 inline int sample_chunks(int64_t V) { return V == 0 ? 0 : (int)((V + 7 + kSampleChunk - 1) / kSampleChunk); }
 hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t s);
+
+// A prefix that all sequences share: cut into pieces, its rows (a kv head's
+// queries of all sequences) padded to tiles.
+struct KvSharedPlan {
+  int64_t pieces, piece_len, rows_padded;
+  int64_t most_pieces;  // grows with prefix_len
+};
+KvSharedPlan kv_shared_plan(int64_t B, int64_t group, int64_t kv_heads, int64_t head_dim,
+                            int64_t prefix_len);
+struct KvSharedArgs {
+  KvAttentionArgs own;  // the tokens behind the prefix
+  const int32_t* prefix_pages;
+  float* part_o;   // [kv_heads][pieces][rows_padded][head_dim]
+  float* part_ml;  // [kv_heads][pieces][rows_padded][2]
+  int prefix_len, pieces, piece_len, rows_padded;
+};
+hipError_t launch_kv_shared(const KvSharedArgs& a, bool bf16, const int8mm_kv& kv, hipStream_t s);
 
 size_t kv_pages_workspace(int64_t num_pages, int64_t n);
 hipError_t launch_kv_pages_copy(const int8mm_kv& kv, const int32_t* src, const int32_t* dst, int n,

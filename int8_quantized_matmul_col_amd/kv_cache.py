@@ -74,6 +74,12 @@ class PagedKVCache:
         """kv_attention of one new token per row (see there for the options)."""
         return serving.kv_attention(q, self._layers[layer], self.table, self.lengths, rows, **kw)
 
+    def attend_shared(self, layer: int, q, prefix_row: int, prefix_len: int, rows=None, **kw):
+        """kv_attention_shared: attend for sequences that all begin with the first
+        prefix_len tokens of row prefix_row (of which they were forked)."""
+        return serving.kv_attention_shared(q, self._layers[layer], self.table, self.lengths,
+                                           self.table[prefix_row], prefix_len, rows, **kw)
+
     def fork(self, parents, children):
         """kv_pages_fork: children[i] becomes a copy of the sequence parents[i]."""
         return serving.kv_pages_fork(self.pages, self.table, self.lengths, self.refcount, parents,

@@ -67,6 +67,9 @@ SIGNATURES = {
     "kv_attention_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "kv_attention": (_INT, [_P, _INT, _I64, _I64, _I64, _I64, _KV, _P, _I64, _I64, _P, _P, _I64,
                             _F, _I64, _F, _P, _P, _P, _SZ, _P]),
+    "kv_attention_shared_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "kv_attention_shared": (_INT, [_P, _INT, _I64, _I64, _I64, _I64, _KV, _P, _I64, _I64, _P, _P, _P,
+                                   _I64, _I64, _F, _I64, _F, _P, _P, _P, _SZ, _P]),
     "kv_pages_workspace_size": (_SZ, [_I64, _I64]),
     "kv_pages_copy": (_INT, [_KV, _P, _P, _I64, _P]),
     "kv_pages_reserve": (_INT, [_I32, _I32, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ,
@@ -525,6 +528,70 @@ def kv_attention(q, kv: PagedKV, table, lengths, rows=None, scale: Optional[floa
           None if rows is None else rows.data_ptr(), max_len,
           D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(),
           None if lse is None else lse.data_ptr(),
+          None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.nbytes)
+    return (out, lse) if return_lse else out
+
+
+def kv_attention_shared_workspace_size(B: int, q_heads: int, kv_heads: int, head_dim: int,
+                                       prefix_len: int, max_len: int) -> int:
+    return int(_lib().kv_attention_shared_workspace_size(int(B), int(q_heads), int(kv_heads),
+                                                         int(head_dim), int(prefix_len),
+                                                         int(max_len)))
+
+
+def kv_attention_shared(q, kv: PagedKV, table, lengths, prefix_pages, prefix_len: int, rows=None,
+                        scale: Optional[float] = None, window: int = 0, softcap: float = 0.0,
+                        max_len: Optional[int] = None, return_lse: bool = False, out=None,
+                        workspace=None):
+    """kv_attention of sequences that all begin with the same prefix_len tokens
+    (forks of one prompt), which are read once for the whole batch: token t <
+    prefix_len of every sequence is in page prefix_pages[t // page_size] (int32,
+    the prompt's row of the table or as much of one), later ones as the table
+    says.  A shorter sequence sees its first lengths[row] tokens.  The other
+    arguments and what is returned as kv_attention."""
+    _one_layer(kv)
+    dev = kv.device
+    dt = kv.row_dtype(q.dtype, "q")
+    _on(q, "q", dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != kv.head_dim:
+        raise ValueError(f"q has shape {tuple(shape)}, expected [B][q_heads][{kv.head_dim}]")
+    B, Hq, D = shape
+    if Hq == 0 or Hq % kv.kv_heads:
+        raise ValueError(f"{Hq} query heads do not divide over {kv.kv_heads} kv heads")
+    sb, sh, sd = q.stride()
+    if sd != 1 or sb % 8 or sh % 8 or q.data_ptr() % 16:
+        q = q.clone(memory_format=torch.contiguous_format)
+        sb, sh = Hq * D, D
+    _check_table(table, dev)
+    S, width = table.shape
+    _indexes(lengths, "lengths", dev, (S,))
+    if rows is not None:
+        _indexes(rows, "rows", dev, (B,))
+    elif B > S:
+        raise ValueError(f"{B} queries, and the table has {S} rows")
+    _indexes(prefix_pages, "prefix_pages", dev)
+    prefix_len = int(prefix_len)
+    if prefix_len < 0 or prefix_pages.dim() != 1 or prefix_pages.numel() * kv.page_size < prefix_len:
+        raise ValueError(f"prefix_pages {tuple(prefix_pages.shape)} of {kv.page_size} tokens do not "
+                         f"hold a prefix of {prefix_len}")
+    room = width * kv.page_size
+    max_len = room if max_len is None else min(int(max_len), room)
+    if out is None:
+        out = q.new_empty(shape)
+    else:
+        _check_out(out, (B, Hq, D), q.dtype, "out", dev)
+    lse = q.new_empty((B, Hq), dtype=torch.float32) if return_lse else None
+    if workspace is None:
+        n = _lib().kv_attention_shared_workspace_size(B, Hq, kv.kv_heads, D, prefix_len, max_len)
+        workspace = table.new_empty((n // 4,)) if n else None
+    else:
+        _check_workspace(workspace, dev)
+    _call("kv_attention_shared", kv.index, q.data_ptr(), dt, B, Hq, sb, sh, kv._ref,
+          table.data_ptr(), S, width, lengths.data_ptr(), None if rows is None else rows.data_ptr(),
+          prefix_pages.data_ptr(), prefix_len, max_len, D ** -0.5 if scale is None else scale,
+          window, softcap, out.data_ptr(), None if lse is None else lse.data_ptr(),
           None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.nbytes)
     return (out, lse) if return_lse else out

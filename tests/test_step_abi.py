@@ -163,3 +163,46 @@ def test_reference_sample():
     assert [pick(u, m=0.6) for u in (0.0, 0.6)] == [1, 3]
     assert pick(0.9, t=0.0) == 1 and pick(0.9, p=0.0) == 1 and pick(0.9, t=1e-3) == 1
     assert ref.sample([0.0, math.nan], 0.5, 1.0, 0, 1.0, 0.0)[0] == -1
+
+
+# ------------------------------------------------ attention over a shared prefix
+
+def test_shared_attention_refusals(lib):
+    from test_serving_abi import _kv
+    need = lib.kv_attention_shared_workspace_size(2, 4, 2, 64, 500, 1600)
+    assert need > 2 * 4 * 64 * 4
+
+    def att(q=FAKE, dt=0, B=2, Hq=4, qb=256, qh=64, kv=None, t=FAKE, tr=2, tw=100, n=FAKE, rows=None,
+            pages=FAKE, n0=500, top=1600, scale=0.1, window=0, cap=0.0, out=FAKE, lse=None, ws=FAKE,
+            nb=need):
+        return lib.kv_attention_shared(q, dt, B, Hq, qb, qh, kv or _kv(), t, tr, tw, n, rows, pages, n0,
+                                       top, scale, window, cap, out, lse, ws, nb, None)
+    for n in ("q", "t", "n", "pages", "out"):
+        assert att(**{n: None}) == EINVAL, n
+    for n in ("t", "n", "pages", "rows", "lse"):
+        assert att(**{n: FAKE + 2}) == EINVAL, n
+    assert att(q=FAKE + 8) == EINVAL and att(qb=252) == EINVAL and att(qh=60) == EINVAL
+    assert att(dt=1) == EINVAL and att(dt=2) == EINVAL
+    assert att(kv=_kv(dtype=3)) == EINVAL and att(kv=_kv(page_size=24)) == ESHAPE
+    for kw in (dict(Hq=3), dict(Hq=0), dict(B=-1), dict(B=1 << 22), dict(window=-1), dict(top=-1),
+               dict(n0=-1), dict(n0=(1 << 30) + 1), dict(tw=1 << 27), dict(tr=-1)):
+        assert att(**kw) == ESHAPE, kw
+    for bad in (math.nan, math.inf):
+        assert att(scale=bad) == EINVAL and att(cap=bad) == EINVAL
+    assert att(cap=-1.0) == EINVAL
+    assert att(ws=None) == EWORKSPACE and att(ws=FAKE + 16) == EWORKSPACE
+    assert att(nb=need - 1) == EWORKSPACE and att(B=0) == OK
+    for bad in ((-1, 4, 2, 64, 5, 5), (2, 3, 2, 64, 5, 5), (2, 4, 2, 8, 5, 5), (2, 4, 2, 64, -1, 5),
+                (2, 4, 2, 64, 5, -1), (2, 4, 2, 64, (1 << 30) + 1, 5), (0, 4, 2, 64, 5, 5)):
+        assert lib.kv_attention_shared_workspace_size(*bad) == 0, bad
+
+
+def test_shared_workspace_grows_with_the_bound(lib):
+    """What is told for a bound serves every shorter one."""
+    g = np.random.default_rng(5)
+    size = lib.kv_attention_shared_workspace_size
+    for _ in range(3000):
+        H = int(g.choice([1, 2, 4, 8, 32]))
+        Hq, D = H * int(g.choice([1, 2, 4, 8, 16, 17])), int(g.choice([64, 80, 128, 256]))
+        B, n0, top = int(g.integers(1, 200)), int(2 ** g.uniform(0, 17)), int(2 ** g.uniform(0, 18))
+        assert size(B, Hq, H, D, n0, int(g.integers(0, top + 1))) <= size(B, Hq, H, D, n0, top)
