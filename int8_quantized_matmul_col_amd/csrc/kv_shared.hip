@@ -94,7 +94,7 @@ __device__ __forceinline__ float tanh_of(float x) {
 // CT: the cache's type; QBF: bfloat16 queries; NK: 32-dim steps (EXACT: head_dim
 // is NK * 32, otherwise at most that); R: tiles of 16 rows.
 template <int CT, bool QBF, int NK, bool EXACT, int R>
-__global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_prefix(KvSharedArgs a, Pages pg) {
+__global__ __launch_bounds__(kThreads, NK <= 4 ? 2 : 1) void k_kv_prefix(KvSharedArgs a, Pages pg) {
   constexpr bool I8 = CT == kI8;
   constexpr bool PBF = CT != kF16;                    // type of the P x V operands
   constexpr int kParts = PBF ? (R == 1 ? 3 : 2) : 2;  // that hold a probability
@@ -107,7 +107,10 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
   constexpr float kB = PBF ? 0.0f : kBiasF16, kS = PBF ? kSlack : kSlackF16;
   const int D = EXACT ? NK * 32 : pg.D;
 
-  __shared__ float so[kWaves * DT * 256];  // outputs, [wave][tile][4][lane]
+  // outputs, [wave][tile][4][lane]; the 2 behind each tile keep what a wave reads
+  // together, 16 dims apart, in different banks
+  constexpr int kTile = 258;
+  __shared__ float so[kWaves * DT * kTile];
   __shared__ float sm[kWaves * 16], sl[kWaves * 16];
   __shared__ v4u sq[R * NK * 64];  // Q^T operands, [tile][32 dims][lane]
 
@@ -122,7 +125,65 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
   const int group = a.own.group;
   const int M = a.own.B * group;
 
-  // this lane's rows: queries, what they see
+  int s0 = piece * a.piece_len;
+  const int n_pages = (a.prefix_len + pg.ps - 1) >> pg.lps;
+  int pbase = s0 >> pg.lps;
+  auto entries = [&](int at) __attribute__((always_inline)) {
+    return at + lane < n_pages ? a.prefix_pages[at + lane] : -1;
+  };
+  int tab = entries(pbase);  // lane's page id: entry pbase + lane
+  // values are requested a chunk ahead where registers hold two
+  constexpr bool kAhead = NK == 2 || (R == 1 && NK <= 4);
+  v4u kr[NT][NKL], vr[DT], vn[kAhead ? DT : 1];
+  float ksc = 0.0f, vsc = 0.0f;
+  bool vvalid = false;  // of the chunk last addressed: this lane's page exists
+  const uint8_t* vptr = nullptr;
+
+  // pages of chunk c; loads its keys (and scales)
+  auto load_k = [&](int c) __attribute__((always_inline)) {
+    const int t0 = s0 + c * CH;
+    if (((t0 + CH - 1) >> pg.lps) >= pbase + 64) {
+      pbase = t0 >> pg.lps;
+      tab = entries(pbase);
+    }
+    const int kt = t0 + SUB * (r >> 2) + (r & 3);
+    const int vt = t0 + SUB * qd;
+    int pk = __shfl(tab, (kt >> pg.lps) - pbase);
+    int pv = __shfl(tab, (vt >> pg.lps) - pbase);
+    vvalid = (unsigned)pv < (unsigned)pg.num_pages;
+    pk = (unsigned)pk < (unsigned)pg.num_pages ? pk : 0;
+    pv = vvalid ? pv : 0;
+    const int kslot = kt & (pg.ps - 1), vslot = vt & (pg.ps - 1);
+    const uint8_t* kp = pg.k + pk * pg.k_page + ((int64_t)kvh * pg.ps + kslot) * (D * EB) + qd * 16;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < NKL; ++j) {
+        const int at = j * 64 + qd * 16;  // byte in the row
+        if (EXACT || at < D * EB)
+          kr[t][j] = *reinterpret_cast<const v4u*>(kp + t * 4 * D * EB + j * 64);
+        else
+          kr[t][j] = v4u{0, 0, 0, 0};
+      }
+    vptr = pg.v + pv * pg.v_page + ((int64_t)kvh * D * pg.ps + vslot) * EB;
+    if constexpr (I8) {
+      ksc = pg.ks[pv * pg.ks_page + kvh * pg.ps + vslot + r];
+      vsc = pg.vs[pv * pg.vs_page + kvh * pg.ps + vslot + r];
+    }
+  };
+  const uint32_t vrow = r * pg.ps * EB;
+  auto load_v = [&](v4u* v) __attribute__((always_inline)) {
+    uint32_t step = 16 * pg.ps * EB;
+    asm volatile("" : "+s"(step));  // (offsets formed anew, not kept in registers)
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      // (tiles past head_dim, which are not stored, read its last one)
+      const uint32_t at = (EXACT ? i : min(i, D / 16 - 1)) * step;
+      v[i] = *reinterpret_cast<const v4u*>(vptr + at + vrow);
+    }
+  };
+
+  // what this lane's rows see
   int lo[R], hi[R];
   bool none[R];  // sees nothing: its row is computed as the others are, and dropped
   int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, hi_max = 0;
@@ -142,26 +203,41 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
       hi_min = min(hi_min, v.hi);
       hi_max = max(hi_max, v.hi);
     }
-    const uint16_t* qp = a.own.q + (int64_t)b * a.own.q_batch_stride + (int64_t)(kvh * group + m % group) * a.own.q_head_stride;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) {
-      if ((t * NK + j) % kWaves != wave) continue;
-      const int d = I8 ? (j / 2) * 64 + qd * 16 + (j & 1) * 8 : j * 32 + qd * 8;
-      v4u x = v4u{0, 0, 0, 0};
-      if (EXACT || d < D) x = *reinterpret_cast<const v4u*>(qp + d);
-      sq[(t * NK + j) * 64 + lane] = x;
-    }
   }
-  __syncthreads();
   lo_min = __builtin_amdgcn_readfirstlane(wave_min_i(lo_min));
   lo_max = __builtin_amdgcn_readfirstlane(wave_max_i(lo_max));
   hi_min = __builtin_amdgcn_readfirstlane(wave_min_i(hi_min));
   hi_max = __builtin_amdgcn_readfirstlane(wave_max_i(hi_max));
 
   // the piece's tokens that any row sees
-  const int s0 = max(piece * a.piece_len, min(lo_min, a.prefix_len) & ~(kAlign - 1));
+  s0 = max(s0, min(lo_min, a.prefix_len) & ~(kAlign - 1));
   const int s1 = min(min((piece + 1) * a.piece_len, a.prefix_len), hi_max);
   const int chunks = s1 > s0 ? (s1 - s0 + CH - 1) / CH : 0;
+  if (s0 >> pg.lps >= pbase + 64) {
+    pbase = s0 >> pg.lps;
+    tab = entries(pbase);
+  }
+  if (wave < chunks) {
+    load_k(wave);
+    load_v(vr);
+  }
+
+  // queries, each wave a share of the operands
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    const int m = min((tile * R + t) * 16 + r, M - 1);
+    const uint16_t* qp = a.own.q + (int64_t)(m / group) * a.own.q_batch_stride + (int64_t)(kvh * group + m % group) * a.own.q_head_stride;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      if ((t * NK + j) % kWaves != wave) continue;
+      const int d = I8 ? (j / 2) * 64 + qd * 16 + (j & 1) * 8 : j * 32 + qd * 8;
+      v4u x = v4u{0, 0, 0, 0};
+      if (EXACT || d < D) x = *reinterpret_cast<const v4u*>(qp + d);
+      if (a.own.scale < 0.0f) x ^= 0x80008000u;  // (a factor below 0 turns the maximum round)
+      sq[(t * NK + j) * 64 + lane] = x;
+    }
+  }
+  __syncthreads();
 
   v4f o[R][DT];
   float m[R], l[R];
@@ -174,67 +250,19 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
   }
 
   if (wave < chunks) {
-    const int n_pages = (a.prefix_len + pg.ps - 1) >> pg.lps;
-    int pbase = s0 >> pg.lps;
-    auto entries = [&](int at) __attribute__((always_inline)) {
-      return at + lane < n_pages ? a.prefix_pages[at + lane] : -1;
-    };
-    int tab = entries(pbase);  // lane's page id: entry pbase + lane
-    // values are requested a chunk ahead where registers hold two
-    constexpr bool kAhead = NK <= 4;
-    v4u kr[NT][NKL], vr[DT], vn[kAhead ? DT : 1];
-    float ksc = 0.0f, vsc = 0.0f;
-    bool vvalid = false;  // of the chunk last addressed: this lane's page exists
-    const uint8_t* vptr = nullptr;
-
-    // pages of chunk c; loads its keys (and scales)
-    auto load_k = [&](int c) __attribute__((always_inline)) {
-      const int t0 = s0 + c * CH;
-      if (((t0 + CH - 1) >> pg.lps) >= pbase + 64) {
-        pbase = t0 >> pg.lps;
-        tab = entries(pbase);
-      }
-      const int kt = t0 + SUB * (r >> 2) + (r & 3);
-      const int vt = t0 + SUB * qd;
-      int pk = __shfl(tab, (kt >> pg.lps) - pbase);
-      int pv = __shfl(tab, (vt >> pg.lps) - pbase);
-      vvalid = (unsigned)pv < (unsigned)pg.num_pages;
-      pk = (unsigned)pk < (unsigned)pg.num_pages ? pk : 0;
-      pv = vvalid ? pv : 0;
-      const int kslot = kt & (pg.ps - 1), vslot = vt & (pg.ps - 1);
-      const uint8_t* kp = pg.k + pk * pg.k_page + ((int64_t)kvh * pg.ps + kslot) * (D * EB) + qd * 16;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < NKL; ++j) {
-          const int at = j * 64 + qd * 16;  // byte in the row
-          if (EXACT || at < D * EB)
-            kr[t][j] = *reinterpret_cast<const v4u*>(kp + t * 4 * D * EB + j * 64);
-          else
-            kr[t][j] = v4u{0, 0, 0, 0};
-        }
-      vptr = pg.v + pv * pg.v_page + ((int64_t)kvh * D * pg.ps + vslot) * EB;
-      if constexpr (I8) {
-        ksc = pg.ks[pv * pg.ks_page + kvh * pg.ps + vslot + r];
-        vsc = pg.vs[pv * pg.vs_page + kvh * pg.ps + vslot + r];
-      }
-    };
-    const uint32_t vrow = r * pg.ps * EB;
-    auto load_v = [&](v4u* v) __attribute__((always_inline)) {
-      uint32_t step = 16 * pg.ps * EB;
-      asm volatile("" : "+s"(step));  // (offsets formed anew, not kept in registers)
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        // (tiles past head_dim, which are not stored, read its last one)
-        const uint32_t at = (EXACT ? i : min(i, D / 16 - 1)) * step;
-        v[i] = *reinterpret_cast<const v4u*>(vptr + at + vrow);
-      }
-    };
-
-    const float scale2 = a.own.softcap > 0.0f ? a.own.scale / a.own.softcap : a.own.scale * kLog2e;
-    load_k(wave);
-    load_v(vr);
+    // scores times `scale2` are exponents of 2; it is above 0, so that the largest
+    // score is found before it is applied
+    const float scale1 = fabsf(a.own.scale);
+    const float scale2 = a.own.softcap > 0.0f ? 1.0f : fmaxf(scale1 * kLog2e, 1e-30f);
     for (int c = wave; c < chunks; c += kWaves) {
+      if constexpr (I8) {
+        // (the codes stay codes until here: turned into operands ahead of the loop
+        // they take four times the registers)
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int j = 0; j < NKL; ++j) asm volatile("" : "+v"(kr[u][j]));
+      }
       const int t0 = s0 + c * CH;
       const bool page_ok = vvalid;
       // all rows see all of it
@@ -336,13 +364,12 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
           const int tok = t0 + SUB * qd + 4 * u + i;
           return page_ok && tok >= lo[t] && tok < min(hi[t], s1);
         };
-#pragma unroll
-        for (int u = 0; u < NT; ++u) s[t][u] *= scale2;
         if (a.own.softcap > 0.0f) {
+          const float in = scale1 / a.own.softcap, out = a.own.softcap * kLog2e;
 #pragma unroll
           for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[t][u][i] = a.own.softcap * kLog2e * tanh_of(s[t][u][i]);
+            for (int i = 0; i < 4; ++i) s[t][u][i] = out * tanh_of(in * s[t][u][i]);
         }
         if (!whole) {
 #pragma unroll
@@ -356,6 +383,7 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
         for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][u][i]);
+        top *= scale2;
         if (__any(top > m[t] + kS)) {
           top = fmaxf(top, __shfl_xor(top, 16));
           top = fmaxf(top, __shfl_xor(top, 32));
@@ -371,7 +399,7 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
         for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s[t][u][i] = __builtin_amdgcn_exp2f(s[t][u][i] - base);
+            s[t][u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][u][i], scale2, -base));
             l[t] += s[t][u][i];
           }
         if constexpr (I8) {
@@ -441,28 +469,32 @@ __global__ __launch_bounds__(kThreads, R == 1 && NK <= 4 ? 2 : 1) void k_kv_pref
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) so[((wave * DT + i) * 4 + e) * 64 + lane] = none[t] ? 0.0f : o[t][i][e];
+      for (int e = 0; e < 4; ++e) so[(wave * DT + i) * kTile + e * 64 + lane] = none[t] ? 0.0f : o[t][i][e];
     if (qd == 0) {
       sm[wave * 16 + r] = none[t] ? -INFINITY : m[t];
       sl[wave * 16 + r] = none[t] ? 0.0f : l[t];
     }
     __syncthreads();
     const int64_t at_t = ((int64_t)kvh * a.pieces + piece) * a.rows_padded + (tile * R + t) * 16;
-    for (int at = threadIdx.x; at < 16 * D; at += kThreads) {
-      const int h = at / D, d = at % D;
+    const int quads = D / 4;  // a thread joins 4 dims of a row
+    for (int at = threadIdx.x; at < 16 * quads; at += kThreads) {
+      const int h = at / quads, d = at % quads * 4;
       float mx = sm[h];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, sm[w * 16 + h]);
-      float sum = 0.0f, den = 0.0f;
+      float den = 0.0f;
+      v4f sum = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float mw = sm[w * 16 + h];
         // a wave without a visible token has l = 0 and o = 0
         const float f = mw == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(mw - mx);
         den += f * sl[w * 16 + h];
-        sum += f * so[((w * DT + (d >> 4)) * 4 + (d & 3)) * 64 + ((d & 15) >> 2) * 16 + h];
+        const float* x = so + (w * DT + (d >> 4)) * kTile + ((d & 15) >> 2) * 16 + h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += f * x[e * 64];
       }
-      a.part_o[(at_t + h) * D + d] = sum;
+      *reinterpret_cast<v4f*>(a.part_o + (at_t + h) * D + d) = sum;
       if (d == 0) {
         a.part_ml[2 * (at_t + h)] = mx - kB;
         a.part_ml[2 * (at_t + h) + 1] = den;
@@ -574,7 +606,7 @@ __global__ __launch_bounds__(kThreads) void k_shared_join(KvSharedArgs a, int D)
 
 // Tiles of 16 rows that a workgroup of the prefix's kernel takes where there are
 // more than 16 rows: what the registers hold.
-constexpr int full_rows(int nk) { return nk <= 4 ? 4 : 2; }
+constexpr int full_rows(int nk) { return 2; }
 
 template <int CT, bool QBF, int NK, bool EXACT>
 hipError_t run(const KvSharedArgs& a, const Pages& pg, hipStream_t s) {
@@ -607,7 +639,7 @@ KvSharedPlan kv_shared_plan(int64_t B, int64_t group, int64_t kv_heads, int64_t 
   p.rows_padded = tiles * 16;
   const int R = tiles == 1 ? 1 : full_rows(head_dim <= 128 ? 4 : 8);
   // one workgroup for every CU, two of the small ones; a wave has a chunk
-  const int64_t want = (tiles == 1 ? 512 : 256) / (kv_heads * ((tiles + R - 1) / R));
+  const int64_t want = (head_dim <= 128 ? 512 : 256) / (kv_heads * ((tiles + R - 1) / R));
   const int64_t most = (prefix_len + 255) / 256;
   int64_t n = want < 1 ? 1 : want;
   if (n > most) n = most;
