@@ -219,9 +219,10 @@ __device__ void plan_extend(const Rows& r, const Extend& x, const Snapshot& s, u
       __syncthreads();
       names[threadIdx.x] = j0 + (int)threadIdx.x < r.n ? r.a[j0 + threadIdx.x] : -1;
       __syncthreads();
-      // in this thread's own part only the names before it
-      const int top = j0 < i0 ? kScanThreads : min(kScanThreads, r.n - j0);
+      // in this thread's own part only the names before it, and none for waves
+      // without a row
       const int mine = j0 < i0 ? kScanThreads : (int)threadIdx.x;
+      const int top = i0 + (int)(threadIdx.x & ~63) >= r.n ? 0 : j0 < i0 ? kScanThreads : (int)(threadIdx.x | 63) + 1;
       bool twice = false;
 #pragma unroll 4
       for (int j = 0; j < top; j += 4) {
@@ -494,6 +495,66 @@ __global__ __launch_bounds__(kThreads) void k_pages_extend(Rows r, Extend x, Sna
   }
 }
 
+// Small pools and batches in one launch: one workgroup scans, plans and writes,
+// with the snapshot and the plan in LDS.
+constexpr int kOneBlocks = 4, kOneRequests = kScanThreads, kOneTokens = 16384;
+__global__ __launch_bounds__(kScanThreads) void k_pages_extend_one(Rows r, Extend x, int blocks) {
+  __shared__ uint64_t words[kOneBlocks * 64];
+  __shared__ uint32_t before[kOneBlocks * 64], counts[kOneBlocks], pre[kOneBlocks + 1], sh[64];
+  __shared__ __attribute__((aligned(16))) int32_t names[kScanThreads];
+  __shared__ int32_t plan[kOneRequests], starts[kOneRequests + 1];
+  __shared__ uint32_t first[kOneRequests], need[kOneRequests];
+  Snapshot s;
+  s.words = words, s.before = before, s.counts = counts;
+  s.plan = plan, s.first = first, s.need = need;
+  for (int b = 0; b < blocks; ++b) {
+    scan_pages(r.refcount, r.num_pages, b, s, sh);
+    __syncthreads();
+  }
+  Extend y = x;
+  y.starts = starts;
+  plan_extend(r, y, s, sh, names);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    pre[0] = 0;
+    for (int b = 0; b < blocks; ++b) pre[b + 1] = pre[b] + counts[b];
+  }
+  __syncthreads();
+  auto done = [&](int i) { return plan[i] >= 0 && (need[i] == 0 || sat_add(first[i], need[i]) <= pre[blocks]); };
+  const int i = threadIdx.x;
+  if (i < r.n) {
+    const bool ok = done(i);
+    r.status[i] = plan[i] < 0 ? INT8MM_KV_BAD_ROW : ok ? INT8MM_KV_DONE : INT8MM_KV_NO_PAGES;
+    if (ok) r.lengths[r.a[i]] = plan[i] + r.b[i];
+  }
+  if (i <= r.n) x.starts[i] = starts[i];
+  if (r.n > 0 && i == 0) x.starts[r.n] = starts[r.n];
+  auto last_at = [&](auto at, int hi) {  // the last index in 0 .. hi whose entry at() accepts
+    int lo = 0;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (at(mid)) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  // pages in the order of the requests: each finds whose it is
+  const uint32_t all = r.n > 0 ? min(sat_add(first[r.n - 1], need[r.n - 1]), pre[blocks]) : 0;
+  for (uint32_t k = threadIdx.x; k < all; k += kScanThreads) {
+    const int j = last_at([&](int m) { return first[m] <= k; }, r.n - 1);
+    if (!done(j)) continue;
+    const int page = select_page<true>(s, pre, blocks, k);
+    const int64_t old = ((int64_t)plan[j] + (1 << r.lps) - 1) >> r.lps;
+    r.table[(int64_t)r.a[j] * r.table_width + old + (k - first[j])] = page;
+    r.refcount[page] = 1;
+  }
+  for (int t = threadIdx.x; t < x.total; t += kScanThreads) {
+    const int j = last_at([&](int m) { return starts[m] <= t; }, r.n);
+    const bool there = j < r.n && done(j);
+    x.token_rows[t] = there ? r.a[j] : -1;
+    x.positions[t] = there ? plan[j] + t - starts[j] : -1;
+  }
+}
+
 // Workgroups of pair i: they share the `per` slices of the partly filled page,
 // the first also writes the child's row.
 __global__ __launch_bounds__(kThreads) void k_pages_fork(Rows r, Snapshot s, int blocks, Copier c,
@@ -660,6 +721,10 @@ hipError_t launch_kv_pages_extend(int num_pages, int page_size, int32_t* table, 
   const Rows r{table, lengths, refcount, rows, counts, status,
                table_rows, table_width, n, num_pages, __builtin_ctz(page_size)};
   const Extend x{starts, token_rows, positions, total};
+  if (blocks <= kOneBlocks && n <= kOneRequests && total <= kOneTokens) {
+    hipLaunchKernelGGL(k_pages_extend_one, dim3(1), dim3(kScanThreads), 0, s, r, x, blocks);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_pages_plan_extend, dim3(blocks + 1), dim3(kScanThreads), 0, s, r, x, sn);
   const hipError_t e = hipGetLastError();
   const int grid = n + (total + kTokens - 1) / kTokens;

@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional, Sequence, Tuple, Union
 import torch
 
 from .binding import _require
-from .serving import _call, _indexes, _on, _row_dtype
+from .serving import _DTYPES, _call, _indexes, _on, _row_dtype
 
 INT8MM_ROPE_MAX_DIM = 256
 INT8MM_ROPE_HALF, INT8MM_ROPE_INTERLEAVED = 0, 1
@@ -103,13 +103,18 @@ def rotary(rot_dim: int, theta: float = 10000.0, layout: str = "half",
 def _rows(t, name: str, T: int, D: Optional[int], device):
     """(heads, token distance, head distance) of rows [T][heads][D]."""
     _on(t, name, device)
-    if t.dim() != 3 or t.shape[0] != T or (D is not None and t.shape[2] != D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{T}][heads]"
-                         f"[{'head_dim' if D is None else D}]")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{T}][heads][{D}]")
     st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1 and t.numel() > 0:
+    if sd != 1 and D > 1 and t.numel() > 0:
         raise ValueError(f"the last dim of {name} must be contiguous")
     return t.shape[1], st, sh
+
+
+def _check_weight(w, name: str, dtype, D: int, device) -> None:
+    _require(w, dtype, name, device)
+    if w.shape != (D,):
+        raise ValueError(f"{name} has shape {tuple(w.shape)}, expected [{D}]")
 
 
 def qk_rope(q, k, positions, rotary: Rotary, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -121,46 +126,49 @@ def qk_rope(q, k, positions, rotary: Rotary, q_weight=None, k_weight=None, eps: 
 
     Returns new contiguous (q, k), or writes out = (q, k), which may be the
     inputs themselves."""
-    dt = _row_dtype(q, "q")
+    dtype = q.dtype
+    dt = _DTYPES.get(dtype)
+    index = q.get_device()
     dev = q.device
-    _on(q, "q")
+    if dt is None or index < 0:
+        _row_dtype(q, "q")
+        _on(q, "q")
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [T][heads][head_dim]")
     T, _, D = q.shape
     Hq, qt, qh = _rows(q, "q", T, D, dev)
     Hk = kt = kh = 0
     if k is not None:
-        if k.dtype != q.dtype:
-            raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+        if k.dtype is not dtype:
+            raise TypeError(f"k must be {dtype}, got {k.dtype}")
         Hk, kt, kh = _rows(k, "k", T, D, dev)
     _indexes(positions, "positions", dev, (T,))
-    if not isinstance(rotary, Rotary):
+    if rotary.__class__ is not Rotary:
         raise TypeError("rotary must be a Rotary (see rotary())")
-    _require(rotary.turns, torch.int64, "rotary.turns", dev)
-    if rotary.turns.numel() * 2 != rotary.rot_dim or rotary.rot_dim > D:
-        raise ValueError(f"{rotary.turns.numel()} frequencies of rot_dim {rotary.rot_dim} for "
-                         f"heads of {D} dims")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _require(w, q.dtype, name, dev)
-            if w.shape != (D,):
-                raise ValueError(f"{name} has shape {tuple(w.shape)}, expected [{D}]")
+    turns, rot_dim, layout, factor = rotary
+    if not (turns.dtype is torch.int64 and turns.get_device() == index and turns.is_contiguous()):
+        _require(turns, torch.int64, "rotary.turns", dev)
+    if turns.numel() * 2 != rot_dim or rot_dim > D:
+        raise ValueError(f"{turns.numel()} frequencies of rot_dim {rot_dim} for heads of {D} dims")
+    if q_weight is not None:
+        _check_weight(q_weight, "q_weight", dtype, D, dev)
+    if k_weight is not None:
+        _check_weight(k_weight, "k_weight", dtype, D, dev)
     if out is None:
         yq = q.new_empty((T, Hq, D))
         yk = None if k is None else q.new_empty((T, Hk, D))
         qot, qoh, kot, koh = Hq * D, D, Hk * D, D
     else:
         yq, yk = out
-        if yq.dtype != q.dtype or (yk is None) != (k is None) or \
-                (yk is not None and yk.dtype != q.dtype):
-            raise TypeError(f"out must be tensors of {q.dtype} for q and for k, if there is one")
+        if yq.dtype != dtype or (yk is None) != (k is None) or (yk is not None and yk.dtype != dtype):
+            raise TypeError(f"out must be tensors of {dtype} for q and for k, if there is one")
         n, qot, qoh = _rows(yq, "out[0] (q)", T, D, dev)
         m, kot, koh = (0, 0, 0) if yk is None else _rows(yk, "out[1] (k)", T, D, dev)
         if (n, m) != (Hq, Hk):
             raise ValueError(f"out has {n} and {m} heads, expected {Hq} and {Hk}")
-    _call("qk_rope", dev.index, q.data_ptr(), None if k is None else k.data_ptr(), dt, T, Hq, Hk,
-          D, qt, qh, kt, kh, positions.data_ptr(), rotary.turns.data_ptr(), rotary.rot_dim,
-          rotary.layout, rotary.factor, None if q_weight is None else q_weight.data_ptr(),
+    _call("qk_rope", index, q.data_ptr(), None if k is None else k.data_ptr(), dt, T, Hq, Hk,
+          D, qt, qh, kt, kh, positions.data_ptr(), turns.data_ptr(), rot_dim, layout, factor,
+          None if q_weight is None else q_weight.data_ptr(),
           None if k_weight is None else k_weight.data_ptr(), eps, yq.data_ptr(),
           None if yk is None else yk.data_ptr(), qot, qoh, kot, koh)
     return yq, yk

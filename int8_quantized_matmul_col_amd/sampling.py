@@ -17,7 +17,8 @@ def _each(x, name: str, dtype, B: int, device):
     """(address or None, value): of a tensor with an entry for each row, or of
     one number for all."""
     if isinstance(x, torch.Tensor):
-        _require(x, dtype, name, device)
+        if not (x.dtype is dtype and x.get_device() == device.index and x.is_contiguous()):
+            _require(x, dtype, name, device)
         if x.shape != (B,):
             raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{B}]")
         return x.data_ptr(), 0
@@ -54,9 +55,9 @@ def sample_tokens(logits, u, temperature: Union[float, torch.Tensor] = 1.0,
     sb, sv = logits.stride()
     if sv != 1 and V > 1 and B > 0:
         raise ValueError("the rows of logits must be contiguous")
-    _require(u, torch.float32, "u", dev)
-    if u.shape != (B,):
-        raise ValueError(f"u has shape {tuple(u.shape)}, expected [{B}]")
+    if not isinstance(u, torch.Tensor):
+        raise TypeError("u must be a torch.Tensor")
+    u_ptr, _ = _each(u, "u", torch.float32, B, dev)
     t, t_all = _each(temperature, "temperature", torch.float32, B, dev)
     k, k_all = _each(top_k, "top_k", torch.int32, B, dev)
     p, p_all = _each(top_p, "top_p", torch.float32, B, dev)
@@ -72,7 +73,7 @@ def sample_tokens(logits, u, temperature: Union[float, torch.Tensor] = 1.0,
             workspace = u.new_empty((n // 4,))
     else:
         _check_workspace(workspace, dev)
-    _call("sample_tokens", dev.index, logits.data_ptr(), dt, B, V, sb, u.data_ptr(), t, t_all, k,
+    _call("sample_tokens", dev.index, logits.data_ptr(), dt, B, V, sb, u_ptr, t, t_all, k,
           k_all, p, p_all, m, m_all, out.data_ptr(),
           None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.nbytes)

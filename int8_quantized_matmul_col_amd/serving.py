@@ -642,6 +642,11 @@ def kv_pages_reserve(table, lengths, refcount, rows, new_lengths, page_size: int
     return status
 
 
+@functools.lru_cache(maxsize=1024)
+def _extend_workspace(num_pages: int, n: int) -> int:
+    return int(_lib().kv_pages_workspace_size(num_pages, n))
+
+
 class BatchPlan(NamedTuple):
     """What kv_pages_extend returns, int32 on the GPU: status [n] of each
     request, starts [n + 1] of their tokens, and each token's table row and
@@ -671,14 +676,24 @@ def kv_pages_extend(table, lengths, refcount, rows, counts, total: int, page_siz
     n, P, total = rows.numel(), refcount.numel(), int(total)
     if total < 0:
         raise ValueError("total must not be negative")
-    maps = rows.new_empty((2 * n + 1 + 2 * total,))
-    ws = _pages_workspace(P, n, dev, workspace)
+    # the maps, and a workspace before them (on 256 bytes: a new tensor is)
+    if workspace is None:
+        size = _extend_workspace(P, n)
+        if size == 0:
+            raise Int8mmError("kv_pages_workspace_size", INT8MM_ESHAPE)
+        lead = size // 4
+    else:
+        _check_workspace(workspace, dev)
+        size, lead = workspace.nbytes, 0
+    maps = rows.new_empty((lead + 2 * n + 1 + 2 * total,))
     at = maps.data_ptr()
+    ws = at if workspace is None else workspace.data_ptr()
+    at += 4 * lead
     _call("kv_pages_extend", dev.index, P, page_size, table.data_ptr(), table.shape[0],
           table.shape[1], lengths.data_ptr(), refcount.data_ptr(), rows.data_ptr(),
           counts.data_ptr(), n, total, at, at + 4 * n, at + 4 * (2 * n + 1),
-          at + 4 * (2 * n + 1 + total), ws.data_ptr(), ws.nbytes)
-    return BatchPlan(*maps.split((n, n + 1, total, total)))
+          at + 4 * (2 * n + 1 + total), ws, size)
+    return BatchPlan(*maps.split((lead, n, n + 1, total, total))[1:])
 
 
 def kv_pages_fork(kv: PagedKV, table, lengths, refcount, parents, children, workspace=None):

@@ -43,7 +43,8 @@ def both(lib, table, lengths, count, rows, counts, total, ps):
 @pytest.mark.parametrize("S,P,ps,width,n,pad", [
     (1, 8, 16, 8, 1, 0), (5, 40, 16, 6, 3, 7), (64, 900, 16, 20, 64, 0), (64, 5000, 32, 9, 40, 1),
     (300, 13000, 16, 40, 256, 100), (2500, 20000, 16, 12, 1500, 0), (2500, 20000, 16, 12, 2500, 3),
-    (40, 30, 64, 8, 33, 5),
+    (40, 30, 64, 8, 33, 5), (1024, 16384, 16, 20, 1024, 9), (1100, 16384, 16, 20, 1025, 0),
+    (900, 16385, 16, 20, 300, 0), (400, 16000, 64, 20, 300, 0),
 ])
 def test_extend(lib, S, P, ps, width, n, pad):
     g = sc.rng(1, S, P, n)
@@ -54,11 +55,17 @@ def test_extend(lib, S, P, ps, width, n, pad):
     both(lib, table, lengths, count, rows, [1] * n, n, ps)  # a decode step
 
 
-def test_refused_requests(lib):
+# pages in use behind the others: a pool of more than 16384 takes two launches
+POOLS = [0, 20000]
+
+
+@pytest.mark.parametrize("used", POOLS)
+def test_refused_requests(lib, used):
     """Rows out of range, named twice, too long, negative counts, a count at
     int32's end, and what follows them."""
     g = sc.rng(2)
     table, lengths, count = state(g, 12, 60, 16, 4, 30)
+    count = np.r_[count, np.ones(used, np.int32)]
     lengths[7] = -3  # a row that something else broke
     big = 2 ** 31 - 1
     rows = [3, -1, 12, 3, 4, 5, 6, 7, 4, 8, big, -big - 1, 9, 0]
@@ -74,12 +81,14 @@ def test_refused_requests(lib):
     both(lib, table, lengths, count, [], [], 70, 16)
 
 
+@pytest.mark.parametrize("used", POOLS)
 @pytest.mark.parametrize("free", [0, 1, 3, 6])
-def test_pages_run_out(lib, free):
+def test_pages_run_out(lib, free, used):
     """Those that fit in order are done, the others unchanged, their tokens -1."""
     table = np.full((6, 5), -1, np.int32)
     count = np.ones(20, np.int32)
     count[np.arange(free) * 3] = 0
+    count = np.r_[count, np.ones(used, np.int32)]
     lengths = np.array([0, 0, 0, 0, 0, 0], np.int32)
     table[5, 0], lengths[5] = 1, 3
     plan, _ = both(lib, table, lengths, count, [0, 1, 5, 2, 3], [20, 33, 13, 16, 0], 82, 16)
