@@ -76,6 +76,9 @@ __device__ __forceinline__ double bin_scale(int below) {
 template <int T>
 struct Piece {
   uint4 w[T == kF32 ? 2 : 1];
+  __device__ __forceinline__ uint32_t dword(int d) const {
+    return d == 0 ? w[0].x : d == 1 ? w[0].y : d == 2 ? w[0].z : w[0].w;
+  }
   __device__ __forceinline__ float value(int e) const {
     const uint4& q = w[T == kF32 ? e / 4 : 0];
     const int d = T == kF32 ? e % 4 : e / 2;
@@ -382,16 +385,6 @@ __device__ __forceinline__ int block_find(bool yes, int* part) {
   if (waves == 0) return -1;
   return __shfl(mine, FIRST ? __builtin_ctzll(waves) : 63 - __builtin_clzll(waves), 64);
 }
-// Places behind *n for the lanes that are here, one atomic for all of them.
-__device__ __forceinline__ int append(int* n) {
-  const uint64_t here = __ballot(true);
-  const int lane = threadIdx.x & 63, leader = __builtin_ctzll(here);
-  int first = 0;
-  if (lane == leader) first = atomicAdd(n, __popcll(here));
-  first = __builtin_amdgcn_readlane(first, leader);
-  return first + __popcll(here & (((uint64_t)1 << lane) - 1));
-}
-
 struct Pick {
   double scale[kPitch];   // e^(-bin / 7)
   double mass[kPitch];    // before a bin, in bin order (largest z first)
@@ -404,19 +397,32 @@ struct Pick {
   uint64_t extra[kSampleMaxChunks];  // of the bin that is kept in part
   double chunk[kSampleMaxChunks];    // kept mass of a chunk
   int off[kSampleMaxChunks], last[kSampleMaxChunks];
-  int has[kSampleMaxChunks];         // chunks with tokens of a bin
   uint32_t ties[kSampleMaxChunks];   // tokens of a chunk with one logit
   unsigned long long part_u[kPickWaves];
   double part_d[kPickWaves];
   uint32_t part_n[kPickWaves];
   int part_i[kPickWaves];
   float tops[kPickWaves];
-  int found, n, n_has;
+  int found, n;
   uint64_t answer[4];
 };
 
 __device__ __forceinline__ void add_lds(uint64_t* p, uint64_t x) {
   atomicAdd(reinterpret_cast<unsigned long long*>(p), (unsigned long long)x);
+}
+
+// The bits of a number in the logits' 16-bit type: float16 the nearest, bfloat16
+// the next to 0; order is kept.
+template <int T>
+__device__ __forceinline__ uint32_t raw_of(float x) {
+  return T == kBF16 ? __float_as_uint(x) >> 16 : f2h(x);
+}
+// 1 in each half of a dword that lies in first .. first + n, without a carry.
+__device__ __forceinline__ uint32_t within(uint32_t w, uint32_t first, uint32_t n) {
+  typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+  const unsigned short f = (unsigned short)first, m = (unsigned short)(n + 1);
+  const v2u t = __builtin_bit_cast(v2u, w) - v2u{f, f};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_elementwise_sub_sat(v2u{m, m}, t), v2u{1, 1}));
 }
 
 // A logit by its place.
@@ -564,6 +570,13 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
       const double lo = lower / r.per7, hi = (lower + 1.0) / r.per7;
       float flo = (float)(lo - (fabs(lo) * 1e-6 + 1e-40)), fhi = (float)(hi + (fabs(hi) * 1e-6 + 1e-40));
       if (!(r.per7 > 0.0)) flo = -INFINITY, fhi = INFINITY;  // an infinite temperature
+      // logits of 16 bits whose bin has one sign: their bits from raw0 on, raw_n more
+      const bool packed = T != kF32 && (flo > 0.0f || fhi < 0.0f);
+      uint32_t raw0 = 0, raw_n = 0;
+      if (packed) {
+        raw0 = raw_of<T>(flo > 0.0f ? flo : fhi);
+        raw_n = raw_of<T>(flo > 0.0f ? fhi : flo) - raw0;
+      }
       uint32_t k0 = key_of(fhi), k1 = key_of(flo), left = s.own[at], rank0 = 0;
       uint64_t mass0 = 0;
 
@@ -580,7 +593,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
         int shift = 32 - __builtin_clz(k1 - k0 | 1) - kDigitBits;
         if (shift < 0) shift = 0;
         __syncthreads();
-        if (tid == 0) s.n = 0, s.n_has = 0;
+        if (tid == 0) s.n = 0;
         if (step == kSplit)
 #pragma unroll
           for (int i = 0; i < kCopies / 2; ++i) s.digit_mass[i][tid] = 0, s.digit_count[i][tid] = 0;
@@ -611,39 +624,61 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
             take((uint32_t)(x >> 32), (uint32_t)x, ((int)(uint32_t)x + r.mis) / kSampleChunk);
           }
         } else {
-          if (tid < a.S && (word(tid, at) >> kCountShift) != 0) s.has[append(&s.n_has)] = tid;  // (any order)
-          __syncthreads();
-          // pieces of 8 logits, two of a chunk for each thread
-          constexpr int kU = T == kF32 ? 4 : 8;  // in flight
-          const int pieces = s.n_has * 2;
+          // pieces of 8 logits, as many requested together as registers hold: a CU
+          // reads a row at 30 GB/s with 8 a thread
+          constexpr int kU = T == kF32 ? 8 : 24, kG = kU / 8;
+          const int pieces = a.S * 2;  // two of a chunk for each thread
+          auto first_of = [&](int p) __attribute__((always_inline)) { return (p * kPickThreads + tid) * 8; };
 #pragma unroll 1
-          for (int i = 0; i < pieces; i += kU) {
+          for (int i0 = 0; i0 < pieces; i0 += kU) {
             Piece<T> x[kU];
-            int v0[kU];
 #pragma unroll
-            for (int k = 0; k < kU; ++k) {
-              const int j = min(i + k, pieces - 1);
-              v0[k] = s.has[j >> 1] * kSampleChunk + ((j & 1) * kPickThreads + tid) * 8;
-              x[k] = load_piece<T>(r.base, v0[k], r.mis, r.end);
-            }
-            uint64_t hits = 0;
+            for (int g = 0; g < kG; ++g)
+              if (g == 0 || i0 + g * 8 < pieces) {
 #pragma unroll
-            for (int k = 0; k < kU; ++k) {
-              patch_piece<T>(x[k], r.base, v0[k], r.mis, r.end);
-              uint32_t h = 0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float y = x[k].value(e);
-                h |= (y >= flo && y <= fhi ? 1u : 0u) << e;
+                for (int k = g * 8; k < g * 8 + 8; ++k)
+                  x[k] = load_piece<T>(r.base, first_of(i0 + k), r.mis, r.end);
               }
-              if (i + k < pieces) hits |= (uint64_t)h << 8 * k;
+            // bit 8 k + e: logit e of piece k; packed: e / 2, and 4 bits a piece, in
+            // 16 bits of even logits and 16 of odd ones, 4 pieces each
+            uint64_t hits[kG];
+            int mine = 0;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              hits[g] = 0;
+              if (g > 0 && i0 + g * 8 >= pieces) continue;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const Piece<T>& y = x[g * 8 + k];
+                uint32_t h = 0;
+                const bool whole = whole_piece(first_of(i0 + g * 8 + k), r.mis, r.end);
+                if (T != kF32 && packed) {
+#pragma unroll
+                  for (int d = 0; d < 4; ++d) h |= within(y.dword(d), raw0, raw_n) << d;
+                  hits[g] |= (uint64_t)(whole ? h : 0) << (k / 4 * 32 + k % 4 * 4);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) h |= (y.value(e) >= flo && y.value(e) <= fhi ? 1u : 0u) << e;
+                  hits[g] |= (uint64_t)(whole ? h : 0) << 8 * k;
+                }
+              }
+              mine += __popcll(hits[g]);
             }
+            // the pieces that the row begins and ends in, one logit a thread
+            int edge = -1;
+            if (i0 == 0 && tid < 16) {
+              const int tail = r.end & ~7, v = tid < 8 ? tid : tail + tid - 8;
+              const bool cut = tid < 8 ? !whole_piece(0, r.mis, r.end) : tail > 0 && tail < r.end;
+              if (cut && v >= r.mis && v < r.end) {
+                const float y = load1<T>(r.base, v);
+                if (y >= flo && y <= fhi) edge = v, ++mine;
+              }
+            }
+            // places in the list for all of a wave's at once; a token goes there
+            // first as its own place, and is looked up afterwards, so that no load
+            // is waited for here
+            int j = mine;
             if (step == kFill) {
-              // places in the list for all of a wave's at once; a token goes there
-              // as its piece, thread and bit, and is looked up afterwards, so that
-              // no load is waited for here
-              const int mine = __popcll(hits);
-              int j = mine;
 #pragma unroll
               for (int o = 1; o < 64; o <<= 1) {
                 const int y = __shfl_up(j, o, 64);
@@ -652,21 +687,28 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
               int first = 0;
               if ((tid & 63) == 63 && j > 0) first = atomicAdd(&s.n, j);
               j += __builtin_amdgcn_readlane(first, 63) - mine;
+            }
+            auto found = [&](int v) __attribute__((always_inline)) {
+              if (step != kFill)
+                take(key_of(load1<T>(r.base, v)), (uint32_t)(v - r.mis), v / kSampleChunk);
+              else if (j < kList)
+                s.list[j] = (uint32_t)v;
+              ++j;
+            };
 #pragma unroll 1
-              for (; hits != 0; hits &= hits - 1, ++j) {
-                const int k = __builtin_ctzll(hits);
-                if (j < kList) s.list[j] = (uint64_t)((i + (k >> 3)) * (8 * kPickThreads) + tid * 8 + (k & 7));
+            for (int g = 0; g < kG; ++g) {
+              // (by selects: an index would put hits into memory)
+              uint64_t h = hits[0];
+#pragma unroll
+              for (int e = 1; e < kG; ++e) h = g == e ? hits[e] : h;
+#pragma unroll 1
+              for (; h != 0; h &= h - 1) {
+                int k = __builtin_ctzll(h);
+                if (T != kF32 && packed) k = ((k >> 5) * 4 + (k >> 2 & 3)) * 8 + (k & 3) * 2 + (k >> 4 & 1);
+                found(first_of(i0 + g * 8 + (k >> 3)) + (k & 7));
               }
             }
-#pragma unroll 1
-            while (hits != 0) {
-              const int k = __builtin_ctzll(hits);
-              hits &= hits - 1;
-              const int p = i + (k >> 3), c = s.has[p >> 1];
-              const int v = c * kSampleChunk + ((p & 1) * kPickThreads + tid) * 8 + (k & 7);
-              // (what lies beside the row is no logit)
-              if (v >= r.mis && v < r.end) take(key_of(load1<T>(r.base, v)), (uint32_t)(v - r.mis), c);
-            }
+            if (edge >= 0) found(edge);
           }
         }
         if (step == kSum) break;
@@ -677,11 +719,8 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
           if (listed == at) {
 #pragma unroll 4
             for (int i = tid; i < n_list; i += kPickThreads) {
-              const int p = (int)s.list[i] / (8 * kPickThreads), in = (int)s.list[i] % (8 * kPickThreads);
-              const int v = s.has[p >> 1] * kSampleChunk + (p & 1) * (8 * kPickThreads) + in;
-              const bool there = v >= r.mis && v < r.end;
-              const uint32_t key = key_of(load1<T>(r.base, there ? v : r.mis));
-              s.list[i] = there ? (uint64_t)key << 32 | (uint32_t)(v - r.mis) : ~(uint64_t)0;
+              const int v = (int)s.list[i];
+              s.list[i] = comp(load1<T>(r.base, v), v);
             }
           }
           if (phase == 2 && listed == at) break;
