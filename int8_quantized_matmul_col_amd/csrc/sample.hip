@@ -147,27 +147,31 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int b) {
   return r;
 }
 
-// z in sevenths, and the weight of what it exceeds its bin's lower end by.
+// z in sevenths; exp of where it lies in its bin, and that as a whole number.
 __device__ __forceinline__ double sevenths(float x, double per7) {
 #pragma clang fp contract(off)
   return (double)x * per7;
 }
-__device__ __forceinline__ uint64_t weight(double z7, double bin) {
+__device__ __forceinline__ double exp_in_bin(double z7, double bin) {
 #pragma clang fp contract(off)
-  const double x = (z7 - bin - 0.5) * (1.0 / 7.0);  // +- 1/14
-  // the series of exp; what follows is below 2^-45
-  double p = 1.0 / 5040;
-  p = __builtin_fma(p, x, 1.0 / 720);
-  p = __builtin_fma(p, x, 1.0 / 120);
-  p = __builtin_fma(p, x, 1.0 / 24);
-  p = __builtin_fma(p, x, 1.0 / 6);
-  p = __builtin_fma(p, x, 0.5);
-  p = __builtin_fma(p, x, 1.0);
-  p = __builtin_fma(p, x, 1.0);
-  // rounded to a whole number by the addition; its bits are the mantissa's
-  const double y = __builtin_fma(p, 0x1p36, 0x1p52);
-  return (uint64_t)__double_as_longlong(y) & (((uint64_t)1 << 52) - 1);
+  const double x = z7 - bin - 0.5;
+  // the series of exp(x / 7) (1 / (7^k k!)); what follows is below 2^-39
+  double p = 1.0 / 84707280.0;
+  p = __builtin_fma(p, x, 1.0 / 2016840.0);
+  p = __builtin_fma(p, x, 1.0 / 57624.0);
+  p = __builtin_fma(p, x, 1.0 / 2058.0);
+  p = __builtin_fma(p, x, 1.0 / 98.0);
+  p = __builtin_fma(p, x, 1.0 / 7.0);
+  return __builtin_fma(p, x, 1.0);
 }
+__device__ __forceinline__ double rounded(double z7, double bin) {  // + 2^52
+  return __builtin_fma(exp_in_bin(z7, bin), 0x1p36, 0x1p52);
+}
+__device__ __forceinline__ uint64_t weight(double z7, double bin) {
+  // the addition rounds to a whole number; its bits are the mantissa's
+  return (uint64_t)__double_as_longlong(rounded(z7, bin)) & (((uint64_t)1 << 52) - 1);
+}
+__device__ __forceinline__ double weight_d(double z7, double bin) { return rounded(z7, bin) - 0x1p52; }
 
 // Whether a row's filters cut anywhere that bins are needed for.
 struct Filters {
@@ -270,7 +274,7 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(SampleArgs a) {
         const double z7 = sevenths(x[i][e], r.per7);
         const double bin = floor(z7);
         const double below = upper - bin;
-        if (below <= (double)kLastBin) sum += (double)weight(z7, bin) * s.scale[(int)below];
+        if (below <= (double)kLastBin) sum = __builtin_fma(weight_d(z7, bin), s.scale[(int)below], sum);
       }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
@@ -882,7 +886,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
       const double below = upper - f;
       return top7 - z7 < (double)kLastBin && below <= (double)bin &&
                      (below < (double)bin || (comp(x, v) <= cut && z7 >= least))
-                 ? (double)weight(z7, f) * s.scale[(int)below]
+                 ? weight_d(z7, f) * s.scale[(int)below]
                  : 0.0;
     };
     double w[16], mine = 0.0;
