@@ -157,6 +157,16 @@ def test_long(lib, cache, dtype):
     check(lib, c, queries(g, 5, 4, 64, sc.DTYPES[dtype]), max_len=n0 + 700)
 
 
+def test_many_rows(lib):
+    """Thousands of queries on one kv head: many tiles, one piece."""
+    g = sc.rng(13)
+    n0, B = 50, 2000
+    lengths = [n0 + (b % 3) for b in range(B)]
+    lengths[77] = 12
+    c = Shared(lib, g, n0, lengths, 1, 16, 16, "f16")
+    check(lib, c, queries(g, B, 20, 16, torch.float16))
+
+
 def test_no_prefix_and_nothing_else(lib):
     g = sc.rng(5)
     c = Shared(lib, g, 0, [30, 0, 300], 2, 64, 16, "f16")

@@ -106,6 +106,21 @@ def test_many_close_logits(lib):
         check(lib, x, g.random(2).astype(np.float32), **f)
 
 
+def test_many_logits_beside_a_bin(lib):
+    """Bins begin at whole sevenths: next to the few tokens of the one that is cut
+    lie many more than are listed, too close to tell apart in 32 bits' bounds."""
+    g = sc.rng(9)
+    x = np.full((2, 9000), np.nextafter(np.float32(3), np.float32(0)), np.float32)
+    x[:, 100:110] = 3 + 0.01 * np.arange(10)
+    x[:, 200:205] = 5.0
+    for f in (dict(top_k=9), dict(top_k=15), dict(top_p=0.04), dict(top_k=700, top_p=0.5)):
+        check(lib, sc.dev(x), g.random(2).astype(np.float32), exact_ties=True, **f)
+    x = np.full((1, 9000), -3.0, np.float32)  # and from above, below zero
+    x[:, 100:110] = np.nextafter(np.float32(-3), np.float32(-4))
+    for k in (8995, 3000, 8990, 8991):
+        check(lib, sc.dev(x), [0.7], top_k=k, exact_ties=True)
+
+
 def test_no_distribution(lib):
     """-1 where there is none, and only there; masked tokens are not drawn."""
     g = sc.rng(5)
