@@ -33,7 +33,7 @@ PROBE_SOURCES = ["ceilings.hip"]
 SOURCES = ["api.hip", "prepare.hip", "activation.hip", "gemm_prefill.hip", "gemm_decode.hip",
            "serving_api.hip", "int4_linear.hip", "kv_attention.hip", "kv_shared.hip", "kv_rows.hip",
            "kv_pages.hip", "qk_rope.hip", "sample.hip"]
-HEADERS = ["device_common.h", "launch.h", "serving_launch.h", "kv_device.h"]
+HEADERS = ["device_common.h", "launch.h", "serving_launch.h", "kv_device.h", "kv_attention.h"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

@@ -11,31 +11,33 @@
 // an int8 cache) in turn.  As in kv_attention a score tile's rows are tokens,
 // permuted so that the probabilities that a lane forms are the operand of the
 // second product as they are; here one load of keys and values serves R tiles
-// of 16 rows, whose queries and outputs stay in registers (64 rows at 128 dims:
-// 64 + 128 registers, one wave a SIMD).  R = 1 is for batches of up to 16 rows,
-// two waves a SIMD.  Pieces are as long as leave one workgroup for every CU (two
-// at R = 1): each costs a partial output to write and to join.
+// of 16 rows, whose outputs stay in registers and whose queries in LDS: 32 rows,
+// and 16 for batches that have no more, two waves a SIMD.  Pieces are as long as
+// leave two workgroups for every CU: each costs a partial output to write and to
+// join.
 //
-// What bounds it: at 64 rows a tile's softmax, about 130 vector instructions for
-// 24 matrix instructions of 16 cycles; at 16 rows HBM.
+// What bounds it: at 32 rows the softmax's vector instructions and the matrix
+// instructions, of which two waves a SIMD overlap a part (64 sequences on 8000
+// tokens, 8 kv heads of 128 dims, 4 query heads each, bf16: 31.4 us, 400 TFLOP/s; 33
+// on 30001 int8 tokens 59.5 us); at 16 rows HBM and the launch.  64 rows, with
+// one wave a SIMD, take 37.9 us of the former; values requested a chunk ahead
+// at 32 rows do not fit the registers (40.5); two waves that share a chunk
+// through LDS wait for each other (42).
 //
 // Precision as kv_attention's, but for probabilities: two bfloat16 numbers (three
 // at R = 1), which hold 16 bits, or two of float16 in one sum, which hold 22 of
 // those of at least 2^-14 of the maximum and end at 2^-38 of it.
-#include "kv_device.h"
+#include "kv_attention.h"
 
 namespace i8mm {
 
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kAlign = 64;       // of a piece's first token, a multiple of both chunk sizes
 constexpr int kMaxPieces = 512;  // of the prefix, and of a sequence's own tokens
 
 // float16: probabilities are held times 2^13, at most 2^15.
 constexpr float kSlackF16 = 2.0f, kBiasF16 = 13.0f;
-constexpr float kSlack = 8.0f;
 
 // As split() of float16, the remainder unscaled: it is at least 2^-12 of the
 // number (positive down to 2^-26 of the maximum).
@@ -92,9 +94,18 @@ __device__ __forceinline__ float tanh_of(float x) {
 }
 
 // CT: the cache's type; QBF: bfloat16 queries; NK: 32-dim steps (EXACT: head_dim
-// is NK * 32, otherwise at most that); R: tiles of 16 rows.
-template <int CT, bool QBF, int NK, bool EXACT, int R>
-__global__ __launch_bounds__(kThreads, NK <= 4 ? 2 : 1) void k_kv_prefix(KvSharedArgs a, Pages pg) {
+// is NK * 32, otherwise at most that); R: tiles of 16 rows; OWN: behind
+// the prefix's workgroups are kv_attention's, own_x for each head group.
+template <int CT, bool QBF, int NK, bool EXACT, int R, bool OWN>
+__global__ __launch_bounds__(kThreads, NK <= 4 ? 2 : 1) void k_kv_prefix(KvSharedArgs a, Pages pg, int own_x) {
+  const int each = (a.pieces * pg.kv_heads + 7) & ~7;
+  if constexpr (OWN) {
+    const int at = (int)blockIdx.x - each;
+    if (at >= 0) {
+      attend_own<CT, QBF, NK, EXACT>(a.own, pg, at % own_x, at / own_x);
+      return;
+    }
+  }
   constexpr bool I8 = CT == kI8;
   constexpr bool PBF = CT != kF16;                    // type of the P x V operands
   constexpr int kParts = PBF ? (R == 1 ? 3 : 2) : 2;  // that hold a probability
@@ -118,7 +129,6 @@ __global__ __launch_bounds__(kThreads, NK <= 4 ? 2 : 1) void k_kv_prefix(KvShare
   const int r = lane & 15, qd = lane >> 4;
   // The tiles of one head and piece are a multiple of 8 workgroups apart, so on
   // one XCD, whose L2 has the keys and values for all of them.
-  const int each = (a.pieces * pg.kv_heads + 7) & ~7;
   const int tile = blockIdx.x / each, at_tile = blockIdx.x - tile * each;
   if (at_tile >= a.pieces * pg.kv_heads) return;
   const int kvh = at_tile % pg.kv_heads, piece = at_tile / pg.kv_heads;
@@ -436,7 +446,8 @@ __global__ __launch_bounds__(kThreads, NK <= 4 ? 2 : 1) void k_kv_prefix(KvShare
 
       if constexpr (I8) {
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+        for (int i = 0; i < DT; ++i) {
+          asm volatile("" : "+v"(vr[i]));  // (as the keys)
 #pragma unroll
           for (int u = 0; u < kV; ++u) {
             const v4u x = codes8<true>(vr[i][2 * u], vr[i][2 * u + 1]);
@@ -445,6 +456,7 @@ __global__ __launch_bounds__(kThreads, NK <= 4 ? 2 : 1) void k_kv_prefix(KvShare
 #pragma unroll
               for (int t = 0; t < R; ++t) o[t][i] = mfma32<true>(x, p[t][u][e], o[t][i]);
           }
+        }
       }
       if (more) {
         if constexpr (kAhead) {
@@ -605,29 +617,47 @@ __global__ __launch_bounds__(kThreads) void k_shared_join(KvSharedArgs a, int D)
 }
 
 // Tiles of 16 rows that a workgroup of the prefix's kernel takes where there are
-// more than 16 rows: what the registers hold.
-constexpr int full_rows(int nk) { return 2; }
+// more than 16 rows: what the registers hold of two waves a SIMD.
+constexpr int kRows = 2;
 
+// Batches of one tile are launched together with their own tokens, whose
+// workgroups wait for memory and those of the prefix too: 4 sequences on 1000
+// float16 tokens of 8 x 128 dims take 11.9 us on the GPU so, 10.8 and 8.7 one
+// after the other.  Larger tiles keep the matrix cores busy and gain nothing (59.8
+// and 31.4 + 28.4 us, 64 sequences on 8000); int8's of both do not fit the registers.
 template <int CT, bool QBF, int NK, bool EXACT>
-hipError_t run(const KvSharedArgs& a, const Pages& pg, hipStream_t s) {
+hipError_t run(const KvSharedArgs& a, bool bf16, const int8mm_kv& kv, const Pages& pg, hipStream_t s) {
   const int each = (a.pieces * pg.kv_heads + 7) & ~7, tiles = a.rows_padded / 16;
-  constexpr int R = full_rows(NK);
-  if (tiles == 1)
-    hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, 1>), dim3(each), dim3(kThreads), 0, s, a, pg);
-  else
-    hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, R>), dim3((unsigned)((tiles + R - 1) / R * each)),
-                       dim3(kThreads), 0, s, a, pg);
-  return hipGetLastError();
+  constexpr bool kTogether = CT != kI8 && NK <= 4;
+  if (kTogether && tiles == 1 && a.pieces > 0) {
+    const int own_x = a.own.parts > 0 ? a.own.parts : a.own.B;
+    const int own_y = pg.kv_heads * ((a.own.group + kKvHeadTile - 1) / kKvHeadTile);
+    hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, 1, kTogether>), dim3((unsigned)(each + own_x * own_y)),
+                       dim3(kThreads), 0, s, a, pg, own_x);
+    return hipGetLastError();
+  }
+  if (a.pieces > 0) {
+    if (tiles == 1)
+      hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, 1, kTogether>), dim3(each), dim3(kThreads), 0, s, a,
+                         pg, 1);
+    else
+      hipLaunchKernelGGL((k_kv_prefix<CT, QBF, NK, EXACT, kRows, false>),
+                         dim3((unsigned)((tiles + kRows - 1) / kRows * each)), dim3(kThreads), 0, s, a, pg, 1);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return launch_kv_attention(a.own, bf16, kv, s);
 }
 
 template <int CT, bool QBF>
-hipError_t pick(const KvSharedArgs& a, const Pages& pg, hipStream_t s) {
+hipError_t pick(const KvSharedArgs& a, bool bf16, const int8mm_kv& kv, hipStream_t s) {
+  const Pages pg = pages_of(kv);
   switch (pg.D) {
-    case 64: return run<CT, QBF, 2, true>(a, pg, s);
-    case 128: return run<CT, QBF, 4, true>(a, pg, s);
-    case 256: return run<CT, QBF, 8, true>(a, pg, s);
+    case 64: return run<CT, QBF, 2, true>(a, bf16, kv, pg, s);
+    case 128: return run<CT, QBF, 4, true>(a, bf16, kv, pg, s);
+    case 256: return run<CT, QBF, 8, true>(a, bf16, kv, pg, s);
   }
-  return pg.D < 128 ? run<CT, QBF, 4, false>(a, pg, s) : run<CT, QBF, 8, false>(a, pg, s);
+  return pg.D < 128 ? run<CT, QBF, 4, false>(a, bf16, kv, pg, s) : run<CT, QBF, 8, false>(a, bf16, kv, pg, s);
 }
 
 }  // namespace
@@ -637,7 +667,7 @@ KvSharedPlan kv_shared_plan(int64_t B, int64_t group, int64_t kv_heads, int64_t 
   KvSharedPlan p;
   const int64_t tiles = (B * group + 15) / 16;
   p.rows_padded = tiles * 16;
-  const int R = tiles == 1 ? 1 : full_rows(head_dim <= 128 ? 4 : 8);
+  const int R = tiles == 1 ? 1 : kRows;
   // one workgroup for every CU, two of the small ones; a wave has a chunk
   const int64_t want = (head_dim <= 128 ? 512 : 256) / (kv_heads * ((tiles + R - 1) / R));
   const int64_t most = (prefix_len + 255) / 256;
@@ -652,24 +682,19 @@ KvSharedPlan kv_shared_plan(int64_t B, int64_t group, int64_t kv_heads, int64_t 
 }
 
 hipError_t launch_kv_shared(const KvSharedArgs& a, bool bf16, const int8mm_kv& kv, hipStream_t s) {
-  const Pages pg = pages_of(kv);
-  hipError_t e = hipSuccess;
-  if (a.pieces > 0) {
-    if (kv.dtype == INT8MM_F16)
-      e = pick<kF16, false>(a, pg, s);
-    else if (kv.dtype == INT8MM_BF16)
-      e = pick<kBF16, true>(a, pg, s);
-    else
-      e = bf16 ? pick<kI8, true>(a, pg, s) : pick<kI8, false>(a, pg, s);
-    if (e != hipSuccess) return e;
-  }
-  e = launch_kv_attention(a.own, bf16, kv, s);
+  hipError_t e;
+  if (kv.dtype == INT8MM_F16)
+    e = pick<kF16, false>(a, bf16, kv, s);
+  else if (kv.dtype == INT8MM_BF16)
+    e = pick<kBF16, true>(a, bf16, kv, s);
+  else
+    e = bf16 ? pick<kI8, true>(a, bf16, kv, s) : pick<kI8, false>(a, bf16, kv, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((int64_t)a.own.B * a.own.q_heads));
   if (bf16)
-    hipLaunchKernelGGL(k_shared_join<true>, grid, dim3(kThreads), 0, s, a, pg.D);
+    hipLaunchKernelGGL(k_shared_join<true>, grid, dim3(kThreads), 0, s, a, kv.head_dim);
   else
-    hipLaunchKernelGGL(k_shared_join<false>, grid, dim3(kThreads), 0, s, a, pg.D);
+    hipLaunchKernelGGL(k_shared_join<false>, grid, dim3(kThreads), 0, s, a, kv.head_dim);
   return hipGetLastError();
 }
 
