@@ -3,8 +3,8 @@
 // device, so that a serving loop neither waits for the GPU nor copies them.
 //
 // Bound by HBM where pages move (each read and written once), else by the
-// launches (copy and free are one kernel, the others two) and, in reserve and
-// fork, by the plan: one workgroup compares every row named with every other
+// launches (copy and free are one kernel, the others two; extend of a small pool
+// and batch one) and, in reserve and fork, by the plan: one workgroup compares every row named with every other
 // (32 pairs 6.7 us, 64 rows 13, of 16 us for the whole reserve call).  The first
 // of the two kernels snapshots which pages are free: one bit a page, a running
 // count per 64-page word and a count per 4096-page block.  From these any thread
@@ -496,8 +496,12 @@ __global__ __launch_bounds__(kThreads) void k_pages_extend(Rows r, Extend x, Sna
 }
 
 // Small pools and batches in one launch: one workgroup scans, plans and writes,
-// with the snapshot and the plan in LDS.
-constexpr int kOneBlocks = 4, kOneRequests = kScanThreads, kOneTokens = 16384;
+// with the snapshot and the plan in LDS.  It saves the host a launch (4 us: a call
+// of two batches of 8 requests and a free 28 us, 39 with two launches each).  On the
+// GPU it takes 8.4 us with 4096 pages (two kernels 8.0), 10.6 with 8192 (8.6), 14.4
+// with 16384 (8.7), and up to 2 us more for 4096 tokens, 13 for 16384 (0.2): so up
+// to 8192 pages and 4096 tokens.
+constexpr int kOneBlocks = 2, kOneRequests = kScanThreads, kOneTokens = 4096;
 __global__ __launch_bounds__(kScanThreads) void k_pages_extend_one(Rows r, Extend x, int blocks) {
   __shared__ uint64_t words[kOneBlocks * 64];
   __shared__ uint32_t before[kOneBlocks * 64], counts[kOneBlocks], pre[kOneBlocks + 1], sh[64];
