@@ -5,7 +5,10 @@
  *   - products of a few rows with 4-bit weights and group scales (int4_*);
  *   - a paged key-value cache in float16, bfloat16 or int8: writing and
  *     reading rows (kv_append, kv_gather), one new token's attention over it
- *     (kv_attention), and the upkeep of its pages (kv_pages_*).
+ *     (kv_attention), also where a batch shares a prompt (kv_attention_shared),
+ *     the upkeep of its pages and a batch's token maps (kv_pages_*);
+ *   - queries and keys turned by their positions, with their norms (qk_rope);
+ *   - the next tokens, drawn from logits (sample_tokens).
  *
  * The conventions of int8mm.h hold for every entry point here: device
  * pointers owned by the caller, nothing allocated, no host synchronisation,
@@ -236,9 +239,10 @@ INT8MM_API size_t kv_attention_shared_workspace_size(int64_t B, int64_t q_heads,
  * first lengths[row] tokens.  All else as kv_attention, but that
  *   - an infinity or NaN makes what depends on it infinite or NaN, which of the
  *     two is unspecified;
- *   - probabilities enter the matrix cores with 16 bits (float16: 22 bits of
- *     those of at least 2^-14 of the maximum, ending at 2^-38 of it) where the
- *     query heads of a kv head, of all sequences, are more than 16;
+ *   - the prefix's probabilities enter the matrix cores with 22 bits of those of
+ *     at least 2^-14 of the maximum, ending at 2^-38 of it, in a float16 cache;
+ *     in others with 16 bits where the query heads of a kv head, of all
+ *     sequences, are more than 16;
  *   - how sums are rounded may depend on the sizes of the batch and on all
  *     sequences' lengths; the same call gives the same bits again.
  * prefix_len 0 .. 2^30.  Errors: EINVAL, ESHAPE, EWORKSPACE, EHIP.

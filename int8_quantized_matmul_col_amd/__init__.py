@@ -20,9 +20,12 @@ for it.  ``outlier_stats`` summarizes the column maxima of an activation
 Beside the matmul stand the other operators of a decode step (``serving``,
 ``include/int8mm_serving.h``): ``int4_linear`` (few rows times 4-bit weights
 with group scales; ``Int4Linear`` is its module), and a paged key-value cache
-(``PagedKVCache``) with ``kv_append``, ``kv_gather``, ``kv_attention`` and the
-upkeep of its pages, ``kv_pages_reserve``, ``_copy``, ``_fork``, ``_free`` and
-``_compact``.
+(``PagedKVCache``) with ``kv_append``, ``kv_gather``, ``kv_attention``,
+``kv_attention_shared`` (a batch that shares a prompt) and the upkeep of its
+pages, ``kv_pages_reserve``, ``_extend`` (with the token maps of a batch),
+``_copy``, ``_fork``, ``_free`` and ``_compact``; ``qk_rope`` turns queries and
+keys by their positions, with their norms (``rotary`` prepares the frequencies),
+and ``sample_tokens`` draws the next tokens.
 """
 
 from .binding import (  # noqa: F401

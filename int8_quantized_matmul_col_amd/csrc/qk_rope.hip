@@ -19,6 +19,11 @@
 // lanes of one head are a power of two that reduce within themselves; without,
 // the runs of all heads follow one another and no lane is idle.  Halves, heads or
 // addresses of odd lengths take a plain kernel, a wave a head.
+//
+// Bound by HBM, each element read and written once: 8192 tokens of 40 heads of
+// 128 dims with norms take 38 us, 4.4 TB/s (a large copy: 5.16); 1999 tokens of
+// 64 heads of 80 dims, of which 20 are turned, 11.7 us, 3.5 TB/s; and by the launch
+// where tokens are few (1 token of 18 heads 3.3 us, 64 of 40 heads 4.2).
 #include "device_common.h"
 #include "serving_launch.h"
 

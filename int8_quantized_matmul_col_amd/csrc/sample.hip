@@ -19,6 +19,13 @@
 // each filter cuts, reads the row again (from L2) for that bin's tokens, and
 // narrows their range to the one logit at which it cuts; then the chunk that the
 // given number falls into, and reads that.  Nothing is sorted.
+//
+// Measured: 256 rows of 50021 fp32 logits without a filter 19.3 us, 2.7 TB/s (the
+// weights' 64-bit instructions bound it), and 9.0 in the second kernel; 64 rows
+// of 128000 bfloat16 logits with top-k and top-p 12.4 us and 49.4; one row of 32000
+// 5.4 and 22.  What filters need is a chain of readings by one workgroup a row: of
+// the bin's counts, of the row (6 us of 128000 logits), and of its list, with a
+// dozen barriers each.
 #include "device_common.h"
 #include "serving_launch.h"
 
@@ -92,9 +99,8 @@ struct Piece {
   }
 };
 // Pieces are requested without a condition, so that the loads of several do not
-// wait for one another (a row of 128000 logits: 10 us a reading with one, 4
-// so): one that is not wholly in the row reads a table instead, and then
-// (patch_piece) what there is of it.
+// wait for one another: one that is not wholly in the row reads a table instead,
+// and then (patch_piece) what there is of it.
 __device__ __forceinline__ bool whole_piece(int v0, int mis, int end) { return v0 >= mis && v0 + 8 <= end; }
 template <int T>
 __device__ __forceinline__ Piece<T> load_piece(const void* base, int v0, int mis, int end) {
@@ -628,8 +634,8 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
             take((uint32_t)(x >> 32), (uint32_t)x, ((int)(uint32_t)x + r.mis) / kSampleChunk);
           }
         } else {
-          // pieces of 8 logits, as many requested together as registers hold: a CU
-          // reads a row at 30 GB/s with 8 a thread
+          // pieces of 8 logits, as many requested together as registers hold (128000
+          // bfloat16 logits: 8.5 us with 8 a thread, 6 with 24)
           constexpr int kU = T == kF32 ? 8 : 24, kG = kU / 8;
           const int pieces = a.S * 2;  // two of a chunk for each thread
           auto first_of = [&](int p) __attribute__((always_inline)) { return (p * kPickThreads + tid) * 8; };
@@ -762,7 +768,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(SampleArgs a) {
           k0 = (k0 | ends) <= min(k1, 0x7fffffffu) ? k0 | ends : (k0 + ends) & ~ends;
           k1 = k0;
         }
-          // How many of its tokens are kept:
+        // How many of its tokens are kept:
         const uint64_t w = weight(sevenths(of_key(k0), r.per7), lower);
         uint32_t least_n = 1, most_n = left;
         while (least_n < most_n) {

@@ -8,8 +8,10 @@ kernels and there is no fallback.
 * ``int4_prepare_weight`` / ``int4_pack_weight`` / ``int4_linear``: products
   of a few rows with 4-bit weights and group scales.
 * ``PagedKV``: the pages of a key-value cache; ``kv_append``, ``kv_gather``,
-  ``kv_attention`` work on one layer of it, ``kv_pages_*`` on its pages.
-  ``kv_cache.PagedKVCache`` keeps the tables beside them.
+  ``kv_attention``, ``kv_attention_shared`` work on one layer of it,
+  ``kv_pages_*`` on its pages.  ``kv_cache.PagedKVCache`` keeps the tables
+  beside them.
+* ``rope.qk_rope`` and ``sampling.sample_tokens`` are in files of their own.
 """
 
 from __future__ import annotations
