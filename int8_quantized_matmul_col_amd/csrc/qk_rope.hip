@@ -21,7 +21,7 @@
 // addresses of odd lengths take a plain kernel, a wave a head.
 //
 // Bound by HBM, each element read and written once: 8192 tokens of 40 heads of
-// 128 dims with norms take 38 us, 4.4 TB/s (a large copy: 5.16); 1999 tokens of
+// 128 dims with norms take 36.8 us, 4.6 TB/s (a large copy: 5.16); 1999 tokens of
 // 64 heads of 80 dims, of which 20 are turned, 11.7 us, 3.5 TB/s; and by the launch
 // where tokens are few (1 token of 18 heads 3.3 us, 64 of 40 heads 4.2).
 #include "device_common.h"
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void k_qk_rope(QkRopeArgs a, RopeShape g)
     }
   }
 
-  constexpr int kU = 2;  // places in flight
+  constexpr int kU = 2;  // places in flight (4: 46 us instead of 38 for 8192 tokens)
   Place p[kU];
   Run<VEC> ra[kU], rb[kU];
   auto next = [&](int u) __attribute__((always_inline)) {
@@ -375,10 +375,12 @@ hipError_t run(const QkRopeArgs& a, hipStream_t s) {
   g.lanes = 1;
   while (g.lanes < g.units) g.lanes *= 2;
   const int64_t work = (int64_t)H * (NORM ? g.lanes : g.units);  // lanes that a token takes
-  // Enough tokens a workgroup for four of its steps, as long as 1024 workgroups
-  // remain (four on every CU); a token of more than 16 steps is dealt to several.
+  // Enough tokens a workgroup for eight of its steps, as long as 1024 workgroups
+  // remain, four on every CU (8192 tokens: 1 a workgroup takes 47 us, 2 40, 4 38, 8
+  // 36.8; 1999 tokens of four times as many lanes: 1 12.4, 2 14.2); a token of more
+  // than 16 steps is dealt to several.
   int tokens = 1;
-  while (tokens < kMaxTokens && tokens * work < 4 * kThreads && a.T / (2 * tokens) >= 1024) tokens *= 2;
+  while (tokens < kMaxTokens && tokens * work < 8 * kThreads && a.T / (2 * tokens) >= 1024) tokens *= 2;
   g.tokens = tokens;
   int parts = 1;
   if (tokens == 1) parts = (int)((work + 16 * kThreads - 1) / (16 * kThreads));
