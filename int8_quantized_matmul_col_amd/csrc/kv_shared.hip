@@ -16,13 +16,14 @@
 // leave two workgroups for every CU: each costs a partial output to write and to
 // join.
 //
-// What bounds it: at 32 rows the softmax's vector instructions and the matrix
-// instructions, of which two waves a SIMD overlap a part (64 sequences on 8000
-// tokens, 8 kv heads of 128 dims, 4 query heads each, bf16: 31.4 us, 400 TFLOP/s; 33
-// on 30001 int8 tokens 59.5 us); at 16 rows HBM and the launch.  64 rows, with
-// one wave a SIMD, take 37.9 us of the former; values requested a chunk ahead
-// at 32 rows do not fit the registers (40.5); two waves that share a chunk
-// through LDS wait for each other (42).
+// What bounds it: 64 sequences on 8000 bfloat16 tokens, 8 kv heads of 128 dims, 4
+// query heads each: 31.4 us, 400 TFLOP/s, in which the waves wait for memory 46%
+// of their time, vector instructions take 47% of the issue slots and matrix
+// instructions 20%.  33 on 30001 int8 tokens of 4 kv heads: 60 us, vector
+// instructions 80%: of 850 for a chunk and 32 rows 384 turn codes into bfloat16.
+// At 16 rows HBM and the launch.  64 rows, with one wave a SIMD, take 37.9 us of the
+// former; values requested a chunk ahead at 32 rows do not fit the registers
+// (40.5); two waves that share a chunk through LDS wait for each other (42, 68).
 //
 // Precision as kv_attention's, but for probabilities: two bfloat16 numbers (three
 // at R = 1), which hold 16 bits, or two of float16 in one sum, which hold 22 of
