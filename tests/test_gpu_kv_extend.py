@@ -55,7 +55,7 @@ def test_extend(lib, S, P, ps, width, n, pad):
     both(lib, table, lengths, count, rows, [1] * n, n, ps)  # a decode step
 
 
-# pages in use behind the others: a pool of more than 16384 takes two launches
+# pages in use behind the others: a pool of more than 8192 takes two launches
 POOLS = [0, 20000]
 
 
@@ -95,6 +95,19 @@ def test_pages_run_out(lib, free, used):
     assert plan.status.tolist()[2] == plan.status.tolist()[4] == 0  # need no page
     empty = np.zeros(0, np.int32)
     both(lib, table, np.zeros(6, np.int32), empty, [0, 1], [1, 0], 1, 16)
+
+
+@pytest.mark.parametrize("P", [4096, 4097, 8192, 8193])
+@pytest.mark.parametrize("total", [4096, 4097])
+@pytest.mark.parametrize("n", [1, 1024, 1025])
+def test_one_launch_or_two(lib, P, total, n):
+    """Both sides of what one launch takes, the free pages at the pool's end."""
+    count = np.ones(P, np.int32)
+    count[P - 700:] = 0
+    table, lengths = np.full((n, 300), -1, np.int32), np.zeros(n, np.int32)
+    counts = [total // n] * n
+    counts[-1] += total - sum(counts)
+    both(lib, table, lengths, count, list(range(n)), counts, total, 16)
 
 
 def test_many_pages(lib):
