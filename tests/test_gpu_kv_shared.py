@@ -134,6 +134,22 @@ def test_short_and_empty_rows(lib, B, Hq, H, D, cache, dtype):
     check(lib, c, q)
 
 
+@pytest.mark.parametrize("cache,dtype", [("f16", "f16"), ("bf16", "bf16"), ("i8", "bf16")])
+@pytest.mark.parametrize("B,Hq,H,D,window", [
+    (3, 8, 8, 128, 0), (5, 6, 2, 64, 0), (4, 4, 2, 96, 700), (1, 20, 1, 128, 0), (17, 2, 2, 128, 0),
+    (2, 32, 4, 80, 300), (3, 2, 2, 256, 0),
+])
+def test_long_own_tokens(lib, B, Hq, H, D, window, cache, dtype):
+    """Own tokens dealt out over workgroups beside a prefix of one tile and of two."""
+    g = sc.rng(14, B, Hq, D)
+    n0 = 150
+    lengths = [n0 + int(x) for x in g.integers(300, 1500, B)]
+    if B > 2:
+        lengths[1], lengths[2] = 40, 0
+    c = Shared(lib, g, n0, lengths, H, D, 16, cache)
+    check(lib, c, queries(g, B, Hq, D, sc.DTYPES[dtype]), window=window)
+
+
 @pytest.mark.parametrize("window", [1, 20, 64, 150, 1000])
 @pytest.mark.parametrize("cache,dtype", [("f16", "f16"), ("bf16", "bf16"), ("i8", "f16")])
 def test_window_and_softcap(lib, cache, dtype, window):
